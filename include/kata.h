@@ -401,9 +401,74 @@ KATA_API kata_status_t kata_fwd_delta(const void *q, const void *k, const void *
                                       size_t workspace_bytes, kata_stream_t stream);
 
 /*
+ * Gated delta rule (the delta rule on the raw keys, with a decay of the state
+ * and without a normaliser; the KATA explainer's section 4 compares delta-rule
+ * layers): per value head, with a log decay g_t <= 0 and a write strength
+ * beta_t,
+ *   S_t = e^(g_t) S_(t-1) + k_t d_t^T,  d_t = beta_t (v_t - e^(g_t) S_(t-1)^T k_t),
+ *   o_t = S_t^T q_t
+ * (the token's own write is read). Computed in chunks of 64 tokens, an exact
+ * form (a triangular solve per chunk).
+ *   q, k               device [B, H_k, T, d_k], dtype. Value head h reads query
+ *                      / key head h / (H / H_k): H must be a multiple of H_k.
+ *   v, o               device [B, H, T, d_v], dtype.
+ *   g, beta            device fp32 [B, H, T]. A g below -100 (-inf included: the
+ *                      state is dropped before the token) counts as -100, whose
+ *                      decay is 0 in fp32. A token with beta = 0 and g = 0 leaves
+ *                      the state as it is (padding). Values outside g <= 0,
+ *                      0 <= beta |k|^2 <= 2 give the rule's arithmetic, which may
+ *                      then grow without bound.
+ *   S0, S_out          optional device fp32 [B, H, d_k, d_v]: the state before the
+ *                      first and after the last token (NULL: zero, not wanted).
+ *                      They may not overlap.
+ *   workspace          device, >= kata_fwd_gated_delta_workspace_bytes(...),
+ *                      256-byte aligned, contents on entry ignored, not shared by
+ *                      calls that run concurrently; kata_workspace_status applies.
+ * d_k, d_v in {16, 32, 64, 128}; any T. T = 0 copies S0 to S_out.
+ */
+KATA_API size_t kata_fwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_k, int d_v,
+                                                     kata_dtype_t dtype);
+KATA_API kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v,
+                                            const float *g, const float *beta, void *o, int B,
+                                            int H_k, int H, int T, int d_k, int d_v,
+                                            kata_dtype_t dtype, const float *S0, float *S_out,
+                                            void *workspace, size_t workspace_bytes,
+                                            kata_stream_t stream);
+
+/*
+ * Gradient of kata_fwd_gated_delta: given dout = dL/do and, optionally, dS =
+ * dL/dS_out (NULL: zero), writes dq, dk, dv (dtype, shapes of q, k, v; dq and
+ * dk of a shared head are summed over its value heads in fp32, in head order,
+ * then rounded once), dg and dbeta (fp32 [B, H, T]) and, unless NULL, dS0 (fp32
+ * [B, H, d_k, d_v]). The forward's output is not an input: the states at the
+ * chunks' borders are rebuilt into the workspace. Outputs may not overlap
+ * inputs. Results are bitwise reproducible. T = 0 copies dS to dS0.
+ */
+KATA_API size_t kata_bwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_k, int d_v,
+                                                     kata_dtype_t dtype);
+KATA_API kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v,
+                                            const float *g, const float *beta, const void *dout,
+                                            const float *S0, const float *dS, void *dq, void *dk,
+                                            void *dv, float *dg, float *dbeta, float *dS0, int B,
+                                            int H_k, int H, int T, int d_k, int d_v,
+                                            kata_dtype_t dtype, void *workspace,
+                                            size_t workspace_bytes, kata_stream_t stream);
+
+/*
+ * One token of the gated delta rule, batched over B x H heads, the state
+ * updated in place: q, k [B, H_k, d_k], v, y [B, H, d_v] (dtype), g, beta fp32
+ * [B, H], S fp32 [B, H, d_k, d_v], 16-byte aligned. No workspace.
+ */
+KATA_API kata_status_t kata_gated_delta_step(const void *q, const void *k, const void *v,
+                                             const float *g, const float *beta, float *S, void *y,
+                                             int B, int H_k, int H, int d_k, int d_v,
+                                             kata_dtype_t dtype, kata_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads the status word a kata_fwd_chunked(...),
  * kata_fwd_chunked_sequential(...), kata_fwd_chunked_from_state(...),
- * kata_chunked_state(...), kata_bwd_chunked(...), kata_fwd_delta(...) or
+ * kata_chunked_state(...), kata_bwd_chunked(...), kata_fwd_delta(...),
+ * kata_fwd_gated_delta(...), kata_bwd_gated_delta(...) or
  * kata_selftest_device_timeout(...) call left in `workspace`: KATA_OK, or
  * KATA_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel gave up (the
  * kernel returned early, its outputs are undefined, the context is usable),

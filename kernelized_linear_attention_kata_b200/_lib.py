@@ -70,6 +70,14 @@ SIGNATURES = {
                                         _i, _i, _i, _i, _vp, _sz, _vp]),
     "kata_fwd_delta": (ctypes.c_int, [_cvp, _cvp, _cvp, _fp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                       _fp, _fp, _vp, _sz, _vp]),
+    "kata_fwd_gated_delta_workspace_bytes": (ctypes.c_size_t, [_i] * 7),
+    "kata_fwd_gated_delta": (ctypes.c_int, [_cvp, _cvp, _cvp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _i,
+                                            _i, _fp, _fp, _vp, _sz, _vp]),
+    "kata_bwd_gated_delta_workspace_bytes": (ctypes.c_size_t, [_i] * 7),
+    "kata_bwd_gated_delta": (ctypes.c_int, [_cvp, _cvp, _cvp, _fp, _fp, _cvp, _fp, _fp, _vp, _vp, _vp,
+                                            _fp, _fp, _fp, _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "kata_gated_delta_step": (ctypes.c_int, [_cvp, _cvp, _cvp, _fp, _fp, _fp, _vp, _i, _i, _i, _i, _i,
+                                             _i, _vp]),
     "kata_workspace_status": (ctypes.c_int, [_cvp, _vp]),
     "kata_selftest_device_timeout": (ctypes.c_int, [_vp, _sz, _vp]),
     "kata_profile_enable": (ctypes.c_int, [_i]),

@@ -239,6 +239,164 @@ def fwd_delta(q, k, v, beta, feature="psd", return_state=False, S0=None):
     return (o, S) if return_state else o
 
 
+def _gated_shapes(q, k, v, g, beta, token_axis):
+    """(B, H_k, H, T, d_k, d_v) of a gated delta rule's inputs, checked; T is
+    None for the one-token step (no token axis)."""
+    n = 4 if token_axis else 3
+    tok = ", T" if token_axis else ""
+    if q.dim() != n or k.shape != q.shape or v.dim() != n or v.shape[0] != q.shape[0] or \
+            v.shape[2:-1] != q.shape[2:-1]:
+        raise ValueError(f"expected q, k [B, H_k{tok}, d_k] and v [B, H{tok}, d_v]; got "
+                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    if not (k.dtype == v.dtype == q.dtype):
+        raise TypeError("q, k, v must share one dtype")
+    B, H_k, H = q.shape[0], q.shape[1], v.shape[1]
+    if H and (H_k == 0 or H % H_k):
+        raise ValueError(f"the {H} value heads must be a multiple of the {H_k} key heads")
+    for t, name in ((g, "g"), (beta, "beta")):
+        if t.shape != v.shape[:-1]:
+            raise ValueError(f"{name} must be {list(v.shape[:-1])} fp32, got {list(t.shape)}")
+    return B, H_k, H, (q.shape[2] if token_axis else None), q.shape[-1], v.shape[-1]
+
+
+def _like(t, shape, dtype, name):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name} must be {list(shape)} {dtype}, got {list(t.shape)} {t.dtype}")
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+
+
+class _On:
+    """The device of a call's tensors and the stream it runs on (the device's
+    current stream unless one is given). What is allocated inside belongs to
+    that stream, so the caching allocator does not hand it out again while the
+    call's kernels still use it."""
+
+    def __init__(self, device, stream):
+        self.device, self.given = device, stream
+
+    def __enter__(self):
+        self.guard = torch.cuda.device(self.device)
+        self.guard.__enter__()
+        self.stream = self.given if self.given is not None else torch.cuda.current_stream(self.device)
+        self.inner = torch.cuda.stream(self.given) if self.given is not None else None
+        if self.inner is not None:
+            self.inner.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
+        return self.guard.__exit__(*exc)
+
+
+def fwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, dtype=torch.bfloat16) -> int:
+    return int(lib().kata_fwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, _DTYPES[dtype]))
+
+
+def bwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, dtype=torch.bfloat16) -> int:
+    return int(lib().kata_bwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, _DTYPES[dtype]))
+
+
+def _gated_workspace(workspace, bytes_fn, shape, q):
+    if workspace is None:
+        n = bytes_fn(*shape, q.dtype)
+        if n == 0:
+            raise ValueError("unsupported shape for the gated delta rule: B, H_k, H, T, d_k, d_v = "
+                             f"{shape}")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _same_device(q, workspace)
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+
+
+def kata_fwd_gated_delta(q, k, v, g, beta, o, S0=None, S_out=None, workspace=None, stream=None):
+    """Gated delta rule forward into `o` (see include/kata.h): q, k
+    [B, H_k, T, d_k], v, o [B, H, T, d_v], g (log decays) and beta (write
+    strengths) fp32 [B, H, T]; S0 / S_out optional fp32 [B, H, d_k, d_v]."""
+    shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
+    dt = _dtype(q)
+    _like(o, v.shape, q.dtype, "o")
+    for t, name in ((S0, "S0"), (S_out, "S_out")):
+        _like(t, (B, H, d_k, d_v), torch.float32, name)
+    _same_device(q, k, v, g, beta, o, S0, S_out)
+    ptrs = (_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g", torch.float32),
+            _dev(beta, "beta", torch.float32), _dev(o, "o"))
+    with _On(q.device, stream) as s:
+        ws, n, workspace = _gated_workspace(workspace, fwd_gated_delta_workspace_bytes, shape, q)
+        st = lib().kata_fwd_gated_delta(*ptrs, *shape, dt, _opt(S0, "S0"), _opt(S_out, "S_out"), ws, n, s)
+    check("kata_fwd_gated_delta", st)
+    return o
+
+
+def kata_bwd_gated_delta(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0=None, dS=None, dS0=None,
+                         workspace=None, stream=None):
+    """Gradient of kata_fwd_gated_delta into dq, dk, dv, dg, dbeta and, if
+    given, dS0, from dout = dL/do and optionally dS = dL/dS_out (see
+    include/kata.h)."""
+    shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
+    dt = _dtype(q)
+    for t, like, dtype, name in ((dout, v, q.dtype, "dout"), (dq, q, q.dtype, "dq"),
+                                 (dk, k, q.dtype, "dk"), (dv, v, q.dtype, "dv"),
+                                 (dg, g, torch.float32, "dg"), (dbeta, g, torch.float32, "dbeta")):
+        _like(t, like.shape, dtype, name)
+    for t, name in ((S0, "S0"), (dS, "dS"), (dS0, "dS0")):
+        _like(t, (B, H, d_k, d_v), torch.float32, name)
+    _same_device(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0, dS, dS0)
+    ptrs = (_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g", torch.float32),
+            _dev(beta, "beta", torch.float32), _dev(dout, "dout"), _opt(S0, "S0"), _opt(dS, "dS"),
+            _dev(dq, "dq"), _dev(dk, "dk"), _dev(dv, "dv"), _dev(dg, "dg"), _dev(dbeta, "dbeta"),
+            _opt(dS0, "dS0"))
+    with _On(q.device, stream) as s:
+        ws, n, workspace = _gated_workspace(workspace, bwd_gated_delta_workspace_bytes, shape, q)
+        st = lib().kata_bwd_gated_delta(*ptrs, *shape, dt, ws, n, s)
+    check("kata_bwd_gated_delta", st)
+    return dq, dk, dv, dg, dbeta, dS0
+
+
+def kata_gated_delta_step(q, k, v, g, beta, S, y, stream=None):
+    """In-place one-token step of the gated delta rule: q, k [B, H_k, d_k],
+    v, y [B, H, d_v], g, beta fp32 [B, H]; S fp32 [B, H, d_k, d_v] updated."""
+    B, H_k, H, _, d_k, d_v = _gated_shapes(q, k, v, g, beta, False)
+    dt = _dtype(q)
+    _like(y, v.shape, q.dtype, "y")
+    _like(S, (B, H, d_k, d_v), torch.float32, "S")
+    _same_device(q, k, v, g, beta, S, y)
+    ptrs = (_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g", torch.float32),
+            _dev(beta, "beta", torch.float32), _dev(S, "S"), _dev(y, "y"))
+    with _On(q.device, stream) as s:
+        st = lib().kata_gated_delta_step(*ptrs, B, H_k, H, d_k, d_v, dt, s)
+    check("kata_gated_delta_step", st)
+    return y
+
+
+def fwd_gated_delta(q, k, v, g, beta, S0=None, return_state=False):
+    """(o) or (o, S) of the gated delta rule, allocated with torch."""
+    o = torch.empty_like(v)
+    S = None
+    if return_state:
+        S = torch.empty((q.shape[0], v.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
+                        device=q.device)
+    kata_fwd_gated_delta(q, k, v, g, beta, o, S0=S0, S_out=S)
+    return (o, S) if return_state else o
+
+
+def bwd_gated_delta(q, k, v, g, beta, dout, S0=None, dS=None):
+    """(dq, dk, dv, dg, dbeta, dS0) of sum(dout * o) + sum(dS * S) for
+    (o, S) = fwd_gated_delta(...); dS0 is None unless S0 is given."""
+    return kata_bwd_gated_delta(q, k, v, g, beta, dout, torch.empty_like(q), torch.empty_like(k),
+                                torch.empty_like(v), torch.empty_like(g), torch.empty_like(beta),
+                                S0=S0, dS=dS, dS0=None if S0 is None else torch.empty_like(S0))
+
+
+def gated_delta_step(q, k, v, g, beta, S):
+    """y of the one-token step, allocated with torch; S is updated in place."""
+    return kata_gated_delta_step(q, k, v, g, beta, S, torch.empty_like(v))
+
+
 def kata_workspace_status(workspace, stream=None) -> int:
     """Synchronises the stream and returns the status code left in the workspace."""
     return int(lib().kata_workspace_status(_dev(workspace, "workspace"), _stream(stream)))
@@ -318,5 +476,7 @@ __all__ = [
     "kata_workspace_status", "profile_enable", "profile_read", "fwd_chunked", "fwd_quadratic", "decode_step", "_lib",
     "bwd_chunked_workspace_bytes", "kata_bwd_chunked", "bwd_chunked", "kata_chunked_state",
     "chunked_state", "kata_selftest_device_timeout", "fwd_chunked_plan", "kata_fwd_delta",
-    "fwd_delta",
+    "fwd_delta", "fwd_gated_delta_workspace_bytes", "bwd_gated_delta_workspace_bytes",
+    "kata_fwd_gated_delta", "kata_bwd_gated_delta", "kata_gated_delta_step", "fwd_gated_delta",
+    "bwd_gated_delta", "gated_delta_step",
 ]

@@ -1,0 +1,50 @@
+// Launch descriptors of the gated delta rule (forward, gradient, one-token
+// step), shared by its C ABI file and its kernel files.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+namespace kata {
+
+constexpr int kGdChunk = 64;     // tokens a chunk, in every kernel of the family
+
+// Tensors [B, heads, T, d], contiguous; value head h reads query / key head
+// h / (H / Hk). BH = B * H value heads, N = ceil(T / kGdChunk) chunks.
+struct GatedDeltaLaunch {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  void *o;                       // forward; null for the gradient
+  const float *S0;               // nullable [BH][d_k][d_v]
+  float *S_out;                  // forward: nullable
+  long long BH;
+  int H, Hk, T, N;
+  cudaStream_t stream;
+  // gradient
+  const void *dout = nullptr;
+  const float *dS = nullptr;     // nullable: the last state's gradient
+  void *dq = nullptr, *dk = nullptr, *dv = nullptr;
+  float *dg = nullptr, *dbeta = nullptr, *dS0 = nullptr;   // dS0 nullable
+  // workspace regions (CUDA-core kernels)
+  float *M = nullptr, *P = nullptr;             // [BH][N][64][64]
+  float *starts = nullptr, *ends = nullptr;     // [BH][N][d_k][d_v]: S and dS at the chunks' borders
+  float *writes = nullptr, *dR = nullptr;       // [BH][T][d_v]
+  float *dq_part = nullptr, *dk_part = nullptr; // [BH][T][d_k], only where heads share keys
+};
+
+struct GatedDeltaStep {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  float *S;
+  void *y;
+  long long BH;
+  int H, Hk;
+  cudaStream_t stream;
+};
+
+template <typename Tin> cudaError_t simt_gated_delta(const GatedDeltaLaunch &a, int d_k, int d_v);
+template <typename Tin> cudaError_t simt_gated_delta_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
+template <typename Tin> cudaError_t gated_delta_step(const GatedDeltaStep &a, int d_k, int d_v);
+
+}  // namespace kata

@@ -1,0 +1,183 @@
+// C ABI of the gated delta rule: argument checks, workspace layout and kernel
+// dispatch. The contract is in include/kata.h.
+#include "../../include/kata.h"
+
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "gated_delta.h"
+
+using namespace kata;
+
+namespace {
+
+constexpr size_t kHeaderBytes = 256;   // status word + padding
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool head_size(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+
+kata_status_t check_shape(int B, int H_k, int H, int T, int d_k, int d_v, kata_dtype_t dtype) {
+  if (B < 0 || H_k < 0 || H < 0 || T < 0) return KATA_ERR_INVALID_ARGUMENT;
+  if (dtype != KATA_DTYPE_F32 && dtype != KATA_DTYPE_BF16) return KATA_ERR_UNSUPPORTED;
+  if (!head_size(d_k) || !head_size(d_v)) return KATA_ERR_UNSUPPORTED;
+  if (H > 0 && (H_k == 0 || H % H_k != 0)) return KATA_ERR_INVALID_ARGUMENT;
+  if (T > 0x7fffffff - kGdChunk) return KATA_ERR_UNSUPPORTED;   // token indices stay in an int
+  // one block per head, chunk and 16 or 32 value columns: the largest grid
+  const long long N = T / kGdChunk + (T % kGdChunk != 0);
+  const long long per_head = N > d_v / 16 ? N : d_v / 16;
+  if ((long long)B * H > 0x7fffffffLL / (per_head > 0 ? per_head : 1)) return KATA_ERR_UNSUPPORTED;
+  return KATA_OK;
+}
+
+// Workspace: status header, then the regions of the launch descriptor in the
+// order below. `bytes` counts, `place` also hands out the pointers.
+struct Regions {
+  unsigned char *base;
+  size_t used = kHeaderBytes;
+  float *take(size_t floats) {
+    float *p = base ? reinterpret_cast<float *>(base + used) : nullptr;
+    used += align_up(floats * sizeof(float));
+    return p;
+  }
+};
+
+size_t place_forward(GatedDeltaLaunch &a, void *ws) {
+  Regions r{static_cast<unsigned char *>(ws)};
+  const size_t square = (size_t)a.BH * a.N * kGdChunk * kGdChunk;
+  a.M = r.take(square);
+  a.P = r.take(square);
+  return r.used;
+}
+
+size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, void *ws) {
+  Regions r{static_cast<unsigned char *>(ws)};
+  const size_t chunks = (size_t)a.BH * a.N, tokens = (size_t)a.BH * a.T;
+  a.M = r.take(chunks * kGdChunk * kGdChunk);
+  a.P = r.take(chunks * kGdChunk * kGdChunk);
+  a.starts = r.take(chunks * d_k * d_v);
+  a.ends = r.take(chunks * d_k * d_v);
+  a.writes = r.take(tokens * d_v);
+  a.dR = r.take(tokens * d_v);
+  if (a.H != a.Hk) {
+    a.dq_part = r.take(tokens * d_k);
+    a.dk_part = r.take(tokens * d_k);
+  }
+  return r.used;
+}
+
+GatedDeltaLaunch describe(int B, int H_k, int H, int T) {
+  GatedDeltaLaunch a{};
+  a.BH = (long long)B * H;
+  a.H = H;
+  a.Hk = H_k;
+  a.T = T;
+  a.N = T / kGdChunk + (T % kGdChunk != 0);
+  return a;
+}
+
+bool overlap(const float *x, const float *y, size_t floats) {
+  if (!x || !y) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  const uintptr_t n = floats * sizeof(float);
+  return a < b + n && b < a + n;
+}
+
+// an empty sequence leaves the state (or its gradient) as it came
+kata_status_t pass_state(const float *from, float *to, size_t floats, cudaStream_t stream) {
+  if (!to || floats == 0) return KATA_OK;
+  const size_t n = floats * sizeof(float);
+  const cudaError_t e = from ? cudaMemcpyAsync(to, from, n, cudaMemcpyDeviceToDevice, stream)
+                             : cudaMemsetAsync(to, 0, n, stream);
+  return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
+}
+
+kata_status_t check_workspace(const void *ws, size_t have, size_t need) {
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % kAlign != 0 || have < need) return KATA_ERR_WORKSPACE;
+  return KATA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kata_fwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_k, int d_v,
+                                            kata_dtype_t dtype) {
+  if (check_shape(B, H_k, H, T, d_k, d_v, dtype) != KATA_OK) return 0;
+  GatedDeltaLaunch a = describe(B, H_k, H, T);
+  return place_forward(a, nullptr);
+}
+
+kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, const float *g,
+                                   const float *beta, void *o, int B, int H_k, int H, int T, int d_k,
+                                   int d_v, kata_dtype_t dtype, const float *S0, float *S_out,
+                                   void *workspace, size_t workspace_bytes, kata_stream_t stream_) {
+  const kata_status_t shape = check_shape(B, H_k, H, T, d_k, d_v, dtype);
+  if (shape != KATA_OK) return shape;
+  GatedDeltaLaunch a = describe(B, H_k, H, T);
+  const kata_status_t ws = check_workspace(workspace, workspace_bytes, place_forward(a, workspace));
+  if (ws != KATA_OK) return ws;
+  a.stream = reinterpret_cast<cudaStream_t>(stream_);
+  const size_t state = (size_t)a.BH * d_k * d_v;
+  if (overlap(S0, S_out, state)) return KATA_ERR_INVALID_ARGUMENT;
+  if (a.BH > 0 && T > 0 && (!q || !k || !v || !g || !beta || !o)) return KATA_ERR_INVALID_ARGUMENT;
+  if (cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
+  if (a.BH == 0 || T == 0) return pass_state(S0, S_out, state, a.stream);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.o = o; a.S0 = S0; a.S_out = S_out;
+  const cudaError_t e = dtype == KATA_DTYPE_F32 ? simt_gated_delta<float>(a, d_k, d_v)
+                                                : simt_gated_delta<__nv_bfloat16>(a, d_k, d_v);
+  return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
+}
+
+size_t kata_bwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_k, int d_v,
+                                            kata_dtype_t dtype) {
+  if (check_shape(B, H_k, H, T, d_k, d_v, dtype) != KATA_OK) return 0;
+  GatedDeltaLaunch a = describe(B, H_k, H, T);
+  return place_backward(a, d_k, d_v, nullptr);
+}
+
+kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, const float *g,
+                                   const float *beta, const void *dout, const float *S0,
+                                   const float *dS, void *dq, void *dk, void *dv, float *dg,
+                                   float *dbeta, float *dS0, int B, int H_k, int H, int T, int d_k,
+                                   int d_v, kata_dtype_t dtype, void *workspace,
+                                   size_t workspace_bytes, kata_stream_t stream_) {
+  const kata_status_t shape = check_shape(B, H_k, H, T, d_k, d_v, dtype);
+  if (shape != KATA_OK) return shape;
+  GatedDeltaLaunch a = describe(B, H_k, H, T);
+  const kata_status_t ws =
+      check_workspace(workspace, workspace_bytes, place_backward(a, d_k, d_v, workspace));
+  if (ws != KATA_OK) return ws;
+  a.stream = reinterpret_cast<cudaStream_t>(stream_);
+  const size_t state = (size_t)a.BH * d_k * d_v;
+  if (overlap(dS, dS0, state) || overlap(S0, dS0, state)) return KATA_ERR_INVALID_ARGUMENT;
+  if (a.BH > 0 && T > 0 &&
+      (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta))
+    return KATA_ERR_INVALID_ARGUMENT;
+  if (cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
+  if (a.BH == 0 || T == 0) return pass_state(dS, dS0, state, a.stream);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
+  a.dout = dout; a.dS = dS; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
+  const cudaError_t e = dtype == KATA_DTYPE_F32
+                            ? simt_gated_delta_backward<float>(a, d_k, d_v)
+                            : simt_gated_delta_backward<__nv_bfloat16>(a, d_k, d_v);
+  return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
+}
+
+kata_status_t kata_gated_delta_step(const void *q, const void *k, const void *v, const float *g,
+                                    const float *beta, float *S, void *y, int B, int H_k, int H,
+                                    int d_k, int d_v, kata_dtype_t dtype, kata_stream_t stream_) {
+  const kata_status_t shape = check_shape(B, H_k, H, 1, d_k, d_v, dtype);
+  if (shape != KATA_OK) return shape;
+  const long long BH = (long long)B * H;
+  if (BH == 0) return KATA_OK;
+  if (!q || !k || !v || !g || !beta || !S || !y) return KATA_ERR_INVALID_ARGUMENT;
+  if (reinterpret_cast<uintptr_t>(S) % 16 != 0) return KATA_ERR_INVALID_ARGUMENT;
+  const GatedDeltaStep a{q, k, v, g, beta, S, y, BH, H, H_k, reinterpret_cast<cudaStream_t>(stream_)};
+  const cudaError_t e = dtype == KATA_DTYPE_F32 ? gated_delta_step<float>(a, d_k, d_v)
+                                                : gated_delta_step<__nv_bfloat16>(a, d_k, d_v);
+  return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -27,6 +27,10 @@ Parity status per function (what pins it is listed in tests/test_oracle_pins.py)
   (tests/test_oracle_variants.py: reductions to the rank-one oracle, closed
   forms, invariances, an unpacked delta rule), parity of the readings is
   unpinned.
+* the gated delta rule (oracle/gated_delta.py) -- pinned in
+  tests/test_oracle_gated_delta.py: finite differences of the gradient, the
+  ungated single-token and orthogonal-key closed forms, a reset, padding and
+  the additive limit.
 """
 
 from .kata import *  # noqa: F401,F403
@@ -38,4 +42,5 @@ from .kata import (  # noqa: F401
     psd_pairs, psd_query_feature, query_feature, state_dim, weights,
 )
 from .backward import backward_brute_force, backward_rows  # noqa: F401
+from . import gated_delta  # noqa: F401
 from . import variants  # noqa: F401
