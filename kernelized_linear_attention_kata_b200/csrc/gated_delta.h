@@ -31,6 +31,11 @@ struct GatedDeltaLaunch {
   float *starts = nullptr, *ends = nullptr;     // [BH][N][d_k][d_v]: S and dS at the chunks' borders
   float *writes = nullptr, *dR = nullptr;       // [BH][T][d_v]
   float *dq_part = nullptr, *dk_part = nullptr; // [BH][T][d_k], only where heads share keys
+  // tensor-core kernels: G segments of seg_chunks chunks a head; what the first
+  // G - 1 do to a state, S_end = F S_start + B, and the starting states
+  unsigned *status = nullptr;
+  int G = 1, seg_chunks = 0;
+  float *F = nullptr, *B = nullptr, *seg_starts = nullptr;
 };
 
 struct GatedDeltaStep {
@@ -45,6 +50,10 @@ struct GatedDeltaStep {
 
 template <typename Tin> cudaError_t simt_gated_delta(const GatedDeltaLaunch &a, int d_k, int d_v);
 template <typename Tin> cudaError_t simt_gated_delta_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
+// Tensor-core forward (bf16, d_k and d_v in {64, 128}, 16-byte aligned q, k, v).
+bool gd_tc_shape(int d_k, int d_v);
+void gd_tc_split(long long BH, int N, int sms, int *G, int *seg_chunks);
+cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v);
 template <typename Tin> cudaError_t gated_delta_step(const GatedDeltaStep &a, int d_k, int d_v);
 
 }  // namespace kata

@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 #include "gated_delta.h"
 
@@ -43,8 +45,39 @@ struct Regions {
   }
 };
 
-size_t place_forward(GatedDeltaLaunch &a, void *ws) {
+// bf16 with d_k and d_v in {64, 128} runs on the tensor cores. The choice is
+// made from type and sizes alone, so the workspace needs nothing for the other
+// kernels; TMA loads make 16-byte alignment a condition there.
+bool on_tensor_cores(int d_k, int d_v, kata_dtype_t dtype) {
+  return dtype == KATA_DTYPE_BF16 && gd_tc_shape(d_k, d_v);
+}
+
+bool aligned16(std::initializer_list<const void *> ps) {
+  for (const void *p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+  return true;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+}
+
+// 0 when the device cannot be asked for its size
+size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, void *ws) {
   Regions r{static_cast<unsigned char *>(ws)};
+  if (on_tensor_cores(d_k, d_v, dtype)) {
+    const int sms = sm_count();
+    if (sms <= 0) return 0;
+    if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, sms, &a.G, &a.seg_chunks);
+    if (a.G > 1) {
+      a.F = r.take((size_t)a.BH * (a.G - 1) * d_k * d_k);
+      a.B = r.take((size_t)a.BH * (a.G - 1) * d_k * d_v);
+      a.seg_starts = r.take((size_t)a.BH * a.G * d_k * d_v);
+    }
+    return r.used;
+  }
   const size_t square = (size_t)a.BH * a.N * kGdChunk * kGdChunk;
   a.M = r.take(square);
   a.P = r.take(square);
@@ -106,7 +139,7 @@ size_t kata_fwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_
                                             kata_dtype_t dtype) {
   if (check_shape(B, H_k, H, T, d_k, d_v, dtype) != KATA_OK) return 0;
   GatedDeltaLaunch a = describe(B, H_k, H, T);
-  return place_forward(a, nullptr);
+  return place_forward(a, d_k, d_v, dtype, nullptr);
 }
 
 kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, const float *g,
@@ -116,17 +149,24 @@ kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, 
   const kata_status_t shape = check_shape(B, H_k, H, T, d_k, d_v, dtype);
   if (shape != KATA_OK) return shape;
   GatedDeltaLaunch a = describe(B, H_k, H, T);
-  const kata_status_t ws = check_workspace(workspace, workspace_bytes, place_forward(a, workspace));
+  const size_t need = place_forward(a, d_k, d_v, dtype, workspace);
+  if (need == 0) return KATA_ERR_CUDA;
+  const kata_status_t ws = check_workspace(workspace, workspace_bytes, need);
   if (ws != KATA_OK) return ws;
   a.stream = reinterpret_cast<cudaStream_t>(stream_);
   const size_t state = (size_t)a.BH * d_k * d_v;
   if (overlap(S0, S_out, state)) return KATA_ERR_INVALID_ARGUMENT;
-  if (a.BH > 0 && T > 0 && (!q || !k || !v || !g || !beta || !o)) return KATA_ERR_INVALID_ARGUMENT;
+  const bool tc = on_tensor_cores(d_k, d_v, dtype);
+  if (a.BH > 0 && T > 0 &&
+      (!q || !k || !v || !g || !beta || !o || (tc && !aligned16({q, k, v}))))
+    return KATA_ERR_INVALID_ARGUMENT;
   if (cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
   if (a.BH == 0 || T == 0) return pass_state(S0, S_out, state, a.stream);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.o = o; a.S0 = S0; a.S_out = S_out;
-  const cudaError_t e = dtype == KATA_DTYPE_F32 ? simt_gated_delta<float>(a, d_k, d_v)
-                                                : simt_gated_delta<__nv_bfloat16>(a, d_k, d_v);
+  a.status = static_cast<unsigned *>(workspace);
+  const cudaError_t e = tc ? gd_tc_forward(a, d_k, d_v)
+                        : dtype == KATA_DTYPE_F32 ? simt_gated_delta<float>(a, d_k, d_v)
+                                                  : simt_gated_delta<__nv_bfloat16>(a, d_k, d_v);
   return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
 }
 

@@ -1,0 +1,634 @@
+// The gated delta rule's chunked forward on the tensor cores (tcgen05 / TMEM /
+// TMA): bf16, d_k and d_v in {64, 128}, chunks of C = 64 tokens.
+//
+// Per chunk, from its starting state S [d_k, d_v] (fp32), with G the running
+// sum of g, W_ts = e^{G_t - G_s} (s <= t), M = (I + L)^-1, L_ts = beta_t W_ts
+// k_t.k_s (s < t) and P_ts = W_ts q_t.k_s (s <= t):
+//   R = V - e^G (K S),  D = M diag(beta) R,
+//   O = e^G (Q S) + P D,  S' = e^{G_C} S + K^T (e^{G_C - G} D).
+//
+// Everything with a value axis is held transposed: thread r of a warpgroup
+// owns value column r (one TMEM lane), and the axis of the keys or tokens
+// runs along TMEM columns. Then every left operand (S^T, R^T, D^T) is written
+// to tensor memory by the threads that computed it, every right operand (K,
+// Q, M, P) is a shared-memory tile, and the state itself stays in registers
+// from the first chunk to the last:
+//   [K; Q] S      A = S^T (TMEM)           B = K, Q tiles, K-major
+//   M beta R      A = R^T (TMEM)           B = M diag(beta) tile
+//   K^T D~        A = (e^{G_C-G} D)^T      B = K tile, MN-major
+//   P D           A = D^T                  B = P tile
+// fp32 operands enter as two bf16 halves (hi + lo, 16 bits); q, k and v are
+// bf16 and exact. S rounded to one bf16 per product would put 2^-9 of it into
+// every later state.
+//
+// What bounds it: the chain S -> K S -> R -> D -> S' of one chunk, three MMA
+// rounds and three passes of the value threads over 64 columns, about 2 us a
+// chunk, while the tensor pipe is busy for two thirds of that (the operand
+// halves double its work). So all that does not depend on S is taken off the
+// chain: four warps compute M and P one chunk ahead, and the outputs of a
+// chunk leave while the next chunk's K S runs. With fewer heads than SMs the
+// sequence is cut into G segments: each but the last is first walked for its
+// effect on a state, S_end = F S_start + B (the same kernel without outputs,
+// once on V from S = 0 and once with V = 0 from S = I), a small kernel joins
+// them, and the segments then run side by side.
+//
+// Warps (448 threads): 0-7 the state warps (two warpgroups, each half of the
+// columns), 8-11 the chunk-local group (K rows on lanes 0-63, Q rows on
+// 64-127 of [K; Q] K^T), 12 the MMA issuer, 13 the TMA producer.
+#include "common.cuh"
+#include "gated_delta_tc.cuh"
+#include "profile.h"
+#include "tma_host.h"
+
+namespace kata {
+namespace {
+
+using namespace gdtc;
+
+constexpr int kThreads = 448;
+constexpr int kStateWarps = 8;
+constexpr uint32_t kTmemCols = 512;
+// Tensor memory columns. The state's operand halves share their columns with
+// the update's accumulator, R's with K S, D~'s with M R: each thread rewrites
+// only the columns it has read.
+constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColD = 256, kColDl = 320, kColO = 384,
+                   kColKQ = 448;
+constexpr int kKqStages = 3;
+
+template <int DK, int DV> struct Layout {
+  static constexpr int NP = DK / 64;                       // panels of a K or Q tile
+  static constexpr int kKq = 2 * NP * kPanel;              // [K p0][Q p0][K p1][Q p1]
+  static constexpr int kV = kC * DV * 2;
+  static constexpr int kOffKq = 0;
+  static constexpr int kOffM = kKqStages * kKq;            // two stages of hi, lo
+  static constexpr int kOffP = kOffM + 4 * kPanel;
+  static constexpr int kOffV = kOffP + 4 * kPanel;
+  static constexpr int kOffL = kOffV + 2 * kV;
+  static constexpr int kOffGates = kOffL + kC * kLs * 4;
+  static constexpr int kOffBars = kOffGates + 2 * (int)sizeof(Gates);
+  static constexpr int kBytes = kOffBars + 512 + 1024;     // barriers, alignment slack
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+enum {
+  kKqFull = 0, kKqEmpty = kKqFull + kKqStages, kVFull = kKqEmpty + kKqStages, kVEmpty = kVFull + 2,
+  kPmFull = kVEmpty + 2, kPmEmpty = kPmFull + 2, kSReady = kPmEmpty + 2, kKsDone, kRReady, kDDone,
+  kDtReady, kDlReady, kUDone, kODone, kOFree, kKkDone, kEnd, kEnd2, kNumBars
+};
+static_assert(8 * kNumBars + 8 <= 512, "barrier area");
+
+struct Args {
+  const float *g, *beta, *S0;
+  __nv_bfloat16 *o;
+  float *S_out;
+  float *F, *B;                    // segments' effects [BH][G - 1][..]: kind 1 and kind 0
+  const float *starts;             // segments' starting states [BH][G][d_k][d_v], 1 .. G - 1 used
+  unsigned *status;
+  int H, Hk, T, G, seg_chunks;
+};
+
+// OUT: outputs of segments 0 .. G - 1. !OUT: the effect of segments 0 .. G - 2
+// on a state; blockIdx picks the kind (0: B, from V and S = 0; 1: F, from S = I).
+template <int DK, int DV, bool OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+             const __grid_constant__ CUtensorMap tmv, const Args a) {
+  using L = Layout<DK, DV>;
+  constexpr int NP = L::NP;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBars);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  Gates *gates = reinterpret_cast<Gates *>(smem + L::kOffGates);
+  float *Lm = reinterpret_cast<float *>(smem + L::kOffL);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int segs = OUT ? a.G : a.G - 1;
+  const int kind = OUT ? 0 : (int)(blockIdx.x % 2);
+  const int job = OUT ? (int)blockIdx.x : (int)(blockIdx.x / 2);
+  const int seg = job % segs;
+  const int bh = job / segs;
+  const int kh = bh / a.H * a.Hk + bh % a.H / (a.H / a.Hk);
+  const int t_begin = seg * a.seg_chunks * kC;
+  const int t_left = a.T - t_begin;
+  const int nall = t_left <= 0 ? 0 : (t_left - 1) / kC + 1;
+  const int n = nall < a.seg_chunks ? nall : a.seg_chunks;
+  const bool values = OUT || kind == 0;                    // V is read
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      uint32_t count = 1;
+      if (i == kVEmpty || i == kVEmpty + 1 || i == kSReady || i == kRReady || i == kDtReady ||
+          i == kDlReady || i == kOFree)
+        count = kStateWarps;
+      if (i == kPmFull || i == kPmFull + 1) count = 4;
+      if (i == kPmEmpty || i == kPmEmpty + 1) count = 1 + kStateWarps;
+      mbar_init(&bars[i], count);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp < kStateWarps) {
+    // ------------------------------------------------------------ state warps
+    const int h = warp / 4;                                // half of the columns
+    const int r = 32 * (warp % 4) + lane;                  // value column
+    const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
+    const int width = values ? DV : DK;                    // value columns (kind 1: those of I)
+    const bool active = r < width;                         // the same in the whole warp
+    constexpr int HK = DK / 2;                             // state entries a thread
+    float S[HK];
+    {
+      const float *src = nullptr;
+      if (OUT)
+        src = seg == 0 ? (a.S0 ? a.S0 + (size_t)bh * DK * DV : nullptr)
+                       : a.starts + ((size_t)bh * a.G + seg) * DK * DV;
+#pragma unroll
+      for (int i = 0; i < HK; ++i)
+        S[i] = src && active ? src[(size_t)(HK * h + i) * DV + r] : (kind == 1 && HK * h + i == r ? 1.f : 0.f);
+    }
+    const uint32_t col_s = tbase + lane_off + kColS + HK * h;      // hi: HK / 2 columns, then lo
+    const uint32_t col_half = tbase + lane_off + 32 * h;           // + a 64-token region
+    __nv_bfloat16 *o = OUT ? a.o + ((size_t)bh * a.T + t_begin) * DV + r : nullptr;
+    bool ok = true;
+
+    // outputs of chunk c: o_t = e^{G_t} (Q S)_t + (P D)_t, 32 tokens a thread
+    auto outputs = [&](int c) -> bool {
+      if (!warp_wait(&bars[kODone], c & 1, abort_flag)) return false;
+      tc_fence_after();
+      if (active) {
+        const float *fs = gates[c & 1].from_start + 32 * h;
+        __nv_bfloat16 *dst = o + (size_t)(kC * c + 32 * h) * DV;
+        const int left = t_left - (kC * c + 32 * h);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t x[16], y[16];
+          tmem_ld16(col_half + kColQS + 16 * b, x);
+          tmem_ld16(col_half + kColO + 16 * b, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (16 * b + i < left)
+              dst[(size_t)(16 * b + i) * DV] = __float2bfloat16_rn(
+                  fmaf(fs[16 * b + i], __uint_as_float(x[i]), __uint_as_float(y[i])));
+        }
+      }
+      tc_fence_before();
+      warp_arrive(&bars[kOFree]);
+      warp_arrive(&bars[kPmEmpty + (c & 1)]);
+      return true;
+    };
+
+    for (int c = 0; c < n; ++c) {
+      const int st = c & 1;
+      // S as the next products' operand
+      if (active) {
+#pragma unroll
+        for (int b = 0; b < HK / 32; ++b) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) split2(S[32 * b + 2 * i], S[32 * b + 2 * i + 1], hi[i], lo[i]);
+          tmem_st16(col_s + 16 * b, hi);
+          tmem_st16(col_s + HK / 2 + 16 * b, lo);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      warp_arrive(&bars[kSReady]);
+      if (OUT && c > 0 && !(ok = outputs(c - 1))) break;
+
+      // R = V - e^G (K S)
+      if (!(ok = warp_wait(&bars[kPmFull + st], (c >> 1) & 1, abort_flag))) break;
+      if (values && !(ok = warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag))) break;
+      float R[32];
+      if (active && values) {
+        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + L::kOffV + st * L::kV) +
+                                 32 * h * DV + r;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) R[i] = __bfloat162float(v[i * DV]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) R[i] = 0.f;
+      }
+      if (values) warp_arrive(&bars[kVEmpty + st]);
+      const Gates &gt = gates[st];
+      if (!(ok = warp_wait(&bars[kKsDone], c & 1, abort_flag))) break;
+      tc_fence_after();
+      if (active) {
+        uint32_t x[32];
+        tmem_ld32(col_half + kColKS, x);
+        tmem_wait_ld();
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = *reinterpret_cast<const float2 *>(&gt.from_start[32 * h + 2 * i]);
+          split2(fmaf(-f.x, __uint_as_float(x[2 * i]), R[2 * i]),
+                 fmaf(-f.y, __uint_as_float(x[2 * i + 1]), R[2 * i + 1]), hi[i], lo[i]);
+        }
+        tmem_st16(col_half + kColKS, hi);
+        tmem_st16(col_half + kColKS + 16, lo);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      warp_arrive(&bars[kRReady]);
+
+      // D: scaled for the update first, as it is for the outputs after
+      if (!(ok = warp_wait(&bars[kDDone], c & 1, abort_flag))) break;
+      tc_fence_after();
+      uint32_t d[32];
+      if (active) {
+        tmem_ld32(col_half + kColD, d);
+        tmem_wait_ld();
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = *reinterpret_cast<const float2 *>(&gt.to_end[32 * h + 2 * i]);
+          split2(f.x * __uint_as_float(d[2 * i]), f.y * __uint_as_float(d[2 * i + 1]), hi[i], lo[i]);
+        }
+        tmem_st16(col_half + kColD, hi);
+        tmem_st16(col_half + kColD + 16, lo);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      warp_arrive(&bars[kDtReady]);
+      const float whole = gt.from_start[kC - 1];
+      if (OUT) {
+        if (active) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            split2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]), hi[i], lo[i]);
+          tmem_st16(col_half + kColDl, hi);
+          tmem_st16(col_half + kColDl + 16, lo);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        warp_arrive(&bars[kDlReady]);
+      } else {
+        warp_arrive(&bars[kPmEmpty + st]);
+      }
+
+      // S' = e^{G_C} S + K^T D~
+      if (!(ok = warp_wait(&bars[kUDone], c & 1, abort_flag))) break;
+      tc_fence_after();
+      if (active) {
+#pragma unroll
+        for (int b = 0; b < HK / 32; ++b) {
+          uint32_t x[32];
+          tmem_ld32(col_s + 32 * b, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) S[32 * b + i] = fmaf(whole, S[32 * b + i], __uint_as_float(x[i]));
+        }
+      }
+    }
+    if (OUT && ok && n > 0) ok = outputs(n - 1);
+    if (active && ok) {
+      float *dst = nullptr;
+      int ld = DV;
+      if (OUT) {
+        if (seg == a.G - 1 && a.S_out) dst = a.S_out + (size_t)bh * DK * DV;
+      } else if (kind == 0) {
+        dst = a.B + ((size_t)bh * segs + seg) * DK * DV;
+      } else {
+        dst = a.F + ((size_t)bh * segs + seg) * DK * DK;
+        ld = DK;
+      }
+      if (dst) {
+#pragma unroll
+        for (int i = 0; i < HK; ++i) dst[(size_t)(HK * h + i) * ld + r] = S[i];
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ M and P, one chunk ahead
+    const int w = warp - 8;
+    const int t = 32 * (w & 1) + lane;                     // K row (w < 2) or Q row (w >= 2)
+    const uint32_t lane_off = (uint32_t)(32 * w) << 16;
+    const float *gp = a.g + (size_t)bh * a.T + t_begin, *bp = a.beta + (size_t)bh * a.T + t_begin;
+    float gx = 0.f, gy = 0.f, bx = 0.f, by = 0.f;          // the next chunk's gates
+    auto fetch = [&](int c) {
+      const int u = kC * c + 2 * lane;
+      gx = u < t_left ? gp[u] : 0.f;
+      gy = u + 1 < t_left ? gp[u + 1] : 0.f;
+      bx = u < t_left ? bp[u] : 0.f;
+      by = u + 1 < t_left ? bp[u + 1] : 0.f;
+    };
+    constexpr uint32_t id_kq = idesc_bf16(128, kC, false, false);
+    auto issue_kq = [&](int c) -> bool {                   // [K; Q] K^T of chunk c
+      const int st = c % kKqStages;
+      if (!mbar_wait(&bars[kKqFull + st], (c / kKqStages) & 1, abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t kq = smem_u32(smem + L::kOffKq + st * L::kKq);
+#pragma unroll
+      for (int k = 0; k < DK / 16; ++k) {
+        const uint64_t desc = smem_desc(kq + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128);
+        mma_ss(tbase + kColKQ, desc, desc, id_kq, k > 0);
+      }
+      mma_commit(&bars[kKkDone]);
+      return true;
+    };
+    bool ok = true;
+    if (w == 0) fetch(0);
+    if (w == 2 && lane == 0 && n > 0) ok = issue_kq(0);
+    ok = __all_sync(0xffffffffu, ok);
+    // an aborted warp goes on through the group's barriers without work
+    for (int c = 0; c < n; ++c) {
+      const int st = c & 1;
+      Gates &gt = gates[st];
+      if (ok && c >= 2) ok = warp_wait(&bars[kPmEmpty + st], ((c >> 1) - 1) & 1, abort_flag);
+      if (w == 0) {
+        make_gates(gt, gx, gy, bx, by);
+        if (c + 1 < n) fetch(c + 1);
+      }
+      intra_sync();
+      if (ok) ok = warp_wait(&bars[kKkDone], c & 1, abort_flag);
+      if (ok) tc_fence_after();
+      const float hi_t = gt.hi[t], lo_t = gt.lo[t], b_t = gt.beta[t];
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {               // 32 of the 64 columns
+        if (w == 0 ? half == 1 : (w >= 2 && !OUT)) continue;
+        uint32_t x[32];
+        if (ok) {
+          tmem_ld32(tbase + lane_off + kColKQ + 32 * half, x);
+          tmem_wait_ld();
+        }
+        if (w < 2) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const int s = 32 * half + j;
+            float4 l;
+            l.x = s < t ? b_t * decay_ratio(gt, hi_t, lo_t, s) * __uint_as_float(x[j]) : 0.f;
+            l.y = s + 1 < t ? b_t * decay_ratio(gt, hi_t, lo_t, s + 1) * __uint_as_float(x[j + 1]) : 0.f;
+            l.z = s + 2 < t ? b_t * decay_ratio(gt, hi_t, lo_t, s + 2) * __uint_as_float(x[j + 2]) : 0.f;
+            l.w = s + 3 < t ? b_t * decay_ratio(gt, hi_t, lo_t, s + 3) * __uint_as_float(x[j + 3]) : 0.f;
+            *reinterpret_cast<float4 *>(Lm + t * kLs + s) = l;
+          }
+        } else {
+          uint8_t *tile = smem + L::kOffP + st * 2 * kPanel;
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            float p[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int s = 32 * half + 8 * cc + j;
+              p[j] = s <= t ? decay_ratio(gt, hi_t, lo_t, s) * __uint_as_float(x[8 * cc + j]) : 0.f;
+            }
+            store_split8(tile, tile + kPanel, t, 4 * half + cc, p);
+          }
+        }
+      }
+      tc_fence_before();
+      intra_sync();                                        // the products have been read
+      if (w < 2) {
+        invert_diagonal(Lm, w);
+      } else if (w == 2 && c + 1 < n) {
+        bool sent = true;
+        if (ok && lane == 0) sent = issue_kq(c + 1);
+        ok = __all_sync(0xffffffffu, sent) && ok;
+      }
+      intra_sync();
+      invert_corner(Lm);
+      uint8_t *tile = smem + L::kOffM + st * 2 * kPanel;
+      store_inverse<true>(Lm, gt, tile, tile + kPanel);
+      fence_async_smem();
+      if (ok) warp_arrive(&bars[kPmFull + st]);
+      intra_sync();                                        // Lm is free
+    }
+    if (w == 2 && lane == 0 && *abort_flag && n > 0) {     // MMAs of this thread in flight
+      mma_commit(&bars[kEnd2]);
+      drain(&bars[kEnd2], 0);
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_n = idesc_bf16(128, kC, false, false);   // K-major right operand
+      constexpr uint32_t id_mn = idesc_bf16(128, 64, false, true);   // MN-major
+      bool ok = true;
+      // D[64 columns] = (hi + lo of a 64-token operand) (hi + lo tile), lo lo left out
+      auto product64 = [&](uint32_t dst, uint32_t op, uint32_t tile) {
+        bool first = true;
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t col = op + 32 * (k / 2) + 8 * (k % 2) + (pass == 2 ? 16 : 0);
+            mma_ts(dst, col, smem_desc(tile + (pass == 1 ? kPanel : 0) + 32 * k, 16, 1024, kSw128), id_n,
+                   !first);
+            first = false;
+          }
+      };
+      // D[64 tokens] = S^T (hi + lo) times the rows of a K or Q tile
+      auto with_state = [&](uint32_t dst, uint32_t rows) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k) {
+            constexpr int HK = DK / 2, KH = HK / 16;       // 16-key steps a warpgroup's half
+            const uint32_t col = tbase + kColS + HK * (k / KH) + 8 * (k % KH) + (half ? HK / 2 : 0);
+            mma_ts(dst, col, smem_desc(rows + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128), id_n,
+                   half > 0 || k > 0);
+          }
+      };
+      for (int c = 0; c < n && ok; ++c) {
+        const int st = c & 1, ks = c % kKqStages;
+        const uint32_t kq = smem_u32(smem + L::kOffKq + ks * L::kKq);
+        if (!(ok = mbar_wait(&bars[kKqFull + ks], (c / kKqStages) & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(&bars[kSReady], c & 1, abort_flag))) break;
+        tc_fence_after();
+        with_state(tbase + kColKS, kq);
+        mma_commit(&bars[kKsDone]);
+        if (OUT) {
+          if (c > 0 && !(ok = mbar_wait(&bars[kOFree], (c - 1) & 1, abort_flag))) break;
+          tc_fence_after();
+          with_state(tbase + kColQS, kq + kPanel);
+        }
+        if (!(ok = mbar_wait(&bars[kPmFull + st], (c >> 1) & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(&bars[kRReady], c & 1, abort_flag))) break;
+        tc_fence_after();
+        product64(tbase + kColD, tbase + kColKS, smem_u32(smem + L::kOffM + st * 2 * kPanel));
+        mma_commit(&bars[kDDone]);
+        if (!(ok = mbar_wait(&bars[kDtReady], c & 1, abort_flag))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              mma_ts(tbase + kColS + 64 * p, tbase + kColD + 32 * (k / 2) + 8 * (k % 2) + 16 * half,
+                     smem_desc(kq + p * 2 * kPanel + k * 2048, 16384, 1024, kSw128), id_mn, half > 0 || k > 0);
+        mma_commit(&bars[kUDone]);
+        if (OUT) {
+          if (!(ok = mbar_wait(&bars[kDlReady], c & 1, abort_flag))) break;
+          tc_fence_after();
+          product64(tbase + kColO, tbase + kColDl, smem_u32(smem + L::kOffP + st * 2 * kPanel));
+          mma_commit(&bars[kODone]);
+        }
+        mma_commit(&bars[kKqEmpty + ks]);
+        mma_commit(&bars[kPmEmpty + st]);
+      }
+      if (!ok) {
+        mma_commit(&bars[kEnd]);
+        drain(&bars[kEnd], 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmk);
+      if (OUT) tma_prefetch_desc(&tmq);
+      if (values) tma_prefetch_desc(&tmv);
+      bool ok = true;
+      int kq_sent = 0, v_sent = 0;
+      for (int c = 0; c < n; ++c) {
+        const int ks = c % kKqStages, vs = c & 1, row = t_begin + kC * c;
+        if (c >= kKqStages &&
+            !(ok = mbar_wait(&bars[kKqEmpty + ks], ((c / kKqStages) - 1) & 1, abort_flag)))
+          break;
+        uint8_t *kq = smem + L::kOffKq + ks * L::kKq;
+        mbar_arrive_expect_tx(&bars[kKqFull + ks], OUT ? L::kKq : L::kKq / 2);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          tma_load_3d(kq + 2 * p * kPanel, &tmk, &bars[kKqFull + ks], 64 * p, row, kh);
+          if (OUT) tma_load_3d(kq + (2 * p + 1) * kPanel, &tmq, &bars[kKqFull + ks], 64 * p, row, kh);
+        }
+        kq_sent = c + 1;
+        if (values) {
+          if (c >= 2 && !(ok = mbar_wait(&bars[kVEmpty + vs], ((c >> 1) - 1) & 1, abort_flag))) break;
+          mbar_arrive_expect_tx(&bars[kVFull + vs], L::kV);
+          tma_load_3d(smem + L::kOffV + vs * L::kV, &tmv, &bars[kVFull + vs], 0, row, bh);
+          v_sent = c + 1;
+        }
+      }
+      if (*abort_flag) {                                   // copies in flight land before the exit
+        for (int c = kq_sent > kKqStages ? kq_sent - kKqStages : 0; c < kq_sent; ++c)
+          drain(&bars[kKqFull + c % kKqStages], (c / kKqStages) & 1);
+        for (int c = v_sent > 2 ? v_sent - 2 : 0; c < v_sent; ++c)
+          drain(&bars[kVFull + (c & 1)], (c >> 1) & 1);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tbase, kTmemCols);
+  if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
+}
+
+// Starting states of the segments, S_{j+1} = F_j S_j + B_j: one block a head
+// and kJoinCols value columns, S in shared memory, F read row by row.
+constexpr int kJoinCols = 16;
+template <int DK>
+__global__ void __launch_bounds__(256)
+gd_join_kernel(const float *__restrict__ F, const float *__restrict__ B, const float *__restrict__ S0,
+               float *__restrict__ starts, int G, int DV) {
+  __shared__ float S[DK][kJoinCols + 1];
+  const int nb = DV / kJoinCols, bh = blockIdx.x / nb, c0 = blockIdx.x % nb * kJoinCols;
+  const int tid = threadIdx.x, col = tid % kJoinCols, row = tid / kJoinCols;    // rows row + 16 i
+  constexpr int PER = DK / 16;
+  for (int e = tid; e < DK * kJoinCols; e += 256)
+    S[e / kJoinCols][e % kJoinCols] =
+        S0 ? S0[((size_t)bh * DK + e / kJoinCols) * DV + c0 + e % kJoinCols] : 0.f;
+  for (int j = 0; j + 1 < G; ++j) {
+    const float *f = F + ((size_t)bh * (G - 1) + j) * DK * DK;
+    const float *b = B + ((size_t)bh * (G - 1) + j) * DK * DV;
+    float acc[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = b[(size_t)(row + 16 * i) * DV + c0 + col];
+    __syncthreads();
+#pragma unroll 4
+    for (int k = 0; k < DK; k += 4) {
+      const float s0 = S[k][col], s1 = S[k + 1][col], s2 = S[k + 2][col], s3 = S[k + 3][col];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(f + (size_t)(row + 16 * i) * DK + k);
+        acc[i] = fmaf(x.x, s0, acc[i]);
+        acc[i] = fmaf(x.y, s1, acc[i]);
+        acc[i] = fmaf(x.z, s2, acc[i]);
+        acc[i] = fmaf(x.w, s3, acc[i]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      S[row + 16 * i][col] = acc[i];
+      starts[(((size_t)bh * G + j + 1) * DK + row + 16 * i) * DV + c0 + col] = acc[i];
+    }
+  }
+}
+
+template <int DK, int DV>
+cudaError_t launch(const GatedDeltaLaunch &a) {
+  using L = Layout<DK, DV>;
+  CUtensorMap tq, tk, tv;
+  const long long BHk = a.BH / a.H * a.Hk;
+  if (!make_tma_3d_bf16_box(&tq, a.q, DK, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tk, a.k, DK, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tv, a.v, DV, a.T, a.BH, DV, kC, false))
+    return cudaErrorInvalidValue;
+  Args x{a.g, a.beta, a.S0, static_cast<__nv_bfloat16 *>(a.o), a.S_out, a.F, a.B, a.seg_starts,
+         a.status, a.H, a.Hk, a.T, a.G, a.seg_chunks};
+  if (a.G > 1) {
+    auto kern = gd_tc_kernel<DK, DV, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (e != cudaSuccess) return e;
+    {
+      ProfileScope prof("gd_tc_segment", a.stream);
+      kern<<<(unsigned)(a.BH * (a.G - 1) * 2), kThreads, L::kBytes, a.stream>>>(tq, tk, tv, x);
+    }
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ProfileScope prof("gd_join", a.stream);
+    gd_join_kernel<DK><<<(unsigned)(a.BH * (DV / kJoinCols)), 256, 0, a.stream>>>(
+        a.F, a.B, a.S0, a.seg_starts, a.G, DV);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  auto kern = gd_tc_kernel<DK, DV, true>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  ProfileScope prof("gd_tc_forward", a.stream);
+  kern<<<(unsigned)(a.BH * a.G), kThreads, L::kBytes, a.stream>>>(tq, tk, tv, x);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool gd_tc_shape(int d_k, int d_v) {
+  return (d_k == 64 || d_k == 128) && (d_v == 64 || d_v == 128);
+}
+
+// Segments a head, by the time they should take: a chunk of the effect pass
+// costs about 3/4 of an output chunk, a wave runs one block an SM, and every
+// segment adds a join step of about two chunks' time.
+void gd_tc_split(long long BH, int N, int sms, int *G, int *seg_chunks) {
+  int best = 1;
+  double least = 1e300;
+  for (int g = 1; g <= 64 && (g == 1 || (long long)g * BH <= sms); ++g) {
+    const int per = (N + g - 1) / g, used = per > 0 ? (N + per - 1) / per : 1;
+    if (used != g) continue;
+    const double out = (double)((BH * g + sms - 1) / sms) * per;
+    const double effect = g > 1 ? 0.75 * (double)((2 * BH * (g - 1) + sms - 1) / sms) * per + 2.0 * g + 6.0 : 0.0;
+    if (out + effect < least) {
+      least = out + effect;
+      best = g;
+    }
+  }
+  *G = best;
+  *seg_chunks = (N + best - 1) / best;
+}
+
+cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v) {
+  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a) : launch<64, 128>(a);
+  return d_v == 64 ? launch<128, 64>(a) : launch<128, 128>(a);
+}
+
+}  // namespace kata

@@ -48,4 +48,19 @@ bool make_tma_3d_bf16(CUtensorMap *map, const void *base, int d, int T, long lon
   return r == CUDA_SUCCESS;
 }
 
+bool make_tma_3d_bf16_box(CUtensorMap *map, const void *base, int d, long long T, long long BH,
+                          int cols, int rows, bool swizzle128) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || !base || T <= 0 || BH <= 0 || reinterpret_cast<uintptr_t>(base) % 16 != 0) return false;
+  if (d % 8 != 0 || cols % 8 != 0 || cols > 128 || (swizzle128 && cols != 64)) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)BH};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * (cuuint64_t)T};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace kata

@@ -14,4 +14,10 @@ namespace kata {
 // failure (unsupported row size, misaligned base, driver error).
 bool make_tma_3d_bf16(CUtensorMap *map, const void *base, int d, int T, long long BH, int rows);
 
+// A box of (cols, rows, 1) over the same tensor, for rows wider than a box:
+// swizzle128 with cols = 64 (128-byte rows), else no swizzle (cols * 2 <= 256
+// bytes, rows dense in shared memory).
+bool make_tma_3d_bf16_box(CUtensorMap *map, const void *base, int d, long long T, long long BH,
+                          int cols, int rows, bool swizzle128);
+
 }  // namespace kata
