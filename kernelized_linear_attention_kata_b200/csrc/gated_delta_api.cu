@@ -158,7 +158,7 @@ kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, 
   if (overlap(S0, S_out, state)) return KATA_ERR_INVALID_ARGUMENT;
   const bool tc = on_tensor_cores(d_k, d_v, dtype);
   if (a.BH > 0 && T > 0 &&
-      (!q || !k || !v || !g || !beta || !o || (tc && !aligned16({q, k, v}))))
+      (!q || !k || !v || !g || !beta || !o || (tc && !aligned16({q, k, v, o}))))
     return KATA_ERR_INVALID_ARGUMENT;
   if (cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
   if (a.BH == 0 || T == 0) return pass_state(S0, S_out, state, a.stream);

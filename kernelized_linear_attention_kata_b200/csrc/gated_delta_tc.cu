@@ -32,9 +32,15 @@
 // once on V from S = 0 and once with V = 0 from S = I), a small kernel joins
 // them, and the segments then run side by side.
 //
-// Warps (448 threads): 0-7 the state warps (two warpgroups, each half of the
+// An issuing thread gets an MMA out every 75-95 cycles whatever its N, so N is
+// 128 wherever two tiles lie side by side: K and Q rows, the two 64-key panels
+// of the update, the hi and lo tiles of M.
+//
+// Warps (512 threads): 0-7 the state warps (two warpgroups, each half of the
 // columns), 8-11 the chunk-local group (K rows on lanes 0-63, Q rows on
-// 64-127 of [K; Q] K^T), 12 the MMA issuer, 13 the TMA producer.
+// 64-127 of [K; Q] K^T), 12 the MMA issuer, 13 the TMA loads, 14 the output
+// stores, 15 the gates. Registers are moved from the last two warpgroups to
+// the state warps, which hold up to 64 entries of S and as many in flight.
 #include "common.cuh"
 #include "gated_delta_tc.cuh"
 #include "profile.h"
@@ -45,40 +51,42 @@ namespace {
 
 using namespace gdtc;
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 512;
 constexpr int kStateWarps = 8;
+constexpr int kStateRegs = 168, kIntraRegs = 112, kHelperRegs = 64;
+static_assert(2 * kStateRegs + kIntraRegs + kHelperRegs <= 4 * 128, "registers at launch");
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory columns. The state's operand halves share their columns with
-// the update's accumulator, R's with K S, D~'s with M R: each thread rewrites
-// only the columns it has read.
+// the update's accumulator, R's with K S, D~'s and D's with M R: each thread
+// rewrites only the columns it has read.
 constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColD = 256, kColDl = 320, kColO = 384,
                    kColKQ = 448;
-constexpr int kKqStages = 3;
+constexpr int kKqStages = 3, kGateStages = 3;
 
 template <int DK, int DV> struct Layout {
   static constexpr int NP = DK / 64;                       // panels of a K or Q tile
   static constexpr int kKq = 2 * NP * kPanel;              // [K p0][Q p0][K p1][Q p1]
-  static constexpr int kV = kC * DV * 2;
+  static constexpr int kV = kC * DV * 2;                   // V, then the outputs in its place
   static constexpr int kOffKq = 0;
   static constexpr int kOffM = kKqStages * kKq;            // two stages of hi, lo
   static constexpr int kOffP = kOffM + 4 * kPanel;
   static constexpr int kOffV = kOffP + 4 * kPanel;
   static constexpr int kOffL = kOffV + 2 * kV;
   static constexpr int kOffGates = kOffL + kC * kLs * 4;
-  static constexpr int kOffBars = kOffGates + 2 * (int)sizeof(Gates);
+  static constexpr int kOffBars = kOffGates + kGateStages * (int)sizeof(Gates);
   static constexpr int kBytes = kOffBars + 512 + 1024;     // barriers, alignment slack
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 enum {
   kKqFull = 0, kKqEmpty = kKqFull + kKqStages, kVFull = kKqEmpty + kKqStages, kVEmpty = kVFull + 2,
-  kPmFull = kVEmpty + 2, kPmEmpty = kPmFull + 2, kSReady = kPmEmpty + 2, kKsDone, kRReady, kDDone,
-  kDtReady, kDlReady, kUDone, kODone, kOFree, kKkDone, kEnd, kEnd2, kNumBars
+  kPmFull = kVEmpty + 2, kPmEmpty = kPmFull + 2, kGateFull = kPmEmpty + 2,
+  kGateEmpty = kGateFull + kGateStages, kSReady = kGateEmpty + kGateStages, kKsDone, kRReady, kDDone,
+  kDtReady, kDlReady, kUDone, kODone, kOReady, kKkDone, kEnd, kEnd2, kNumBars
 };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
 
 struct Args {
   const float *g, *beta, *S0;
-  __nv_bfloat16 *o;
   float *S_out;
   float *F, *B;                    // segments' effects [BH][G - 1][..]: kind 1 and kind 0
   const float *starts;             // segments' starting states [BH][G][d_k][d_v], 1 .. G - 1 used
@@ -91,7 +99,8 @@ struct Args {
 template <int DK, int DV, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-             const __grid_constant__ CUtensorMap tmv, const Args a) {
+             const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
+             const Args a) {
   using L = Layout<DK, DV>;
   constexpr int NP = L::NP;
   extern __shared__ uint8_t smem_raw[];
@@ -119,11 +128,11 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kVEmpty || i == kVEmpty + 1 || i == kSReady || i == kRReady || i == kDtReady ||
-          i == kDlReady || i == kOFree)
+      if (i == kSReady || i == kRReady || i == kDtReady || i == kDlReady || i == kOReady ||
+          (i >= kGateEmpty && i < kGateEmpty + kGateStages) ||
+          (!OUT && (i == kVEmpty || i == kVEmpty + 1)))
         count = kStateWarps;
       if (i == kPmFull || i == kPmFull + 1) count = 4;
-      if (i == kPmEmpty || i == kPmEmpty + 1) count = 1 + kStateWarps;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -140,99 +149,97 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
 
   if (warp < kStateWarps) {
     // ------------------------------------------------------------ state warps
+    more_registers<kStateRegs>();
     const int h = warp / 4;                                // half of the columns
     const int r = 32 * (warp % 4) + lane;                  // value column
     const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
     const int width = values ? DV : DK;                    // value columns (kind 1: those of I)
     const bool active = r < width;                         // the same in the whole warp
     constexpr int HK = DK / 2;                             // state entries a thread
-    float S[HK];
+    float2 S[HK / 2];
     {
       const float *src = nullptr;
       if (OUT)
         src = seg == 0 ? (a.S0 ? a.S0 + (size_t)bh * DK * DV : nullptr)
                        : a.starts + ((size_t)bh * a.G + seg) * DK * DV;
+      auto entry = [&](int k) {
+        return src && active ? src[(size_t)k * DV + r] : (kind == 1 && k == r ? 1.f : 0.f);
+      };
 #pragma unroll
-      for (int i = 0; i < HK; ++i)
-        S[i] = src && active ? src[(size_t)(HK * h + i) * DV + r] : (kind == 1 && HK * h + i == r ? 1.f : 0.f);
+      for (int i = 0; i < HK / 2; ++i) S[i] = make_float2(entry(HK * h + 2 * i), entry(HK * h + 2 * i + 1));
     }
-    const uint32_t col_s = tbase + lane_off + kColS + HK * h;      // hi: HK / 2 columns, then lo
+    const uint32_t col_s = tbase + lane_off + kColS + HK * h;
     const uint32_t col_half = tbase + lane_off + 32 * h;           // + a 64-token region
-    __nv_bfloat16 *o = OUT ? a.o + ((size_t)bh * a.T + t_begin) * DV + r : nullptr;
     bool ok = true;
 
-    // outputs of chunk c: o_t = e^{G_t} (Q S)_t + (P D)_t, 32 tokens a thread
+    // S as the next products' operand, 32 keys at a time: hi, then lo, in the
+    // columns the update of the same keys was read from
+    auto put_state = [&](int b) {
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) split2(S[16 * b + i], hi[i], lo[i]);
+      tmem_st16(col_s + 32 * b, hi);
+      tmem_st16(col_s + 32 * b + 16, lo);
+    };
+    auto state_ready = [&]() {
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&bars[kSReady]);
+    };
+    // outputs of chunk c, o_t = e^{G_t} (Q S)_t + (P D)_t, 32 tokens a thread,
+    // into the places its values of V were read from
     auto outputs = [&](int c) -> bool {
       if (!warp_wait(&bars[kODone], c & 1, abort_flag)) return false;
       tc_fence_after();
       if (active) {
-        const float *fs = gates[c & 1].from_start + 32 * h;
-        __nv_bfloat16 *dst = o + (size_t)(kC * c + 32 * h) * DV;
-        const int left = t_left - (kC * c + 32 * h);
+        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffV + (c & 1) * L::kV) +
+                             32 * h * DV + r;
+        uint32_t x[32];
+        tmem_ld32(col_half + kColO, x);
+        tmem_wait_ld();
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint32_t x[16], y[16];
-          tmem_ld16(col_half + kColQS + 16 * b, x);
-          tmem_ld16(col_half + kColO + 16 * b, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (16 * b + i < left)
-              dst[(size_t)(16 * b + i) * DV] = __float2bfloat16_rn(
-                  fmaf(fs[16 * b + i], __uint_as_float(x[i]), __uint_as_float(y[i])));
-        }
+        for (int i = 0; i < 32; ++i) dst[i * DV] = __float2bfloat16_rn(__uint_as_float(x[i]));
       }
-      tc_fence_before();
-      warp_arrive(&bars[kOFree]);
-      warp_arrive(&bars[kPmEmpty + (c & 1)]);
+      fence_async_smem();
+      warp_arrive(&bars[kOReady]);
       return true;
     };
 
+    if (n > 0) {
+      if (active)
+#pragma unroll
+        for (int b = 0; b < HK / 32; ++b) put_state(b);
+      state_ready();
+    }
     for (int c = 0; c < n; ++c) {
       const int st = c & 1;
-      // S as the next products' operand
-      if (active) {
-#pragma unroll
-        for (int b = 0; b < HK / 32; ++b) {
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) split2(S[32 * b + 2 * i], S[32 * b + 2 * i + 1], hi[i], lo[i]);
-          tmem_st16(col_s + 16 * b, hi);
-          tmem_st16(col_s + HK / 2 + 16 * b, lo);
-        }
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      warp_arrive(&bars[kSReady]);
       if (OUT && c > 0 && !(ok = outputs(c - 1))) break;
 
       // R = V - e^G (K S)
       if (!(ok = warp_wait(&bars[kPmFull + st], (c >> 1) & 1, abort_flag))) break;
       if (values && !(ok = warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag))) break;
-      float R[32];
+      const Gates &gt = gates[c % kGateStages];
+      uint16_t V[32];
       if (active && values) {
-        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + L::kOffV + st * L::kV) +
-                                 32 * h * DV + r;
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + st * L::kV) + 32 * h * DV + r;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) R[i] = __bfloat162float(v[i * DV]);
+        for (int i = 0; i < 32; ++i) V[i] = v[i * DV];
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) R[i] = 0.f;
+        for (int i = 0; i < 32; ++i) V[i] = 0;
       }
-      if (values) warp_arrive(&bars[kVEmpty + st]);
-      const Gates &gt = gates[st];
+      if (!OUT && values) warp_arrive(&bars[kVEmpty + st]);
       if (!(ok = warp_wait(&bars[kKsDone], c & 1, abort_flag))) break;
       tc_fence_after();
       if (active) {
-        uint32_t x[32];
+        uint32_t x[32], hi[16], lo[16];
         tmem_ld32(col_half + kColKS, x);
         tmem_wait_ld();
-        uint32_t hi[16], lo[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 f = *reinterpret_cast<const float2 *>(&gt.from_start[32 * h + 2 * i]);
-          split2(fmaf(-f.x, __uint_as_float(x[2 * i]), R[2 * i]),
-                 fmaf(-f.y, __uint_as_float(x[2 * i + 1]), R[2 * i + 1]), hi[i], lo[i]);
+          const float2 v = as_float2((uint32_t)V[2 * i] << 16, (uint32_t)V[2 * i + 1] << 16);
+          split2(__ffma2_rn(make_float2(-f.x, -f.y), as_float2(x[2 * i], x[2 * i + 1]), v), hi[i], lo[i]);
         }
         tmem_st16(col_half + kColKS, hi);
         tmem_st16(col_half + kColKS + 16, lo);
@@ -240,19 +247,38 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       tc_fence_before();
       warp_arrive(&bars[kRReady]);
+      // e^G (Q S) to where P D is added to it, so that the next chunk's Q S
+      // need not wait for this chunk's outputs
+      if (OUT && active) {
+        uint32_t x[32];
+        tmem_ld32(col_half + kColQS, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = *reinterpret_cast<const float2 *>(&gt.from_start[32 * h + 2 * i]);
+          const float2 y = __fmul2_rn(f, as_float2(x[2 * i], x[2 * i + 1]));
+          x[2 * i] = __float_as_uint(y.x);
+          x[2 * i + 1] = __float_as_uint(y.y);
+        }
+        tmem_st32(col_half + kColO, x);
+        tmem_wait_st();
+      }
 
-      // D: scaled for the update first, as it is for the outputs after
+      // D, from its two accumulators: scaled for the update first, as it is
+      // for the outputs after
       if (!(ok = warp_wait(&bars[kDDone], c & 1, abort_flag))) break;
       tc_fence_after();
-      uint32_t d[32];
+      float2 d[16];
       if (active) {
-        tmem_ld32(col_half + kColD, d);
+        uint32_t x[32], y[32], hi[16], lo[16];
+        tmem_ld32(col_half + kColD, x);
+        tmem_ld32(col_half + kColDl, y);
         tmem_wait_ld();
-        uint32_t hi[16], lo[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 f = *reinterpret_cast<const float2 *>(&gt.to_end[32 * h + 2 * i]);
-          split2(f.x * __uint_as_float(d[2 * i]), f.y * __uint_as_float(d[2 * i + 1]), hi[i], lo[i]);
+          d[i] = __fadd2_rn(as_float2(x[2 * i], x[2 * i + 1]), as_float2(y[2 * i], y[2 * i + 1]));
+          split2(__fmul2_rn(f, d[i]), hi[i], lo[i]);
         }
         tmem_st16(col_half + kColD, hi);
         tmem_st16(col_half + kColD + 16, lo);
@@ -261,35 +287,37 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       tc_fence_before();
       warp_arrive(&bars[kDtReady]);
       const float whole = gt.from_start[kC - 1];
+      warp_arrive(&bars[kGateEmpty + c % kGateStages]);
       if (OUT) {
         if (active) {
           uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            split2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]), hi[i], lo[i]);
+          for (int i = 0; i < 16; ++i) split2(d[i], hi[i], lo[i]);
           tmem_st16(col_half + kColDl, hi);
           tmem_st16(col_half + kColDl + 16, lo);
           tmem_wait_st();
         }
         tc_fence_before();
         warp_arrive(&bars[kDlReady]);
-      } else {
-        warp_arrive(&bars[kPmEmpty + st]);
       }
 
       // S' = e^{G_C} S + K^T D~
       if (!(ok = warp_wait(&bars[kUDone], c & 1, abort_flag))) break;
       tc_fence_after();
       if (active) {
+        const float2 w2 = make_float2(whole, whole);
 #pragma unroll
         for (int b = 0; b < HK / 32; ++b) {
           uint32_t x[32];
           tmem_ld32(col_s + 32 * b, x);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) S[32 * b + i] = fmaf(whole, S[32 * b + i], __uint_as_float(x[i]));
+          for (int i = 0; i < 16; ++i)
+            S[16 * b + i] = __ffma2_rn(w2, S[16 * b + i], as_float2(x[2 * i], x[2 * i + 1]));
+          if (c + 1 < n) put_state(b);
         }
       }
+      if (c + 1 < n) state_ready();
     }
     if (OUT && ok && n > 0) ok = outputs(n - 1);
     if (active && ok) {
@@ -305,27 +333,22 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       if (dst) {
 #pragma unroll
-        for (int i = 0; i < HK; ++i) dst[(size_t)(HK * h + i) * ld + r] = S[i];
+        for (int i = 0; i < HK / 2; ++i) {
+          dst[(size_t)(HK * h + 2 * i) * ld + r] = S[i].x;
+          dst[(size_t)(HK * h + 2 * i + 1) * ld + r] = S[i].y;
+        }
       }
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ M and P, one chunk ahead
+    fewer_registers<kIntraRegs>();
     const int w = warp - 8;
     const int t = 32 * (w & 1) + lane;                     // K row (w < 2) or Q row (w >= 2)
     const uint32_t lane_off = (uint32_t)(32 * w) << 16;
-    const float *gp = a.g + (size_t)bh * a.T + t_begin, *bp = a.beta + (size_t)bh * a.T + t_begin;
-    float gx = 0.f, gy = 0.f, bx = 0.f, by = 0.f;          // the next chunk's gates
-    auto fetch = [&](int c) {
-      const int u = kC * c + 2 * lane;
-      gx = u < t_left ? gp[u] : 0.f;
-      gy = u + 1 < t_left ? gp[u + 1] : 0.f;
-      bx = u < t_left ? bp[u] : 0.f;
-      by = u + 1 < t_left ? bp[u + 1] : 0.f;
-    };
     constexpr uint32_t id_kq = idesc_bf16(128, kC, false, false);
     auto issue_kq = [&](int c) -> bool {                   // [K; Q] K^T of chunk c
       const int st = c % kKqStages;
-      if (!mbar_wait(&bars[kKqFull + st], (c / kKqStages) & 1, abort_flag)) return false;
+      if (!wait_bar(&bars[kKqFull + st], (c / kKqStages) & 1, abort_flag)) return false;
       tc_fence_after();
       const uint32_t kq = smem_u32(smem + L::kOffKq + st * L::kKq);
 #pragma unroll
@@ -337,65 +360,69 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       return true;
     };
     bool ok = true;
-    if (w == 0) fetch(0);
     if (w == 2 && lane == 0 && n > 0) ok = issue_kq(0);
     ok = __all_sync(0xffffffffu, ok);
     // an aborted warp goes on through the group's barriers without work
     for (int c = 0; c < n; ++c) {
       const int st = c & 1;
-      Gates &gt = gates[st];
+      const Gates &gt = gates[c % kGateStages];
       if (ok && c >= 2) ok = warp_wait(&bars[kPmEmpty + st], ((c >> 1) - 1) & 1, abort_flag);
-      if (w == 0) {
-        make_gates(gt, gx, gy, bx, by);
-        if (c + 1 < n) fetch(c + 1);
-      }
-      intra_sync();
+      if (ok) ok = warp_wait(&bars[kGateFull + c % kGateStages], (c / kGateStages) & 1, abort_flag);
       if (ok) ok = warp_wait(&bars[kKkDone], c & 1, abort_flag);
-      if (ok) tc_fence_after();
-      const float hi_t = gt.hi[t], lo_t = gt.lo[t], b_t = gt.beta[t];
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {               // 32 of the 64 columns
-        if (w == 0 ? half == 1 : (w >= 2 && !OUT)) continue;
-        uint32_t x[32];
-        if (ok) {
-          tmem_ld32(tbase + lane_off + kColKQ + 32 * half, x);
+      if (ok) {
+        tc_fence_after();
+        const float hi_t = gt.hi[t], lo_t = gt.lo[t], b_t = gt.beta[t];
+        uint8_t *tile = smem + L::kOffP + st * 2 * kPanel;
+        if (w < 2 || OUT) {
+          uint32_t x[32];
+          float y[8];
+          const int diag = w & 1;                          // the half that holds the row's own block
+          tmem_ld32(tbase + lane_off + kColKQ + 32 * diag, x);
           tmem_wait_ld();
-        }
-        if (w < 2) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const int s = 32 * half + j;
-            float4 l;
-            l.x = s < t ? b_t * decay_ratio(gt, hi_t, lo_t, s) * __uint_as_float(x[j]) : 0.f;
-            l.y = s + 1 < t ? b_t * decay_ratio(gt, hi_t, lo_t, s + 1) * __uint_as_float(x[j + 1]) : 0.f;
-            l.z = s + 2 < t ? b_t * decay_ratio(gt, hi_t, lo_t, s + 2) * __uint_as_float(x[j + 2]) : 0.f;
-            l.w = s + 3 < t ? b_t * decay_ratio(gt, hi_t, lo_t, s + 3) * __uint_as_float(x[j + 3]) : 0.f;
-            *reinterpret_cast<float4 *>(Lm + t * kLs + s) = l;
-          }
-        } else {
-          uint8_t *tile = smem + L::kOffP + st * 2 * kPanel;
+          for (int b = 0; b < 4; ++b) {
+            if (w < 2) {
+              decay8<true, true>(gt, t, hi_t, lo_t, 4 * diag + b, x + 8 * b, y);
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            float p[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int s = 32 * half + 8 * cc + j;
-              p[j] = s <= t ? decay_ratio(gt, hi_t, lo_t, s) * __uint_as_float(x[8 * cc + j]) : 0.f;
+              for (int j = 0; j < 8; ++j)                  // transposed, for the inversion
+                Lm[(32 * diag + 8 * b + j) * kLs + t] = b_t * y[j];
+            } else {
+              decay8<false, true>(gt, t, hi_t, lo_t, 4 * diag + b, x + 8 * b, y);
+              store_split8(tile, tile + kPanel, t, 4 * diag + b, y);
             }
-            store_split8(tile, tile + kPanel, t, 4 * half + cc, p);
+          }
+          if (diag == 1) {
+            tmem_ld32(tbase + lane_off + kColKQ, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              decay8<false, false>(gt, t, hi_t, lo_t, b, x + 8 * b, y);
+              if (w < 2) {
+                float *dst = Lm + t * kLs + 8 * b;
+                *reinterpret_cast<float4 *>(dst) = make_float4(b_t * y[0], b_t * y[1], b_t * y[2], b_t * y[3]);
+                *reinterpret_cast<float4 *>(dst + 4) = make_float4(b_t * y[4], b_t * y[5], b_t * y[6], b_t * y[7]);
+              } else {
+                store_split8(tile, tile + kPanel, t, b, y);
+              }
+            }
+          } else if (w == 2) {
+#pragma unroll
+            for (int b = 4; b < 8; ++b) {
+              *reinterpret_cast<uint4 *>(tile + sw128(t, b)) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4 *>(tile + kPanel + sw128(t, b)) = make_uint4(0, 0, 0, 0);
+            }
           }
         }
+        __syncwarp();
+        if (w < 2) invert_diagonal(Lm, w);
       }
       tc_fence_before();
-      intra_sync();                                        // the products have been read
-      if (w < 2) {
-        invert_diagonal(Lm, w);
-      } else if (w == 2 && c + 1 < n) {
+      intra_sync();                                        // the products are read, the blocks inverted
+      if (w == 2 && c + 1 < n) {
         bool sent = true;
         if (ok && lane == 0) sent = issue_kq(c + 1);
         ok = __all_sync(0xffffffffu, sent) && ok;
       }
-      intra_sync();
       invert_corner(Lm);
       uint8_t *tile = smem + L::kOffM + st * 2 * kPanel;
       store_inverse<true>(Lm, gt, tile, tile + kPanel);
@@ -407,70 +434,66 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       mma_commit(&bars[kEnd2]);
       drain(&bars[kEnd2], 0);
     }
-  } else if (warp == 12) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_n = idesc_bf16(128, kC, false, false);   // K-major right operand
-      constexpr uint32_t id_mn = idesc_bf16(128, 64, false, true);   // MN-major
+  } else {
+    fewer_registers<kHelperRegs>();
+    if (warp == 12 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_64 = idesc_bf16(128, 64, false, false);    // K-major right operand
+      constexpr uint32_t id_128 = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t id_up = idesc_bf16(128, DK, false, true);     // MN-major
       bool ok = true;
-      // D[64 columns] = (hi + lo of a 64-token operand) (hi + lo tile), lo lo left out
-      auto product64 = [&](uint32_t dst, uint32_t op, uint32_t tile) {
-        bool first = true;
-#pragma unroll
-        for (int pass = 0; pass < 3; ++pass)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t col = op + 32 * (k / 2) + 8 * (k % 2) + (pass == 2 ? 16 : 0);
-            mma_ts(dst, col, smem_desc(tile + (pass == 1 ? kPanel : 0) + 32 * k, 16, 1024, kSw128), id_n,
-                   !first);
-            first = false;
-          }
-      };
-      // D[64 tokens] = S^T (hi + lo) times the rows of a K or Q tile
-      auto with_state = [&](uint32_t dst, uint32_t rows) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int k = 0; k < DK / 16; ++k) {
-            constexpr int HK = DK / 2, KH = HK / 16;       // 16-key steps a warpgroup's half
-            const uint32_t col = tbase + kColS + HK * (k / KH) + 8 * (k % KH) + (half ? HK / 2 : 0);
-            mma_ts(dst, col, smem_desc(rows + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128), id_n,
-                   half > 0 || k > 0);
-          }
-      };
+      // operands in tensor memory, blocks of 32 (hi, then lo): columns of 16-deep step k
+      auto step_col = [&](uint32_t op, int k, int lo) { return op + 32 * (k / 2) + 8 * (k % 2) + 16 * lo; };
       for (int c = 0; c < n && ok; ++c) {
         const int st = c & 1, ks = c % kKqStages;
         const uint32_t kq = smem_u32(smem + L::kOffKq + ks * L::kKq);
-        if (!(ok = mbar_wait(&bars[kKqFull + ks], (c / kKqStages) & 1, abort_flag))) break;
-        if (!(ok = mbar_wait(&bars[kSReady], c & 1, abort_flag))) break;
+        if (!(ok = wait_bar(&bars[kKqFull + ks], (c / kKqStages) & 1, abort_flag))) break;
+        if (!(ok = wait_bar(&bars[kSReady], c & 1, abort_flag))) break;
         tc_fence_after();
-        with_state(tbase + kColKS, kq);
-        mma_commit(&bars[kKsDone]);
-        if (OUT) {
-          if (c > 0 && !(ok = mbar_wait(&bars[kOFree], (c - 1) & 1, abort_flag))) break;
-          tc_fence_after();
-          with_state(tbase + kColQS, kq + kPanel);
+        {
+          // [K; Q] S (!OUT: K S): S^T hi and lo against the K and Q rows
+#pragma unroll
+          for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k)
+              mma_ts(tbase + kColKS, step_col(tbase + kColS, k, lo),
+                     smem_desc(kq + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128),
+                     OUT ? id_128 : id_64, lo > 0 || k > 0);
+          mma_commit(&bars[kKsDone]);
         }
-        if (!(ok = mbar_wait(&bars[kPmFull + st], (c >> 1) & 1, abort_flag))) break;
-        if (!(ok = mbar_wait(&bars[kRReady], c & 1, abort_flag))) break;
+        if (!(ok = wait_bar(&bars[kPmFull + st], (c >> 1) & 1, abort_flag))) break;
+        if (!(ok = wait_bar(&bars[kRReady], c & 1, abort_flag))) break;
         tc_fence_after();
-        product64(tbase + kColD, tbase + kColKS, smem_u32(smem + L::kOffM + st * 2 * kPanel));
-        mma_commit(&bars[kDDone]);
-        if (!(ok = mbar_wait(&bars[kDtReady], c & 1, abort_flag))) break;
+        {
+          // R^T hi against [M hi; M lo] (two accumulators), R^T lo against M hi
+          const uint32_t m = smem_u32(smem + L::kOffM + st * 2 * kPanel);
+#pragma unroll
+          for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tbase + kColD, step_col(tbase + kColKS, k, lo), smem_desc(m + 32 * k, 16, 1024, kSw128),
+                     lo ? id_64 : id_128, lo > 0 || k > 0);
+          mma_commit(&bars[kDDone]);
+        }
+        if (!(ok = wait_bar(&bars[kDtReady], c & 1, abort_flag))) break;
         tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-              mma_ts(tbase + kColS + 64 * p, tbase + kColD + 32 * (k / 2) + 8 * (k % 2) + 16 * half,
-                     smem_desc(kq + p * 2 * kPanel + k * 2048, 16384, 1024, kSw128), id_mn, half > 0 || k > 0);
+            mma_ts(tbase + kColS, step_col(tbase + kColD, k, lo),
+                   smem_desc(kq + k * 2048, 2 * kPanel, 1024, kSw128), id_up, lo > 0 || k > 0);
         mma_commit(&bars[kUDone]);
         if (OUT) {
-          if (!(ok = mbar_wait(&bars[kDlReady], c & 1, abort_flag))) break;
+          if (!(ok = wait_bar(&bars[kDlReady], c & 1, abort_flag))) break;
           tc_fence_after();
-          product64(tbase + kColO, tbase + kColDl, smem_u32(smem + L::kOffP + st * 2 * kPanel));
+          const uint32_t p = smem_u32(smem + L::kOffP + st * 2 * kPanel);
+#pragma unroll
+          for (int pass = 0; pass < 3; ++pass)             // += D P: hi hi, hi lo, lo hi
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tbase + kColO, step_col(tbase + kColDl, k, pass == 2),
+                     smem_desc(p + (pass == 1 ? kPanel : 0) + 32 * k, 16, 1024, kSw128), id_64, 1);
           mma_commit(&bars[kODone]);
         }
         mma_commit(&bars[kKqEmpty + ks]);
@@ -480,20 +503,15 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         mma_commit(&bars[kEnd]);
         drain(&bars[kEnd], 0);
       }
-    }
-  } else {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    } else if (warp == 13 && lane == 0) {
+      // ---------------------------------------------------------- TMA loads
       tma_prefetch_desc(&tmk);
       if (OUT) tma_prefetch_desc(&tmq);
       if (values) tma_prefetch_desc(&tmv);
-      bool ok = true;
       int kq_sent = 0, v_sent = 0;
       for (int c = 0; c < n; ++c) {
         const int ks = c % kKqStages, vs = c & 1, row = t_begin + kC * c;
-        if (c >= kKqStages &&
-            !(ok = mbar_wait(&bars[kKqEmpty + ks], ((c / kKqStages) - 1) & 1, abort_flag)))
-          break;
+        if (c >= kKqStages && !wait_bar(&bars[kKqEmpty + ks], ((c / kKqStages) - 1) & 1, abort_flag)) break;
         uint8_t *kq = smem + L::kOffKq + ks * L::kKq;
         mbar_arrive_expect_tx(&bars[kKqFull + ks], OUT ? L::kKq : L::kKq / 2);
 #pragma unroll
@@ -503,7 +521,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         }
         kq_sent = c + 1;
         if (values) {
-          if (c >= 2 && !(ok = mbar_wait(&bars[kVEmpty + vs], ((c >> 1) - 1) & 1, abort_flag))) break;
+          if (c >= 2 && !wait_bar(&bars[kVEmpty + vs], ((c >> 1) - 1) & 1, abort_flag)) break;
           mbar_arrive_expect_tx(&bars[kVFull + vs], L::kV);
           tma_load_3d(smem + L::kOffV + vs * L::kV, &tmv, &bars[kVFull + vs], 0, row, bh);
           v_sent = c + 1;
@@ -514,6 +532,39 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           drain(&bars[kKqFull + c % kKqStages], (c / kKqStages) & 1);
         for (int c = v_sent > 2 ? v_sent - 2 : 0; c < v_sent; ++c)
           drain(&bars[kVFull + (c & 1)], (c >> 1) & 1);
+      }
+    } else if (OUT && warp == 14 && lane == 0) {
+      // ---------------------------------------------------------- output stores
+      tma_prefetch_desc(&tmo);
+      for (int c = 0; c < n; ++c) {
+        if (!wait_bar(&bars[kOReady], c & 1, abort_flag)) break;
+        tma_store_3d(&tmo, smem + L::kOffV + (c & 1) * L::kV, 0, t_begin + kC * c, bh);
+        bulk_commit_group();
+        bulk_wait_read_all();
+        mbar_arrive(&bars[kVEmpty + (c & 1)]);
+      }
+      bulk_wait_all();
+    } else if (warp == 15) {
+      // ---------------------------------------------------------- gates
+      const float *gp = a.g + (size_t)bh * a.T + t_begin, *bp = a.beta + (size_t)bh * a.T + t_begin;
+      float gx = 0.f, gy = 0.f, bx = 0.f, by = 0.f;
+      auto fetch = [&](int c) {
+        const int u = kC * c + 2 * lane;
+        gx = u < t_left ? gp[u] : 0.f;
+        gy = u + 1 < t_left ? gp[u + 1] : 0.f;
+        bx = u < t_left ? bp[u] : 0.f;
+        by = u + 1 < t_left ? bp[u + 1] : 0.f;
+      };
+      if (n > 0) fetch(0);
+      for (int c = 0; c < n; ++c) {
+        const int gs = c % kGateStages;
+        if (c >= kGateStages &&
+            !warp_wait(&bars[kGateEmpty + gs], ((c / kGateStages) - 1) & 1, abort_flag))
+          break;
+        const float x = gx, y = gy, bx0 = bx, by0 = by;
+        if (c + 1 < n) fetch(c + 1);                       // in flight during this chunk's
+        make_gates(gates[gs], x, y, bx0, by0);
+        warp_arrive(&bars[kGateFull + gs]);
       }
     }
   }
@@ -570,13 +621,14 @@ gd_join_kernel(const float *__restrict__ F, const float *__restrict__ B, const f
 template <int DK, int DV>
 cudaError_t launch(const GatedDeltaLaunch &a) {
   using L = Layout<DK, DV>;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   const long long BHk = a.BH / a.H * a.Hk;
   if (!make_tma_3d_bf16_box(&tq, a.q, DK, a.T, BHk, 64, kC, true) ||
       !make_tma_3d_bf16_box(&tk, a.k, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tv, a.v, DV, a.T, a.BH, DV, kC, false))
+      !make_tma_3d_bf16_box(&tv, a.v, DV, a.T, a.BH, DV, kC, false) ||
+      !make_tma_3d_bf16_box(&to, a.o, DV, a.T, a.BH, DV, kC, false))
     return cudaErrorInvalidValue;
-  Args x{a.g, a.beta, a.S0, static_cast<__nv_bfloat16 *>(a.o), a.S_out, a.F, a.B, a.seg_starts,
+  Args x{a.g, a.beta, a.S0, a.S_out, a.F, a.B, a.seg_starts,
          a.status, a.H, a.Hk, a.T, a.G, a.seg_chunks};
   if (a.G > 1) {
     auto kern = gd_tc_kernel<DK, DV, false>;
@@ -584,7 +636,7 @@ cudaError_t launch(const GatedDeltaLaunch &a) {
     if (e != cudaSuccess) return e;
     {
       ProfileScope prof("gd_tc_segment", a.stream);
-      kern<<<(unsigned)(a.BH * (a.G - 1) * 2), kThreads, L::kBytes, a.stream>>>(tq, tk, tv, x);
+      kern<<<(unsigned)(a.BH * (a.G - 1) * 2), kThreads, L::kBytes, a.stream>>>(tq, tk, tv, to, x);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ProfileScope prof("gd_join", a.stream);
@@ -596,7 +648,7 @@ cudaError_t launch(const GatedDeltaLaunch &a) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   ProfileScope prof("gd_tc_forward", a.stream);
-  kern<<<(unsigned)(a.BH * a.G), kThreads, L::kBytes, a.stream>>>(tq, tk, tv, x);
+  kern<<<(unsigned)(a.BH * a.G), kThreads, L::kBytes, a.stream>>>(tq, tk, tv, to, x);
   return cudaGetLastError();
 }
 
