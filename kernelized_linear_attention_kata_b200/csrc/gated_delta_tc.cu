@@ -172,15 +172,14 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     const uint32_t col_half = tbase + lane_off + 32 * h;           // + a 64-token region
     bool ok = true;
 
-    // S as the next products' operand, 32 keys at a time: hi, then lo, in the
-    // columns the update of the same keys was read from
-    auto put_state = [&](int b) {
-      uint32_t hi[16], lo[16];
+    // 32 values of a row as an operand, in 16-deep steps of hi, then lo
+    auto put32 = [&](uint32_t col, const float2 *x) {
+      uint32_t y[32];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) split2(S[16 * b + i], hi[i], lo[i]);
-      tmem_st16(col_s + 32 * b, hi);
-      tmem_st16(col_s + 32 * b + 16, lo);
+      for (int i = 0; i < 16; ++i) split2(x[i], y[16 * (i / 8) + i % 8], y[16 * (i / 8) + 8 + i % 8]);
+      tmem_st32(col, y);
     };
+    auto gate4 = [](const float *g, int i) { return *reinterpret_cast<const float4 *>(g + i); };
     auto state_ready = [&]() {
       tmem_wait_st();
       tc_fence_before();
@@ -208,7 +207,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     if (n > 0) {
       if (active)
 #pragma unroll
-        for (int b = 0; b < HK / 32; ++b) put_state(b);
+        for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
       state_ready();
     }
     for (int c = 0; c < n; ++c) {
@@ -219,30 +218,30 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       if (!(ok = warp_wait(&bars[kPmFull + st], (c >> 1) & 1, abort_flag))) break;
       if (values && !(ok = warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag))) break;
       const Gates &gt = gates[c % kGateStages];
-      uint16_t V[32];
-      if (active && values) {
+      uint32_t V[16];                                      // two tokens a register
+      {
         const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + st * L::kV) + 32 * h * DV + r;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) V[i] = v[i * DV];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) V[i] = 0;
+        for (int i = 0; i < 16; ++i)
+          V[i] = active && values ? (uint32_t)v[2 * i * DV] | (uint32_t)v[(2 * i + 1) * DV] << 16 : 0u;
       }
       if (!OUT && values) warp_arrive(&bars[kVEmpty + st]);
       if (!(ok = warp_wait(&bars[kKsDone], c & 1, abort_flag))) break;
       tc_fence_after();
       if (active) {
-        uint32_t x[32], hi[16], lo[16];
+        uint32_t x[32];
+        float2 y[16];
         tmem_ld32(col_half + kColKS, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 f = *reinterpret_cast<const float2 *>(&gt.from_start[32 * h + 2 * i]);
-          const float2 v = as_float2((uint32_t)V[2 * i] << 16, (uint32_t)V[2 * i + 1] << 16);
-          split2(__ffma2_rn(make_float2(-f.x, -f.y), as_float2(x[2 * i], x[2 * i + 1]), v), hi[i], lo[i]);
+        for (int i = 0; i < 16; i += 2) {
+          const float4 f = gate4(gt.from_start, 32 * h + 2 * i);
+          y[i] = __ffma2_rn(make_float2(-f.x, -f.y), as_float2(x[2 * i], x[2 * i + 1]),
+                            as_float2(V[i] << 16, V[i] & 0xffff0000u));
+          y[i + 1] = __ffma2_rn(make_float2(-f.z, -f.w), as_float2(x[2 * i + 2], x[2 * i + 3]),
+                                as_float2(V[i + 1] << 16, V[i + 1] & 0xffff0000u));
         }
-        tmem_st16(col_half + kColKS, hi);
-        tmem_st16(col_half + kColKS + 16, lo);
+        put32(col_half + kColKS, y);
         tmem_wait_st();
       }
       tc_fence_before();
@@ -254,11 +253,12 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_ld32(col_half + kColQS, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 f = *reinterpret_cast<const float2 *>(&gt.from_start[32 * h + 2 * i]);
-          const float2 y = __fmul2_rn(f, as_float2(x[2 * i], x[2 * i + 1]));
-          x[2 * i] = __float_as_uint(y.x);
-          x[2 * i + 1] = __float_as_uint(y.y);
+        for (int i = 0; i < 32; i += 4) {
+          const float4 f = gate4(gt.from_start, 32 * h + i);
+          x[i] = __float_as_uint(f.x * __uint_as_float(x[i]));
+          x[i + 1] = __float_as_uint(f.y * __uint_as_float(x[i + 1]));
+          x[i + 2] = __float_as_uint(f.z * __uint_as_float(x[i + 2]));
+          x[i + 3] = __float_as_uint(f.w * __uint_as_float(x[i + 3]));
         }
         tmem_st32(col_half + kColO, x);
         tmem_wait_st();
@@ -270,18 +270,20 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       tc_fence_after();
       float2 d[16];
       if (active) {
-        uint32_t x[32], y[32], hi[16], lo[16];
+        uint32_t x[32], y[32];
+        float2 z[16];
         tmem_ld32(col_half + kColD, x);
         tmem_ld32(col_half + kColDl, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 f = *reinterpret_cast<const float2 *>(&gt.to_end[32 * h + 2 * i]);
+        for (int i = 0; i < 16; i += 2) {
+          const float4 f = gate4(gt.to_end, 32 * h + 2 * i);
           d[i] = __fadd2_rn(as_float2(x[2 * i], x[2 * i + 1]), as_float2(y[2 * i], y[2 * i + 1]));
-          split2(__fmul2_rn(f, d[i]), hi[i], lo[i]);
+          d[i + 1] = __fadd2_rn(as_float2(x[2 * i + 2], x[2 * i + 3]), as_float2(y[2 * i + 2], y[2 * i + 3]));
+          z[i] = __fmul2_rn(make_float2(f.x, f.y), d[i]);
+          z[i + 1] = __fmul2_rn(make_float2(f.z, f.w), d[i + 1]);
         }
-        tmem_st16(col_half + kColD, hi);
-        tmem_st16(col_half + kColD + 16, lo);
+        put32(col_half + kColD, z);
         tmem_wait_st();
       }
       tc_fence_before();
@@ -290,11 +292,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       warp_arrive(&bars[kGateEmpty + c % kGateStages]);
       if (OUT) {
         if (active) {
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) split2(d[i], hi[i], lo[i]);
-          tmem_st16(col_half + kColDl, hi);
-          tmem_st16(col_half + kColDl + 16, lo);
+          put32(col_half + kColDl, d);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -306,15 +304,16 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       tc_fence_after();
       if (active) {
         const float2 w2 = make_float2(whole, whole);
+        uint32_t x[HK];
 #pragma unroll
-        for (int b = 0; b < HK / 32; ++b) {
-          uint32_t x[32];
-          tmem_ld32(col_s + 32 * b, x);
-          tmem_wait_ld();
+        for (int b = 0; b < HK / 32; ++b)
+          tmem_ld32(col_s + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * b));
+        tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            S[16 * b + i] = __ffma2_rn(w2, S[16 * b + i], as_float2(x[2 * i], x[2 * i + 1]));
-          if (c + 1 < n) put_state(b);
+        for (int i = 0; i < HK / 2; ++i) S[i] = __ffma2_rn(w2, S[i], as_float2(x[2 * i], x[2 * i + 1]));
+        if (c + 1 < n) {
+#pragma unroll
+          for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
         }
       }
       if (c + 1 < n) state_ready();
@@ -351,7 +350,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       if (!wait_bar(&bars[kKqFull + st], (c / kKqStages) & 1, abort_flag)) return false;
       tc_fence_after();
       const uint32_t kq = smem_u32(smem + L::kOffKq + st * L::kKq);
-#pragma unroll
+#pragma unroll 2
       for (int k = 0; k < DK / 16; ++k) {
         const uint64_t desc = smem_desc(kq + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128);
         mma_ss(tbase + kColKQ, desc, desc, id_kq, k > 0);
@@ -371,23 +370,23 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       if (ok) ok = warp_wait(&bars[kKkDone], c & 1, abort_flag);
       if (ok) {
         tc_fence_after();
-        const float hi_t = gt.hi[t], lo_t = gt.lo[t], b_t = gt.beta[t];
         uint8_t *tile = smem + L::kOffP + st * 2 * kPanel;
+        const int diag = w & 1;                            // the half that holds the row's own block
         if (w < 2 || OUT) {
           uint32_t x[32];
-          float y[8];
-          const int diag = w & 1;                          // the half that holds the row's own block
           tmem_ld32(tbase + lane_off + kColKQ + 32 * diag, x);
+          const RowDecay d = row_decay(gt, t, w < 2);
+          const float b_t = gt.beta[t];
           tmem_wait_ld();
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
+            float y[8];
+            decay8(gt, d, 4 * diag + b, false, x + 8 * b, y);
             if (w < 2) {
-              decay8<true, true>(gt, t, hi_t, lo_t, 4 * diag + b, x + 8 * b, y);
 #pragma unroll
               for (int j = 0; j < 8; ++j)                  // transposed, for the inversion
                 Lm[(32 * diag + 8 * b + j) * kLs + t] = b_t * y[j];
             } else {
-              decay8<false, true>(gt, t, hi_t, lo_t, 4 * diag + b, x + 8 * b, y);
               store_split8(tile, tile + kPanel, t, 4 * diag + b, y);
             }
           }
@@ -396,7 +395,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             tmem_wait_ld();
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-              decay8<false, false>(gt, t, hi_t, lo_t, b, x + 8 * b, y);
+              float y[8];
+              decay8(gt, d, b, true, x + 8 * b, y);
               if (w < 2) {
                 float *dst = Lm + t * kLs + 8 * b;
                 *reinterpret_cast<float4 *>(dst) = make_float4(b_t * y[0], b_t * y[1], b_t * y[2], b_t * y[3]);
@@ -405,7 +405,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 store_split8(tile, tile + kPanel, t, b, y);
               }
             }
-          } else if (w == 2) {
+          } else if (w == 2) {                             // tokens behind every row of the warp
 #pragma unroll
             for (int b = 4; b < 8; ++b) {
               *reinterpret_cast<uint4 *>(tile + sw128(t, b)) = make_uint4(0, 0, 0, 0);
@@ -414,7 +414,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           }
         }
         __syncwarp();
-        if (w < 2) invert_diagonal(Lm, w);
+        if (w < 2) invert_diagonal(Lm + 32 * w * (kLs + 1));
       }
       tc_fence_before();
       intra_sync();                                        // the products are read, the blocks inverted
@@ -442,8 +442,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       constexpr uint32_t id_128 = idesc_bf16(128, 128, false, false);
       constexpr uint32_t id_up = idesc_bf16(128, DK, false, true);     // MN-major
       bool ok = true;
-      // operands in tensor memory, blocks of 32 (hi, then lo): columns of 16-deep step k
-      auto step_col = [&](uint32_t op, int k, int lo) { return op + 32 * (k / 2) + 8 * (k % 2) + 16 * lo; };
+      // operands in tensor memory: columns of the 16-deep step k, hi or lo
+      auto step_col = [&](uint32_t op, int k, int lo) { return op + 16 * k + 8 * lo; };
       for (int c = 0; c < n && ok; ++c) {
         const int st = c & 1, ks = c % kKqStages;
         const uint32_t kq = smem_u32(smem + L::kOffKq + ks * L::kKq);
@@ -452,9 +452,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tc_fence_after();
         {
           // [K; Q] S (!OUT: K S): S^T hi and lo against the K and Q rows
-#pragma unroll
+#pragma unroll 1
           for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < DK / 16; ++k)
               mma_ts(tbase + kColKS, step_col(tbase + kColS, k, lo),
                      smem_desc(kq + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128),
@@ -467,9 +467,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         {
           // R^T hi against [M hi; M lo] (two accumulators), R^T lo against M hi
           const uint32_t m = smem_u32(smem + L::kOffM + st * 2 * kPanel);
-#pragma unroll
+#pragma unroll 1
           for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < 4; ++k)
               mma_ts(tbase + kColD, step_col(tbase + kColKS, k, lo), smem_desc(m + 32 * k, 16, 1024, kSw128),
                      lo ? id_64 : id_128, lo > 0 || k > 0);
@@ -477,9 +477,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         }
         if (!(ok = wait_bar(&bars[kDtReady], c & 1, abort_flag))) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
+#pragma unroll 2
           for (int k = 0; k < 4; ++k)
             mma_ts(tbase + kColS, step_col(tbase + kColD, k, lo),
                    smem_desc(kq + k * 2048, 2 * kPanel, 1024, kSw128), id_up, lo > 0 || k > 0);
@@ -488,9 +488,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           if (!(ok = wait_bar(&bars[kDlReady], c & 1, abort_flag))) break;
           tc_fence_after();
           const uint32_t p = smem_u32(smem + L::kOffP + st * 2 * kPanel);
-#pragma unroll
+#pragma unroll 1
           for (int pass = 0; pass < 3; ++pass)             // += D P: hi hi, hi lo, lo hi
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < 4; ++k)
               mma_ts(tbase + kColO, step_col(tbase + kColDl, k, pass == 2),
                      smem_desc(p + (pass == 1 ? kPanel : 0) + 32 * k, 16, 1024, kSw128), id_64, 1);

@@ -83,9 +83,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float decay_ratio(const Gates &g, float hi_t, float lo_t, int s) {
-  return exp2_fast((hi_t - g.hi[s]) + (lo_t - g.lo[s]));
-}
 
 // Gates of one chunk by one warp, two tokens a lane; gx, gy are their log decays.
 __device__ __forceinline__ void make_gates(Gates &s, float gx, float gy, float bx, float by) {
@@ -114,28 +111,37 @@ __device__ __forceinline__ void make_gates(Gates &s, float gx, float gy, float b
   }
 }
 
-// Row t, columns s = 8 block .. 8 block + 7 of the causal decay matrix times
-// x: e^{G_t - G_s} x_s for s <= t (STRICT: s < t), else 0. `same`: the row may
-// lie in this block or before it.
-template <bool STRICT, bool SAME>
-__device__ __forceinline__ void decay8(const Gates &g, int t, float hi_t, float lo_t, int block,
+// A row's part in the causal decay matrix: w[j] = e^{G_t - G_s} for the eight
+// tokens s of its own block, 0 behind the row (skip = 1: and on the diagonal).
+struct RowDecay {
+  float hi, lo, own[8];
+  int block;
+};
+__device__ __forceinline__ RowDecay row_decay(const Gates &g, int t, int skip) {
+  RowDecay d;
+  d.hi = g.hi[t];
+  d.lo = g.lo[t];
+  d.block = t / 8;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float w = exp2_fast((d.hi - g.hi[t / 8 * 8 + j]) + (d.lo - g.lo[t / 8 * 8 + j]));
+    d.own[j] = j + skip <= t % 8 ? w : 0.f;
+  }
+  return d;
+}
+// Columns 8 block .. 8 block + 7 of the row times x. `before`: the block lies
+// before every row of the warp.
+__device__ __forceinline__ void decay8(const Gates &g, const RowDecay &d, int block, bool before,
                                        const uint32_t *x, float (&out)[8]) {
-  const int rel = t / 8 - block;
-  const float f = decay_ratio(g, hi_t, lo_t, 8 * block + 7);
+  const float f = exp2_fast((d.hi - g.hi[8 * block + 7]) + (d.lo - g.lo[8 * block + 7]));
   const float4 e0 = *reinterpret_cast<const float4 *>(&g.to_block[8 * block]);
   const float4 e1 = *reinterpret_cast<const float4 *>(&g.to_block[8 * block + 4]);
   const float e[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int s = 8 * block + j;
     float w = f * e[j];
-    if (SAME) {
-      const bool seen = STRICT ? s < t : s <= t;
-      w = rel > 0 ? w : decay_ratio(g, hi_t, lo_t, s);
-      out[j] = seen ? w * __uint_as_float(x[j]) : 0.f;
-    } else {
-      out[j] = w * __uint_as_float(x[j]);
-    }
+    if (!before) w = block < d.block ? w : (block == d.block ? d.own[j] : 0.f);
+    out[j] = w * __uint_as_float(x[j]);
   }
 }
 
@@ -151,66 +157,104 @@ template <int R> __device__ __forceinline__ void fewer_registers() {
 // the eight state warps). Its callers reach it in every round, aborted or not.
 __device__ __forceinline__ void intra_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// (I + L)^-1 by blocks of 32, four warps, in `Lm` (row stride kLs):
+// (I + L)^-1 of a chunk, in `Lm` (row stride kLs), by blocks of 16, 32, 64:
 //   [[A, 0], [X, B]]^-1 = [[A', 0], [-B' X A', B']].
-// Warp w < 2 inverts diagonal block w, given transposed: lane j solves column
-// j in registers, and once x_s is known every later x_t takes its term (496
-// independent multiply-adds a lane, a dependent chain of 32). Its own rows of
-// L are all it reads, so only the warp has to have written them. Forward
-// substitution and block products are as stable as the triangular solve
-// itself, where repeated squaring of L would not be (powers of L grow with
-// repeated keys).
-__device__ __forceinline__ void invert_diagonal(float *Lm, int w) {
-  const int lane = threadIdx.x % 32;
-  float *blk = Lm + (32 * w) * kLs + 32 * w;
-  float2 x[16];
+// The 16-blocks by forward substitution, the products on the warp's tensor
+// instructions in three TF32 products an fp32 pair (x = hi + lo up to 2^-22):
+// on the CUDA cores every operand of these small products would be a shared-
+// memory broadcast, which fills the 128 B/cycle return path with one value.
+// Block substitution is as stable as the triangular solve itself, where
+// repeated squaring of L would not be (powers of L grow with repeated keys).
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// acc (16 x 16, two n-tiles) = A (16 x K) B (K x 16) by one warp; element (r,
+// k) of A at A[r * ra + k * ca], B and the result in rows of kLs.
+template <int K>
+__device__ __forceinline__ void product16(const float *A, int ra, int ca, const float *B, float (&acc)[2][4]) {
+  const int g = threadIdx.x % 32 / 4, t = threadIdx.x % 4;
 #pragma unroll
-  for (int t = 0; t < 16; ++t) x[t] = make_float2(2 * t == lane ? 1.f : 0.f, 2 * t + 1 == lane ? 1.f : 0.f);
+  for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
 #pragma unroll
-  for (int s = 0; s < 31; ++s) {
+  for (int k = 0; k < K; k += 8) {
+    uint32_t ah[4], al[4], bh[2][2], bl[2][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      split_tf32(A[(g + 8 * (i & 1)) * ra + (k + t + 4 * (i >> 1)) * ca], ah[i], al[i]);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_tf32(B[(k + t + 4 * i) * kLs + 8 * n + g], bh[n][i], bl[n][i]);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      mma_tf32(acc[n], ah, bh[n]);
+      mma_tf32(acc[n], ah, bl[n]);
+      mma_tf32(acc[n], al, bh[n]);
+    }
+  }
+}
+__device__ __forceinline__ void store16(float *out, const float (&acc)[2][4], float sign) {
+  const int g = threadIdx.x % 32 / 4, t = threadIdx.x % 4;
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    *reinterpret_cast<float2 *>(out + g * kLs + 8 * n + 2 * t) = make_float2(sign * acc[n][0], sign * acc[n][1]);
+    *reinterpret_cast<float2 *>(out + (g + 8) * kLs + 8 * n + 2 * t) =
+        make_float2(sign * acc[n][2], sign * acc[n][3]);
+  }
+}
+// One warp inverts a 32-block given transposed (entry (t, s) of L at [s][t]):
+// a half warp a 16-block, lane j its column j; once x_s is known every later
+// x_t takes its term. Its own rows of L are all it reads.
+__device__ __forceinline__ void invert_diagonal(float *blk) {
+  const int lane = threadIdx.x % 32, half = lane / 16, j = lane % 16;
+  float *sub = blk + 16 * half * (kLs + 1);
+  float2 x[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) x[t] = make_float2(2 * t == j ? 1.f : 0.f, 2 * t + 1 == j ? 1.f : 0.f);
+#pragma unroll
+  for (int s = 0; s < 15; ++s) {
     const float xs = s % 2 ? -x[s / 2].y : -x[s / 2].x;
     const float2 m = make_float2(xs, xs);
 #pragma unroll
-    for (int t = (s + 1) / 4 * 4; t < 32; t += 4) {        // entries t <= s are zero
-      const float4 l = *reinterpret_cast<const float4 *>(blk + s * kLs + t);
+    for (int t = (s + 1) / 4 * 4; t < 16; t += 4) {        // entries t <= s are zero
+      const float4 l = *reinterpret_cast<const float4 *>(sub + s * kLs + t);
       x[t / 2] = __ffma2_rn(make_float2(l.x, l.y), m, x[t / 2]);
       x[t / 2 + 1] = __ffma2_rn(make_float2(l.z, l.w), m, x[t / 2 + 1]);
     }
   }
   __syncwarp();
 #pragma unroll
-  for (int t = 0; t < 32; ++t) blk[t * kLs + lane] = t % 2 ? x[t / 2].y : x[t / 2].x;
+  for (int t = 0; t < 16; ++t) sub[t * kLs + j] = t % 2 ? x[t / 2].y : x[t / 2].x;
+  __syncwarp();
+  float acc[2][4];
+  product16<16>(blk + 16, 1, kLs, blk, acc);               // X A', X transposed in the upper right
+  store16(blk + 16 * kLs, acc, 1.f);
+  __syncwarp();
+  product16<16>(blk + 16 * (kLs + 1), kLs, 1, blk + 16 * kLs, acc);
+  __syncwarp();
+  store16(blk + 16 * kLs, acc, -1.f);
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  *reinterpret_cast<float4 *>(blk + j * kLs + 16 + 8 * half) = zero;
+  *reinterpret_cast<float4 *>(blk + j * kLs + 20 + 8 * half) = zero;
 }
-// 32 x 32 x 32 product by 128 threads: out = sign * A B (all row stride kLs).
-__device__ __forceinline__ void block_product(const float *A, const float *B, float *out, float sign) {
-  const int i = threadIdx.x % 128, r = 2 * (i / 8), c = 4 * (i % 8);
-  float acc[2][4] = {};
-#pragma unroll
-  for (int u = 0; u < 32; u += 4) {
-    const float4 a0 = *reinterpret_cast<const float4 *>(A + r * kLs + u);
-    const float4 a1 = *reinterpret_cast<const float4 *>(A + (r + 1) * kLs + u);
-    const float l0[4] = {a0.x, a0.y, a0.z, a0.w}, l1[4] = {a1.x, a1.y, a1.z, a1.w};
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float4 b = *reinterpret_cast<const float4 *>(B + (u + v) * kLs + c);
-      acc[0][0] = fmaf(l0[v], b.x, acc[0][0]); acc[0][1] = fmaf(l0[v], b.y, acc[0][1]);
-      acc[0][2] = fmaf(l0[v], b.z, acc[0][2]); acc[0][3] = fmaf(l0[v], b.w, acc[0][3]);
-      acc[1][0] = fmaf(l1[v], b.x, acc[1][0]); acc[1][1] = fmaf(l1[v], b.y, acc[1][1]);
-      acc[1][2] = fmaf(l1[v], b.z, acc[1][2]); acc[1][3] = fmaf(l1[v], b.w, acc[1][3]);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    *reinterpret_cast<float4 *>(out + (r + k) * kLs + c) =
-        make_float4(sign * acc[k][0], sign * acc[k][1], sign * acc[k][2], sign * acc[k][3]);
-}
-// After both diagonal blocks (and a barrier): the lower left block. The upper
-// right block, zero in L, holds the product in between.
+// After both 32-blocks (and a barrier): the lower left one, by four warps, X A'
+// into the upper right block (zero in L) and then -B' times it.
 __device__ __forceinline__ void invert_corner(float *Lm) {
-  block_product(Lm + 32 * kLs, Lm, Lm + 32, 1.f);
-  intra_sync();
-  block_product(Lm + 32 * kLs + 32, Lm + 32, Lm + 32 * kLs, -1.f);
-  intra_sync();
+  const int w = threadIdx.x / 32 % 4, r = 16 * (w & 1), c = 16 * (w >> 1);
+#pragma unroll 1
+  for (int step = 0; step < 2; ++step) {
+    float acc[2][4];
+    product16<32>(Lm + 32 * kLs + 32 * step + r * kLs, kLs, 1, Lm + 32 * step + c, acc);
+    store16(Lm + (step ? 32 * kLs : 32) + r * kLs + c, acc, step ? -1.f : 1.f);
+    intra_sync();
+  }
 }
 
 // Row `row` of a 64-column bf16 tile (hi and lo planes, 128B swizzle): 8
