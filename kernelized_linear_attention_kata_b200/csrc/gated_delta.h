@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 namespace kata {
 
@@ -36,6 +37,7 @@ struct GatedDeltaLaunch {
   unsigned *status = nullptr;
   int G = 1, seg_chunks = 0;
   float *F = nullptr, *B = nullptr, *seg_starts = nullptr;
+  uint8_t *records = nullptr;      // what the solve leaves of each chunk [BH][N]
 };
 
 struct GatedDeltaStep {
@@ -53,6 +55,8 @@ template <typename Tin> cudaError_t simt_gated_delta_backward(const GatedDeltaLa
 // Tensor-core forward (bf16, d_k and d_v in {64, 128}, 16-byte aligned q, k, v).
 bool gd_tc_shape(int d_k, int d_v);
 void gd_tc_split(long long BH, int N, int sms, int *G, int *seg_chunks);
+size_t gd_tc_record_bytes();
+cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k, bool with_beta);
 cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v);
 template <typename Tin> cudaError_t gated_delta_step(const GatedDeltaStep &a, int d_k, int d_v);
 

@@ -38,11 +38,12 @@ kata_status_t check_shape(int B, int H_k, int H, int T, int d_k, int d_v, kata_d
 struct Regions {
   unsigned char *base;
   size_t used = kHeaderBytes;
-  float *take(size_t floats) {
-    float *p = base ? reinterpret_cast<float *>(base + used) : nullptr;
-    used += align_up(floats * sizeof(float));
+  unsigned char *take_bytes(size_t n) {
+    unsigned char *p = base ? base + used : nullptr;
+    used += align_up(n);
     return p;
   }
+  float *take(size_t floats) { return reinterpret_cast<float *>(take_bytes(floats * sizeof(float))); }
 };
 
 // bf16 with d_k and d_v in {64, 128} runs on the tensor cores. The choice is
@@ -71,6 +72,7 @@ size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, 
     const int sms = sm_count();
     if (sms <= 0) return 0;
     if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, sms, &a.G, &a.seg_chunks);
+    a.records = r.take_bytes((size_t)a.BH * a.N * gd_tc_record_bytes());
     if (a.G > 1) {
       a.F = r.take((size_t)a.BH * (a.G - 1) * d_k * d_k);
       a.B = r.take((size_t)a.BH * (a.G - 1) * d_k * d_v);

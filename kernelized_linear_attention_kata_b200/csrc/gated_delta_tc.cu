@@ -22,25 +22,23 @@
 // every later state.
 //
 // What bounds it: the chain S -> K S -> R -> D -> S' of one chunk, three MMA
-// rounds and three passes of the value threads over 64 columns, about 2 us a
-// chunk, while the tensor pipe is busy for two thirds of that (the operand
-// halves double its work). So all that does not depend on S is taken off the
-// chain: four warps compute M and P one chunk ahead, and the outputs of a
-// chunk leave while the next chunk's K S runs. With fewer heads than SMs the
-// sequence is cut into G segments: each but the last is first walked for its
-// effect on a state, S_end = F S_start + B (the same kernel without outputs,
-// once on V from S = 0 and once with V = 0 from S = I), a small kernel joins
-// them, and the segments then run side by side.
+// rounds and three passes of the value threads over the columns. What does
+// not depend on S is kept off it: M, P and the decays come ready from the
+// solve (gated_delta_solve.cu), and the outputs of a chunk leave while the next
+// chunk's K S runs. With fewer heads than SMs the sequence is cut into G
+// segments: each but the last is first walked for its effect on a state, S_end =
+// F S_start + B (the same kernel without outputs, once on V from S = 0 and once
+// with V = 0 from S = I), a small kernel joins them, and the segments then run
+// side by side.
 //
 // An issuing thread gets an MMA out every 75-95 cycles whatever its N, so N is
 // 128 wherever two tiles lie side by side: K and Q rows, the two 64-key panels
 // of the update, the hi and lo tiles of M.
 //
-// Warps (512 threads): 0-7 the state warps (two warpgroups, each half of the
-// columns), 8-11 the chunk-local group (K rows on lanes 0-63, Q rows on
-// 64-127 of [K; Q] K^T), 12 the MMA issuer, 13 the TMA loads, 14 the output
-// stores, 15 the gates. Registers are moved from the last two warpgroups to
-// the state warps, which hold up to 64 entries of S and as many in flight.
+// Warps (384 threads): 0-7 the state warps (two warpgroups, each half of the
+// columns), 8 the MMA issuer, 9 the loads, 10 the output stores. Twelve warps
+// leave 168 registers a thread, which the state warps need: up to 64 entries
+// of S and as many in flight.
 #include "common.cuh"
 #include "gated_delta_tc.cuh"
 #include "profile.h"
@@ -51,37 +49,31 @@ namespace {
 
 using namespace gdtc;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;
 constexpr int kStateWarps = 8;
-constexpr int kStateRegs = 168, kIntraRegs = 112, kHelperRegs = 64;
-static_assert(2 * kStateRegs + kIntraRegs + kHelperRegs <= 4 * 128, "registers at launch");
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory columns. The state's operand halves share their columns with
 // the update's accumulator, R's with K S, D~'s and D's with M R: each thread
 // rewrites only the columns it has read.
-constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColD = 256, kColDl = 320, kColO = 384,
-                   kColKQ = 448;
-constexpr int kKqStages = 3, kGateStages = 3;
+constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColD = 256, kColDl = 320, kColO = 384;
+constexpr int kKqStages = 3;
 
 template <int DK, int DV> struct Layout {
   static constexpr int NP = DK / 64;                       // panels of a K or Q tile
   static constexpr int kKq = 2 * NP * kPanel;              // [K p0][Q p0][K p1][Q p1]
   static constexpr int kV = kC * DV * 2;                   // V, then the outputs in its place
   static constexpr int kOffKq = 0;
-  static constexpr int kOffM = kKqStages * kKq;            // two stages of hi, lo
-  static constexpr int kOffP = kOffM + 4 * kPanel;
-  static constexpr int kOffV = kOffP + 4 * kPanel;
-  static constexpr int kOffL = kOffV + 2 * kV;
-  static constexpr int kOffGates = kOffL + kC * kLs * 4;
-  static constexpr int kOffBars = kOffGates + kGateStages * (int)sizeof(Gates);
+  static constexpr int kOffTiles = kKqStages * kKq;        // two stages of M hi, lo, P hi, lo
+  static constexpr int kOffV = kOffTiles + 8 * kPanel;
+  static constexpr int kOffGates = kOffV + 2 * kV;         // two stages
+  static constexpr int kOffBars = kOffGates + 2 * kRecGates;
   static constexpr int kBytes = kOffBars + 512 + 1024;     // barriers, alignment slack
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 enum {
   kKqFull = 0, kKqEmpty = kKqFull + kKqStages, kVFull = kKqEmpty + kKqStages, kVEmpty = kVFull + 2,
-  kPmFull = kVEmpty + 2, kPmEmpty = kPmFull + 2, kGateFull = kPmEmpty + 2,
-  kGateEmpty = kGateFull + kGateStages, kSReady = kGateEmpty + kGateStages, kKsDone, kRReady, kDDone,
-  kDtReady, kDlReady, kUDone, kODone, kOReady, kKkDone, kEnd, kEnd2, kNumBars
+  kRecFull = kVEmpty + 2, kRecEmpty = kRecFull + 2, kSReady = kRecEmpty + 2, kKsDone, kRReady, kDDone,
+  kDtReady, kDlReady, kUDone, kODone, kOReady, kEnd, kNumBars
 };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
 
@@ -89,9 +81,10 @@ struct Args {
   const float *g, *beta, *S0;
   float *S_out;
   float *F, *B;                    // segments' effects [BH][G - 1][..]: kind 1 and kind 0
+  const uint8_t *records;          // [BH][N]
   const float *starts;             // segments' starting states [BH][G][d_k][d_v], 1 .. G - 1 used
   unsigned *status;
-  int H, Hk, T, G, seg_chunks;
+  int H, Hk, T, N, G, seg_chunks;
 };
 
 // OUT: outputs of segments 0 .. G - 1. !OUT: the effect of segments 0 .. G - 2
@@ -109,8 +102,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBars);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  Gates *gates = reinterpret_cast<Gates *>(smem + L::kOffGates);
-  float *Lm = reinterpret_cast<float *>(smem + L::kOffL);
+  const float *gates = reinterpret_cast<const float *>(smem + L::kOffGates);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int segs = OUT ? a.G : a.G - 1;
@@ -129,16 +121,15 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
       if (i == kSReady || i == kRReady || i == kDtReady || i == kDlReady || i == kOReady ||
-          (i >= kGateEmpty && i < kGateEmpty + kGateStages) ||
           (!OUT && (i == kVEmpty || i == kVEmpty + 1)))
         count = kStateWarps;
-      if (i == kPmFull || i == kPmFull + 1) count = 4;
+      if (i == kRecEmpty || i == kRecEmpty + 1) count = 1 + kStateWarps;   // MMAs, decays read
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == 12) {
+  if (warp == 8) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -149,7 +140,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
 
   if (warp < kStateWarps) {
     // ------------------------------------------------------------ state warps
-    more_registers<kStateRegs>();
     const int h = warp / 4;                                // half of the columns
     const int r = 32 * (warp % 4) + lane;                  // value column
     const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
@@ -215,9 +205,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       if (OUT && c > 0 && !(ok = outputs(c - 1))) break;
 
       // R = V - e^G (K S)
-      if (!(ok = warp_wait(&bars[kPmFull + st], (c >> 1) & 1, abort_flag))) break;
+      if (!(ok = warp_wait(&bars[kRecFull + st], (c >> 1) & 1, abort_flag))) break;
       if (values && !(ok = warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag))) break;
-      const Gates &gt = gates[c % kGateStages];
+      const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC;
       uint32_t V[16];                                      // two tokens a register
       {
         const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + st * L::kV) + 32 * h * DV + r;
@@ -235,7 +225,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const float4 f = gate4(gt.from_start, 32 * h + 2 * i);
+          const float4 f = gate4(from_start, 32 * h + 2 * i);
           y[i] = __ffma2_rn(make_float2(-f.x, -f.y), as_float2(x[2 * i], x[2 * i + 1]),
                             as_float2(V[i] << 16, V[i] & 0xffff0000u));
           y[i + 1] = __ffma2_rn(make_float2(-f.z, -f.w), as_float2(x[2 * i + 2], x[2 * i + 3]),
@@ -254,7 +244,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-          const float4 f = gate4(gt.from_start, 32 * h + i);
+          const float4 f = gate4(from_start, 32 * h + i);
           x[i] = __float_as_uint(f.x * __uint_as_float(x[i]));
           x[i + 1] = __float_as_uint(f.y * __uint_as_float(x[i + 1]));
           x[i + 2] = __float_as_uint(f.z * __uint_as_float(x[i + 2]));
@@ -277,7 +267,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const float4 f = gate4(gt.to_end, 32 * h + 2 * i);
+          const float4 f = gate4(to_end, 32 * h + 2 * i);
           d[i] = __fadd2_rn(as_float2(x[2 * i], x[2 * i + 1]), as_float2(y[2 * i], y[2 * i + 1]));
           d[i + 1] = __fadd2_rn(as_float2(x[2 * i + 2], x[2 * i + 3]), as_float2(y[2 * i + 2], y[2 * i + 3]));
           z[i] = __fmul2_rn(make_float2(f.x, f.y), d[i]);
@@ -288,8 +278,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       tc_fence_before();
       warp_arrive(&bars[kDtReady]);
-      const float whole = gt.from_start[kC - 1];
-      warp_arrive(&bars[kGateEmpty + c % kGateStages]);
+      const float whole = from_start[kC - 1];
+      warp_arrive(&bars[kRecEmpty + st]);
       if (OUT) {
         if (active) {
           put32(col_half + kColDl, d);
@@ -338,105 +328,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         }
       }
     }
-  } else if (warp < 12) {
-    // ------------------------------------------------------------ M and P, one chunk ahead
-    fewer_registers<kIntraRegs>();
-    const int w = warp - 8;
-    const int t = 32 * (w & 1) + lane;                     // K row (w < 2) or Q row (w >= 2)
-    const uint32_t lane_off = (uint32_t)(32 * w) << 16;
-    constexpr uint32_t id_kq = idesc_bf16(128, kC, false, false);
-    auto issue_kq = [&](int c) -> bool {                   // [K; Q] K^T of chunk c
-      const int st = c % kKqStages;
-      if (!wait_bar(&bars[kKqFull + st], (c / kKqStages) & 1, abort_flag)) return false;
-      tc_fence_after();
-      const uint32_t kq = smem_u32(smem + L::kOffKq + st * L::kKq);
-#pragma unroll 2
-      for (int k = 0; k < DK / 16; ++k) {
-        const uint64_t desc = smem_desc(kq + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128);
-        mma_ss(tbase + kColKQ, desc, desc, id_kq, k > 0);
-      }
-      mma_commit(&bars[kKkDone]);
-      return true;
-    };
-    bool ok = true;
-    if (w == 2 && lane == 0 && n > 0) ok = issue_kq(0);
-    ok = __all_sync(0xffffffffu, ok);
-    // an aborted warp goes on through the group's barriers without work
-    for (int c = 0; c < n; ++c) {
-      const int st = c & 1;
-      const Gates &gt = gates[c % kGateStages];
-      if (ok && c >= 2) ok = warp_wait(&bars[kPmEmpty + st], ((c >> 1) - 1) & 1, abort_flag);
-      if (ok) ok = warp_wait(&bars[kGateFull + c % kGateStages], (c / kGateStages) & 1, abort_flag);
-      if (ok) ok = warp_wait(&bars[kKkDone], c & 1, abort_flag);
-      if (ok) {
-        tc_fence_after();
-        uint8_t *tile = smem + L::kOffP + st * 2 * kPanel;
-        const int diag = w & 1;                            // the half that holds the row's own block
-        if (w < 2 || OUT) {
-          uint32_t x[32];
-          tmem_ld32(tbase + lane_off + kColKQ + 32 * diag, x);
-          const RowDecay d = row_decay(gt, t, w < 2);
-          const float b_t = gt.beta[t];
-          tmem_wait_ld();
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            float y[8];
-            decay8(gt, d, 4 * diag + b, false, x + 8 * b, y);
-            if (w < 2) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)                  // transposed, for the inversion
-                Lm[(32 * diag + 8 * b + j) * kLs + t] = b_t * y[j];
-            } else {
-              store_split8(tile, tile + kPanel, t, 4 * diag + b, y);
-            }
-          }
-          if (diag == 1) {
-            tmem_ld32(tbase + lane_off + kColKQ, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              float y[8];
-              decay8(gt, d, b, true, x + 8 * b, y);
-              if (w < 2) {
-                float *dst = Lm + t * kLs + 8 * b;
-                *reinterpret_cast<float4 *>(dst) = make_float4(b_t * y[0], b_t * y[1], b_t * y[2], b_t * y[3]);
-                *reinterpret_cast<float4 *>(dst + 4) = make_float4(b_t * y[4], b_t * y[5], b_t * y[6], b_t * y[7]);
-              } else {
-                store_split8(tile, tile + kPanel, t, b, y);
-              }
-            }
-          } else if (w == 2) {                             // tokens behind every row of the warp
-#pragma unroll
-            for (int b = 4; b < 8; ++b) {
-              *reinterpret_cast<uint4 *>(tile + sw128(t, b)) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4 *>(tile + kPanel + sw128(t, b)) = make_uint4(0, 0, 0, 0);
-            }
-          }
-        }
-        __syncwarp();
-        if (w < 2) invert_diagonal(Lm + 32 * w * (kLs + 1));
-      }
-      tc_fence_before();
-      intra_sync();                                        // the products are read, the blocks inverted
-      if (w == 2 && c + 1 < n) {
-        bool sent = true;
-        if (ok && lane == 0) sent = issue_kq(c + 1);
-        ok = __all_sync(0xffffffffu, sent) && ok;
-      }
-      invert_corner(Lm);
-      uint8_t *tile = smem + L::kOffM + st * 2 * kPanel;
-      store_inverse<true>(Lm, gt, tile, tile + kPanel);
-      fence_async_smem();
-      if (ok) warp_arrive(&bars[kPmFull + st]);
-      intra_sync();                                        // Lm is free
-    }
-    if (w == 2 && lane == 0 && *abort_flag && n > 0) {     // MMAs of this thread in flight
-      mma_commit(&bars[kEnd2]);
-      drain(&bars[kEnd2], 0);
-    }
-  } else {
-    fewer_registers<kHelperRegs>();
-    if (warp == 12 && lane == 0) {
+  } else if (warp == 8) {
+    if (lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t id_64 = idesc_bf16(128, 64, false, false);    // K-major right operand
       constexpr uint32_t id_128 = idesc_bf16(128, 128, false, false);
@@ -447,8 +340,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       for (int c = 0; c < n && ok; ++c) {
         const int st = c & 1, ks = c % kKqStages;
         const uint32_t kq = smem_u32(smem + L::kOffKq + ks * L::kKq);
-        if (!(ok = wait_bar(&bars[kKqFull + ks], (c / kKqStages) & 1, abort_flag))) break;
-        if (!(ok = wait_bar(&bars[kSReady], c & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(&bars[kKqFull + ks], (c / kKqStages) & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(&bars[kSReady], c & 1, abort_flag))) break;
         tc_fence_after();
         {
           // [K; Q] S (!OUT: K S): S^T hi and lo against the K and Q rows
@@ -461,12 +354,12 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                      OUT ? id_128 : id_64, lo > 0 || k > 0);
           mma_commit(&bars[kKsDone]);
         }
-        if (!(ok = wait_bar(&bars[kPmFull + st], (c >> 1) & 1, abort_flag))) break;
-        if (!(ok = wait_bar(&bars[kRReady], c & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(&bars[kRecFull + st], (c >> 1) & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(&bars[kRReady], c & 1, abort_flag))) break;
         tc_fence_after();
         {
           // R^T hi against [M hi; M lo] (two accumulators), R^T lo against M hi
-          const uint32_t m = smem_u32(smem + L::kOffM + st * 2 * kPanel);
+          const uint32_t m = smem_u32(smem + L::kOffTiles + st * 4 * kPanel);
 #pragma unroll 1
           for (int lo = 0; lo < 2; ++lo)
 #pragma unroll 2
@@ -475,7 +368,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                      lo ? id_64 : id_128, lo > 0 || k > 0);
           mma_commit(&bars[kDDone]);
         }
-        if (!(ok = wait_bar(&bars[kDtReady], c & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(&bars[kDtReady], c & 1, abort_flag))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int lo = 0; lo < 2; ++lo)
@@ -485,9 +378,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                    smem_desc(kq + k * 2048, 2 * kPanel, 1024, kSw128), id_up, lo > 0 || k > 0);
         mma_commit(&bars[kUDone]);
         if (OUT) {
-          if (!(ok = wait_bar(&bars[kDlReady], c & 1, abort_flag))) break;
+          if (!(ok = mbar_wait(&bars[kDlReady], c & 1, abort_flag))) break;
           tc_fence_after();
-          const uint32_t p = smem_u32(smem + L::kOffP + st * 2 * kPanel);
+          const uint32_t p = smem_u32(smem + L::kOffTiles + (st * 4 + 2) * kPanel);
 #pragma unroll 1
           for (int pass = 0; pass < 3; ++pass)             // += D P: hi hi, hi lo, lo hi
 #pragma unroll 2
@@ -497,21 +390,25 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           mma_commit(&bars[kODone]);
         }
         mma_commit(&bars[kKqEmpty + ks]);
-        mma_commit(&bars[kPmEmpty + st]);
+        mma_commit(&bars[kRecEmpty + st]);
       }
       if (!ok) {
         mma_commit(&bars[kEnd]);
         drain(&bars[kEnd], 0);
       }
-    } else if (warp == 13 && lane == 0) {
-      // ---------------------------------------------------------- TMA loads
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- loads
       tma_prefetch_desc(&tmk);
       if (OUT) tma_prefetch_desc(&tmq);
       if (values) tma_prefetch_desc(&tmv);
-      int kq_sent = 0, v_sent = 0;
+      const uint8_t *rec = a.records + ((size_t)bh * a.N + (size_t)seg * a.seg_chunks) * kRecBytes;
+      constexpr uint32_t tiles = (OUT ? 4 : 2) * kPanel;
+      int kq_sent = 0, rec_sent = 0, v_sent = 0;
       for (int c = 0; c < n; ++c) {
-        const int ks = c % kKqStages, vs = c & 1, row = t_begin + kC * c;
-        if (c >= kKqStages && !wait_bar(&bars[kKqEmpty + ks], ((c / kKqStages) - 1) & 1, abort_flag)) break;
+        const int ks = c % kKqStages, st = c & 1, row = t_begin + kC * c;
+        if (c >= kKqStages && !mbar_wait(&bars[kKqEmpty + ks], ((c / kKqStages) - 1) & 1, abort_flag)) break;
         uint8_t *kq = smem + L::kOffKq + ks * L::kKq;
         mbar_arrive_expect_tx(&bars[kKqFull + ks], OUT ? L::kKq : L::kKq / 2);
 #pragma unroll
@@ -520,59 +417,48 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           if (OUT) tma_load_3d(kq + (2 * p + 1) * kPanel, &tmq, &bars[kKqFull + ks], 64 * p, row, kh);
         }
         kq_sent = c + 1;
+        if (c >= 2 && !mbar_wait(&bars[kRecEmpty + st], ((c >> 1) - 1) & 1, abort_flag)) break;
+        mbar_arrive_expect_tx(&bars[kRecFull + st], kRecGates + tiles);
+        bulk_load(smem + L::kOffGates + st * kRecGates, rec + (size_t)c * kRecBytes, kRecGates,
+                  &bars[kRecFull + st]);
+        bulk_load(smem + L::kOffTiles + st * 4 * kPanel, rec + (size_t)c * kRecBytes + kRecM, tiles,
+                  &bars[kRecFull + st]);
+        rec_sent = c + 1;
         if (values) {
-          if (c >= 2 && !wait_bar(&bars[kVEmpty + vs], ((c >> 1) - 1) & 1, abort_flag)) break;
-          mbar_arrive_expect_tx(&bars[kVFull + vs], L::kV);
-          tma_load_3d(smem + L::kOffV + vs * L::kV, &tmv, &bars[kVFull + vs], 0, row, bh);
+          if (c >= 2 && !mbar_wait(&bars[kVEmpty + st], ((c >> 1) - 1) & 1, abort_flag)) break;
+          mbar_arrive_expect_tx(&bars[kVFull + st], L::kV);
+          tma_load_3d(smem + L::kOffV + st * L::kV, &tmv, &bars[kVFull + st], 0, row, bh);
           v_sent = c + 1;
         }
       }
       if (*abort_flag) {                                   // copies in flight land before the exit
         for (int c = kq_sent > kKqStages ? kq_sent - kKqStages : 0; c < kq_sent; ++c)
           drain(&bars[kKqFull + c % kKqStages], (c / kKqStages) & 1);
+        for (int c = rec_sent > 2 ? rec_sent - 2 : 0; c < rec_sent; ++c)
+          drain(&bars[kRecFull + (c & 1)], (c >> 1) & 1);
         for (int c = v_sent > 2 ? v_sent - 2 : 0; c < v_sent; ++c)
           drain(&bars[kVFull + (c & 1)], (c >> 1) & 1);
       }
-    } else if (OUT && warp == 14 && lane == 0) {
+    }
+  } else if (OUT && warp == 10) {
+    if (lane == 0) {
       // ---------------------------------------------------------- output stores
       tma_prefetch_desc(&tmo);
       for (int c = 0; c < n; ++c) {
-        if (!wait_bar(&bars[kOReady], c & 1, abort_flag)) break;
+        if (!mbar_wait(&bars[kOReady], c & 1, abort_flag)) break;
         tma_store_3d(&tmo, smem + L::kOffV + (c & 1) * L::kV, 0, t_begin + kC * c, bh);
         bulk_commit_group();
         bulk_wait_read_all();
         mbar_arrive(&bars[kVEmpty + (c & 1)]);
       }
       bulk_wait_all();
-    } else if (warp == 15) {
-      // ---------------------------------------------------------- gates
-      const float *gp = a.g + (size_t)bh * a.T + t_begin, *bp = a.beta + (size_t)bh * a.T + t_begin;
-      float gx = 0.f, gy = 0.f, bx = 0.f, by = 0.f;
-      auto fetch = [&](int c) {
-        const int u = kC * c + 2 * lane;
-        gx = u < t_left ? gp[u] : 0.f;
-        gy = u + 1 < t_left ? gp[u + 1] : 0.f;
-        bx = u < t_left ? bp[u] : 0.f;
-        by = u + 1 < t_left ? bp[u + 1] : 0.f;
-      };
-      if (n > 0) fetch(0);
-      for (int c = 0; c < n; ++c) {
-        const int gs = c % kGateStages;
-        if (c >= kGateStages &&
-            !warp_wait(&bars[kGateEmpty + gs], ((c / kGateStages) - 1) & 1, abort_flag))
-          break;
-        const float x = gx, y = gy, bx0 = bx, by0 = by;
-        if (c + 1 < n) fetch(c + 1);                       // in flight during this chunk's
-        make_gates(gates[gs], x, y, bx0, by0);
-        warp_arrive(&bars[kGateFull + gs]);
-      }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tbase, kTmemCols);
+  if (warp == 8) tmem_dealloc(tbase, kTmemCols);
   if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
 }
 
@@ -628,8 +514,10 @@ cudaError_t launch(const GatedDeltaLaunch &a) {
       !make_tma_3d_bf16_box(&tv, a.v, DV, a.T, a.BH, DV, kC, false) ||
       !make_tma_3d_bf16_box(&to, a.o, DV, a.T, a.BH, DV, kC, false))
     return cudaErrorInvalidValue;
-  Args x{a.g, a.beta, a.S0, a.S_out, a.F, a.B, a.seg_starts,
-         a.status, a.H, a.Hk, a.T, a.G, a.seg_chunks};
+  Args x{a.g, a.beta, a.S0, a.S_out, a.F, a.B, a.records, a.seg_starts,
+         a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks};
+  cudaError_t se = gd_tc_solve(a, DK, true);
+  if (se != cudaSuccess) return se;
   if (a.G > 1) {
     auto kern = gd_tc_kernel<DK, DV, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);

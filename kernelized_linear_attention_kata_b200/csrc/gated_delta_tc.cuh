@@ -1,6 +1,6 @@
 // Building blocks of the gated delta rule's tensor-core kernels: operand
-// splitting, barrier waits by whole warps, bounded draining, and the chunk
-// solve (I + L)^-1 of four warps.
+// splitting, barrier waits by whole warps, bounded draining, bulk copies, the
+// record of a chunk, and the chunk solve (I + L)^-1 of four warps.
 #pragma once
 
 #include "gated_delta.h"
@@ -30,23 +30,9 @@ __device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
-// The bounded wait of tc_common.cuh, in line: a kernel that moves registers
-// between its warpgroups makes no calls.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-  if (mbar_test_wait(bar, parity) || mbar_try_wait(bar, parity, kSuspendHintNs)) return true;
-  const uint64_t start = global_ns();
-  while (!mbar_try_wait(bar, parity, kSuspendHintNs)) {
-    if (*abort_flag) return false;
-    if (global_ns() - start > kWaitLimitNs) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
-}
 // A wait by a whole warp: the result is the same in all lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 // One arrival for a warp, after all its lanes got here.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -54,11 +40,31 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 // Waits (at most kWaitLimitNs) for copies or MMAs in flight after an abort.
-__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
+static __device__ __noinline__ void drain(uint64_t *bar, uint32_t parity) {
   const uint64_t start = global_ns();
   while (!mbar_try_wait(bar, parity, kSuspendHintNs))
     if (global_ns() - start > kWaitLimitNs) return;
 }
+
+// Untiled bulk copies (16-byte aligned, multiples of 16 bytes, no multicast).
+__device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *dst, const void *smem_src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(smem_src)), "r"(bytes)
+               : "memory");
+}
+
+// What the chains need of a chunk beside q, k and v, as the solve leaves it in
+// the workspace: e^{G_t} and e^{G_C - G_t}, then 64 x 64 bf16 tiles in the
+// layout of an MMA operand (128-byte rows, 128B swizzle), each as hi and lo:
+// M (times diag(beta) for the forward), then P.
+constexpr int kRecGates = 2 * kC * 4;
+constexpr int kRecM = kRecGates, kRecP = kRecM + 2 * kPanel, kRecBytes = kRecP + 2 * kPanel;
 
 // Byte offset of 16-byte chunk c of row r in a 128-byte-row tile, 128B swizzle.
 __device__ __forceinline__ uint32_t sw128(int r, int c) {
@@ -72,9 +78,9 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) {
 // block's last token: both exponents are <= 0 (for g <= 0), and a row needs 8
 // exponentials plus those of its own block instead of 64.
 struct Gates {
-  float hi[kC], lo[kC];              // G_t
   float from_start[kC];              // e^{G_t}
   float to_end[kC];                  // e^{G_C - G_t}
+  float hi[kC], lo[kC];              // G_t
   float to_block[kC];                // e^{G_a - G_t}, a = t | 7
   float beta[kC];
 };
@@ -144,18 +150,6 @@ __device__ __forceinline__ void decay8(const Gates &g, const RowDecay &d, int bl
     out[j] = w * __uint_as_float(x[j]);
   }
 }
-
-// Register split of a block of four warpgroups, launched with 128 a thread.
-template <int R> __device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R> __device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
-// Barrier of the four warps of the chunk-local group (the 128 threads after
-// the eight state warps). Its callers reach it in every round, aborted or not.
-__device__ __forceinline__ void intra_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // (I + L)^-1 of a chunk, in `Lm` (row stride kLs), by blocks of 16, 32, 64:
 //   [[A, 0], [X, B]]^-1 = [[A', 0], [-B' X A', B']].
@@ -253,7 +247,7 @@ __device__ __forceinline__ void invert_corner(float *Lm) {
     float acc[2][4];
     product16<32>(Lm + 32 * kLs + 32 * step + r * kLs, kLs, 1, Lm + 32 * step + c, acc);
     store16(Lm + (step ? 32 * kLs : 32) + r * kLs + c, acc, step ? -1.f : 1.f);
-    intra_sync();
+    __syncthreads();
   }
 }
 
