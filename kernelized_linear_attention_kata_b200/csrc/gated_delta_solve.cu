@@ -5,9 +5,11 @@
 // One block of four warps a chunk: [K; Q] K^T by tcgen05 (K rows on TMEM lanes
 // 0-63, Q rows on 64-127), thread = row; the K rows become L and are inverted
 // by blocks, the Q rows become P. Four blocks share an SM and hide one
-// another's latencies. Inside the chains' kernel the same work, one chunk
-// ahead, took 10K cycles a chunk to the chain's 5K: with both codes resident
-// every warp waited on the instruction cache.
+// another's latencies. Loops are kept rolled: straight code beyond 32 KB runs
+// from the second instruction cache at 2.4 cycles an instruction (measured),
+// and the same work unrolled to 40 KB took twice as long. Inside the chains'
+// kernel, one chunk ahead, it took 10K cycles a chunk to the chain's 5K, both
+// codes waiting on instructions.
 #include "gated_delta_tc.cuh"
 #include "profile.h"
 #include "common.cuh"
@@ -81,7 +83,7 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       constexpr uint32_t id = idesc_bf16(128, kC, false, false);
       const uint32_t kq = smem_u32(smem);
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < DK / 16; ++k) {
         const uint64_t desc = smem_desc(kq + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128);
         mma_ss(tbase, desc, desc, id, k > 0);
@@ -98,43 +100,28 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     const int diag = w & 1, t = 32 * diag + lane;          // token of the row
     const uint32_t row = tbase + ((uint32_t)(32 * w) << 16);
     uint8_t *tile = smem + 2 * kPanel;                     // P hi, lo
-    uint32_t x[32];
-    tmem_ld32(row + 32 * diag, x);
     const RowDecay d = row_decay(gt, t, w < 2);
     const float b_t = gt.beta[t];
-    tmem_wait_ld();
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      float y[8];
-      decay8(gt, d, 4 * diag + b, false, x + 8 * b, y);
-      if (w < 2) {
+    const int seen = 4 + 4 * diag;                         // blocks of 8 tokens not behind the warp's rows
+#pragma unroll 1
+    for (int b = 0; b < (w < 2 ? seen : 8); ++b) {
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (b < seen) {
+        uint32_t x[8];
+        tmem_ld8(row + 8 * b, x);
+        tmem_wait_ld();
+        decay8(gt, d, b, x, y);
+      }
+      if (w >= 2) {
+        store_split8(tile, tile + kPanel, t, b, y);
+      } else if (b / 4 == diag) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)                        // transposed, for the inversion
-          Lm[(32 * diag + 8 * b + j) * kLs + t] = b_t * y[j];
+          Lm[(8 * b + j) * kLs + t] = b_t * y[j];
       } else {
-        store_split8(tile, tile + kPanel, t, 4 * diag + b, y);
-      }
-    }
-    if (diag == 1) {
-      tmem_ld32(row, x);
-      tmem_wait_ld();
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        float y[8];
-        decay8(gt, d, b, true, x + 8 * b, y);
-        if (w < 2) {
-          float *dst = Lm + t * kLs + 8 * b;
-          *reinterpret_cast<float4 *>(dst) = make_float4(b_t * y[0], b_t * y[1], b_t * y[2], b_t * y[3]);
-          *reinterpret_cast<float4 *>(dst + 4) = make_float4(b_t * y[4], b_t * y[5], b_t * y[6], b_t * y[7]);
-        } else {
-          store_split8(tile, tile + kPanel, t, b, y);
-        }
-      }
-    } else if (w == 2) {                                   // tokens behind every row of the warp
-#pragma unroll
-      for (int b = 4; b < 8; ++b) {
-        *reinterpret_cast<uint4 *>(tile + sw128(t, b)) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(tile + kPanel + sw128(t, b)) = make_uint4(0, 0, 0, 0);
+        float *dst = Lm + t * kLs + 8 * b;
+        *reinterpret_cast<float4 *>(dst) = make_float4(b_t * y[0], b_t * y[1], b_t * y[2], b_t * y[3]);
+        *reinterpret_cast<float4 *>(dst + 4) = make_float4(b_t * y[4], b_t * y[5], b_t * y[6], b_t * y[7]);
       }
     }
     __syncwarp();
@@ -154,7 +141,7 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     bulk_store(rec + kRecM, smem, 4 * kPanel);
     bulk_commit_group();
     if (!ok) flag_status(status, kStatusDeviceTimeout);
-    bulk_wait_all();
+    bulk_wait_read_all();
   }
 }
 

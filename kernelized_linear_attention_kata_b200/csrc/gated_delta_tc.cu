@@ -56,24 +56,26 @@ constexpr uint32_t kTmemCols = 512;
 // the update's accumulator, R's with K S, D~'s and D's with M R: each thread
 // rewrites only the columns it has read.
 constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColD = 256, kColDl = 320, kColO = 384;
-constexpr int kKqStages = 3;
 
 template <int DK, int DV> struct Layout {
   static constexpr int NP = DK / 64;                       // panels of a K or Q tile
   static constexpr int kKq = 2 * NP * kPanel;              // [K p0][Q p0][K p1][Q p1]
   static constexpr int kV = kC * DV * 2;                   // V, then the outputs in its place
   static constexpr int kOffKq = 0;
-  static constexpr int kOffTiles = kKqStages * kKq;        // two stages of M hi, lo, P hi, lo
+  static constexpr int kOffTiles = 2 * kKq;                // two stages of M hi, lo, P hi, lo
   static constexpr int kOffV = kOffTiles + 8 * kPanel;
   static constexpr int kOffGates = kOffV + 2 * kV;         // two stages
   static constexpr int kOffBars = kOffGates + 2 * kRecGates;
   static constexpr int kBytes = kOffBars + 512 + 1024;     // barriers, alignment slack
   static_assert(kBytes <= 232448, "shared memory budget");
 };
+// Loaded: K, Q and the record; V. Free: the chunk's MMAs are done and its
+// outputs are in V's place (OUT), V is read (!OUT). Stored: they have left it.
+// The issuer tests few barriers (110-180 cycles each): the state warps wait for
+// the loads and fold them into their own arrivals.
 enum {
-  kKqFull = 0, kKqEmpty = kKqFull + kKqStages, kVFull = kKqEmpty + kKqStages, kVEmpty = kVFull + 2,
-  kRecFull = kVEmpty + 2, kRecEmpty = kRecFull + 2, kSReady = kRecEmpty + 2, kKsDone, kRReady, kDDone,
-  kDtReady, kDlReady, kUDone, kODone, kOReady, kEnd, kNumBars
+  kKqFull = 0, kVFull = 2, kFree = 4, kStored = 6, kSReady = 8, kKsDone, kRReady, kDDone, kDtReady, kDlReady,
+  kUDone, kODone, kEnd, kNumBars
 };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
 
@@ -120,10 +122,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kSReady || i == kRReady || i == kDtReady || i == kDlReady || i == kOReady ||
-          (!OUT && (i == kVEmpty || i == kVEmpty + 1)))
+      if (i == kFree || i == kFree + 1 || i == kSReady || i == kRReady || i == kDtReady || i == kDlReady)
         count = kStateWarps;
-      if (i == kRecEmpty || i == kRecEmpty + 1) count = 1 + kStateWarps;   // MMAs, decays read
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -170,11 +170,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       tmem_st32(col, y);
     };
     auto gate4 = [](const float *g, int i) { return *reinterpret_cast<const float4 *>(g + i); };
-    auto state_ready = [&]() {
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(&bars[kSReady]);
-    };
     // outputs of chunk c, o_t = e^{G_t} (Q S)_t + (P D)_t, 32 tokens a thread,
     // into the places its values of V were read from
     auto outputs = [&](int c) -> bool {
@@ -190,22 +185,26 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         for (int i = 0; i < 32; ++i) dst[i * DV] = __float2bfloat16_rn(__uint_as_float(x[i]));
       }
       fence_async_smem();
-      warp_arrive(&bars[kOReady]);
+      warp_arrive(&bars[kFree + (c & 1)]);
       return true;
     };
 
-    if (n > 0) {
-      if (active)
-#pragma unroll
-        for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
-      state_ready();
-    }
-    for (int c = 0; c < n; ++c) {
+    for (int c = 0; c <= n; ++c) {
       const int st = c & 1;
+      if (c < n) {
+        if (!(ok = warp_wait(&bars[kKqFull + st], (c >> 1) & 1, abort_flag))) break;
+        if (active) {
+#pragma unroll
+          for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        warp_arrive(&bars[kSReady]);
+      }
       if (OUT && c > 0 && !(ok = outputs(c - 1))) break;
+      if (c == n) break;
 
       // R = V - e^G (K S)
-      if (!(ok = warp_wait(&bars[kRecFull + st], (c >> 1) & 1, abort_flag))) break;
       if (values && !(ok = warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag))) break;
       const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC;
       uint32_t V[16];                                      // two tokens a register
@@ -215,7 +214,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         for (int i = 0; i < 16; ++i)
           V[i] = active && values ? (uint32_t)v[2 * i * DV] | (uint32_t)v[(2 * i + 1) * DV] << 16 : 0u;
       }
-      if (!OUT && values) warp_arrive(&bars[kVEmpty + st]);
       if (!(ok = warp_wait(&bars[kKsDone], c & 1, abort_flag))) break;
       tc_fence_after();
       if (active) {
@@ -279,7 +277,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       tc_fence_before();
       warp_arrive(&bars[kDtReady]);
       const float whole = from_start[kC - 1];
-      warp_arrive(&bars[kRecEmpty + st]);
       if (OUT) {
         if (active) {
           put32(col_half + kColDl, d);
@@ -301,14 +298,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < HK / 2; ++i) S[i] = __ffma2_rn(w2, S[i], as_float2(x[2 * i], x[2 * i + 1]));
-        if (c + 1 < n) {
-#pragma unroll
-          for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
-        }
       }
-      if (c + 1 < n) state_ready();
+      if (!OUT) warp_arrive(&bars[kFree + st]);
     }
-    if (OUT && ok && n > 0) ok = outputs(n - 1);
     if (active && ok) {
       float *dst = nullptr;
       int ld = DV;
@@ -329,73 +321,77 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
     }
   } else if (warp == 8) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      constexpr uint32_t id_64 = idesc_bf16(128, 64, false, false);    // K-major right operand
-      constexpr uint32_t id_128 = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t id_up = idesc_bf16(128, DK, false, true);     // MN-major
-      bool ok = true;
-      // operands in tensor memory: columns of the 16-deep step k, hi or lo
-      auto step_col = [&](uint32_t op, int k, int lo) { return op + 16 * k + 8 * lo; };
-      for (int c = 0; c < n && ok; ++c) {
-        const int st = c & 1, ks = c % kKqStages;
-        const uint32_t kq = smem_u32(smem + L::kOffKq + ks * L::kKq);
-        if (!(ok = mbar_wait(&bars[kKqFull + ks], (c / kKqStages) & 1, abort_flag))) break;
-        if (!(ok = mbar_wait(&bars[kSReady], c & 1, abort_flag))) break;
-        tc_fence_after();
-        {
-          // [K; Q] S (!OUT: K S): S^T hi and lo against the K and Q rows
-#pragma unroll 1
-          for (int lo = 0; lo < 2; ++lo)
-#pragma unroll 2
-            for (int k = 0; k < DK / 16; ++k)
-              mma_ts(tbase + kColKS, step_col(tbase + kColS, k, lo),
-                     smem_desc(kq + (k / 4) * 2 * kPanel + (k % 4) * 32, 16, 1024, kSw128),
-                     OUT ? id_128 : id_64, lo > 0 || k > 0);
-          mma_commit(&bars[kKsDone]);
-        }
-        if (!(ok = mbar_wait(&bars[kRecFull + st], (c >> 1) & 1, abort_flag))) break;
-        if (!(ok = mbar_wait(&bars[kRReady], c & 1, abort_flag))) break;
-        tc_fence_after();
-        {
-          // R^T hi against [M hi; M lo] (two accumulators), R^T lo against M hi
-          const uint32_t m = smem_u32(smem + L::kOffTiles + st * 4 * kPanel);
-#pragma unroll 1
-          for (int lo = 0; lo < 2; ++lo)
-#pragma unroll 2
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tbase + kColD, step_col(tbase + kColKS, k, lo), smem_desc(m + 32 * k, 16, 1024, kSw128),
-                     lo ? id_64 : id_128, lo > 0 || k > 0);
-          mma_commit(&bars[kDDone]);
-        }
-        if (!(ok = mbar_wait(&bars[kDtReady], c & 1, abort_flag))) break;
-        tc_fence_after();
-#pragma unroll 1
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the loop and one lane issues: descriptors and
+    // column addresses are then uniform values (computed by a lane on its own
+    // they cost an MMA 100 cycles instead of 50-60). Descriptors of a stage
+    // differ only in their address field (bytes / 16).
+    constexpr uint32_t id_64 = idesc_bf16(128, 64, false, false);      // K-major right operand
+    constexpr uint32_t id_128 = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t id_up = idesc_bf16(128, DK, false, true);       // MN-major
+    const bool leader = lane == 0;
+    bool ok = true;
+    const uint32_t base = smem_u32(smem);
+    auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
+    for (int c = 0; c < n; ++c) {
+      const int st = c & 1;
+      const uint64_t d_kq = smem_desc(base + L::kOffKq + st * L::kKq, 16, 1024, kSw128);
+      const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, 2 * kPanel, 1024, kSw128);
+      const uint64_t d_m = smem_desc(base + L::kOffTiles + st * 4 * kPanel, 16, 1024, kSw128);
+      const uint64_t d_p = adv(d_m, 2 * kPanel);
+      if (!(ok = warp_wait(&bars[kSReady], c & 1, abort_flag))) break;
+      tc_fence_after();
+      if (leader) {
+        // [K; Q] S (!OUT: K S): S^T hi and lo against the K and Q rows. An
+        // operand in tensor memory takes 16 columns a 16-deep step, hi then lo.
+#pragma unroll
         for (int lo = 0; lo < 2; ++lo)
-#pragma unroll 2
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k)
+            mma_ts(tbase + kColKS, tbase + kColS + 16 * k + 8 * lo, adv(d_kq, (k / 4) * 2 * kPanel + (k % 4) * 32),
+                   OUT ? id_128 : id_64, lo > 0 || k > 0);
+        mma_commit(&bars[kKsDone]);
+      }
+      if (!(ok = warp_wait(&bars[kRReady], c & 1, abort_flag))) break;
+      tc_fence_after();
+      if (leader) {
+        // R^T hi against [M hi; M lo] (two accumulators), R^T lo against M hi
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tbase + kColS, step_col(tbase + kColD, k, lo),
-                   smem_desc(kq + k * 2048, 2 * kPanel, 1024, kSw128), id_up, lo > 0 || k > 0);
+            mma_ts(tbase + kColD, tbase + kColKS + 16 * k + 8 * lo, adv(d_m, 32 * k), lo ? id_64 : id_128,
+                   lo > 0 || k > 0);
+        mma_commit(&bars[kDDone]);
+      }
+      if (!(ok = warp_wait(&bars[kDtReady], c & 1, abort_flag))) break;
+      tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tbase + kColS, tbase + kColD + 16 * k + 8 * lo, adv(d_k_mn, k * 2048), id_up, lo > 0 || k > 0);
         mma_commit(&bars[kUDone]);
-        if (OUT) {
-          if (!(ok = mbar_wait(&bars[kDlReady], c & 1, abort_flag))) break;
-          tc_fence_after();
-          const uint32_t p = smem_u32(smem + L::kOffTiles + (st * 4 + 2) * kPanel);
-#pragma unroll 1
+      }
+      if (OUT) {
+        if (!(ok = warp_wait(&bars[kDlReady], c & 1, abort_flag))) break;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
           for (int pass = 0; pass < 3; ++pass)             // += D P: hi hi, hi lo, lo hi
-#pragma unroll 2
+#pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ts(tbase + kColO, step_col(tbase + kColDl, k, pass == 2),
-                     smem_desc(p + (pass == 1 ? kPanel : 0) + 32 * k, 16, 1024, kSw128), id_64, 1);
+              mma_ts(tbase + kColO, tbase + kColDl + 16 * k + 8 * (pass == 2),
+                     adv(d_p, (pass == 1 ? kPanel : 0) + 32 * k), id_64, 1);
           mma_commit(&bars[kODone]);
         }
-        mma_commit(&bars[kKqEmpty + ks]);
-        mma_commit(&bars[kRecEmpty + st]);
       }
-      if (!ok) {
-        mma_commit(&bars[kEnd]);
-        drain(&bars[kEnd], 0);
-      }
+      __syncwarp();
+    }
+    if (!ok && leader) {
+      mma_commit(&bars[kEnd]);
+      drain(&bars[kEnd], 0);
     }
   } else if (warp == 9) {
     if (lane == 0) {
@@ -405,51 +401,44 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       if (values) tma_prefetch_desc(&tmv);
       const uint8_t *rec = a.records + ((size_t)bh * a.N + (size_t)seg * a.seg_chunks) * kRecBytes;
       constexpr uint32_t tiles = (OUT ? 4 : 2) * kPanel;
-      int kq_sent = 0, rec_sent = 0, v_sent = 0;
+      int sent = 0;
       for (int c = 0; c < n; ++c) {
-        const int ks = c % kKqStages, st = c & 1, row = t_begin + kC * c;
-        if (c >= kKqStages && !mbar_wait(&bars[kKqEmpty + ks], ((c / kKqStages) - 1) & 1, abort_flag)) break;
-        uint8_t *kq = smem + L::kOffKq + ks * L::kKq;
-        mbar_arrive_expect_tx(&bars[kKqFull + ks], OUT ? L::kKq : L::kKq / 2);
+        const int st = c & 1, row = t_begin + kC * c;
+        if (c >= 2 && !mbar_wait(&bars[kFree + st], ((c >> 1) - 1) & 1, abort_flag)) break;
+        uint8_t *kq = smem + L::kOffKq + st * L::kKq;
+        mbar_arrive_expect_tx(&bars[kKqFull + st], (OUT ? L::kKq : L::kKq / 2) + kRecGates + tiles);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          tma_load_3d(kq + 2 * p * kPanel, &tmk, &bars[kKqFull + ks], 64 * p, row, kh);
-          if (OUT) tma_load_3d(kq + (2 * p + 1) * kPanel, &tmq, &bars[kKqFull + ks], 64 * p, row, kh);
+          tma_load_3d(kq + 2 * p * kPanel, &tmk, &bars[kKqFull + st], 64 * p, row, kh);
+          if (OUT) tma_load_3d(kq + (2 * p + 1) * kPanel, &tmq, &bars[kKqFull + st], 64 * p, row, kh);
         }
-        kq_sent = c + 1;
-        if (c >= 2 && !mbar_wait(&bars[kRecEmpty + st], ((c >> 1) - 1) & 1, abort_flag)) break;
-        mbar_arrive_expect_tx(&bars[kRecFull + st], kRecGates + tiles);
         bulk_load(smem + L::kOffGates + st * kRecGates, rec + (size_t)c * kRecBytes, kRecGates,
-                  &bars[kRecFull + st]);
+                  &bars[kKqFull + st]);
         bulk_load(smem + L::kOffTiles + st * 4 * kPanel, rec + (size_t)c * kRecBytes + kRecM, tiles,
-                  &bars[kRecFull + st]);
-        rec_sent = c + 1;
+                  &bars[kKqFull + st]);
+        sent = c + 1;
         if (values) {
-          if (c >= 2 && !mbar_wait(&bars[kVEmpty + st], ((c >> 1) - 1) & 1, abort_flag)) break;
+          if (OUT && c >= 2 && !mbar_wait(&bars[kStored + st], ((c >> 1) - 1) & 1, abort_flag)) break;
           mbar_arrive_expect_tx(&bars[kVFull + st], L::kV);
           tma_load_3d(smem + L::kOffV + st * L::kV, &tmv, &bars[kVFull + st], 0, row, bh);
-          v_sent = c + 1;
         }
       }
-      if (*abort_flag) {                                   // copies in flight land before the exit
-        for (int c = kq_sent > kKqStages ? kq_sent - kKqStages : 0; c < kq_sent; ++c)
-          drain(&bars[kKqFull + c % kKqStages], (c / kKqStages) & 1);
-        for (int c = rec_sent > 2 ? rec_sent - 2 : 0; c < rec_sent; ++c)
-          drain(&bars[kRecFull + (c & 1)], (c >> 1) & 1);
-        for (int c = v_sent > 2 ? v_sent - 2 : 0; c < v_sent; ++c)
-          drain(&bars[kVFull + (c & 1)], (c >> 1) & 1);
-      }
+      if (*abort_flag)                                     // copies in flight land before the exit
+        for (int c = sent > 2 ? sent - 2 : 0; c < sent; ++c) {
+          drain(&bars[kKqFull + (c & 1)], (c >> 1) & 1);
+          if (values) drain(&bars[kVFull + (c & 1)], (c >> 1) & 1);
+        }
     }
   } else if (OUT && warp == 10) {
     if (lane == 0) {
       // ---------------------------------------------------------- output stores
       tma_prefetch_desc(&tmo);
       for (int c = 0; c < n; ++c) {
-        if (!mbar_wait(&bars[kOReady], c & 1, abort_flag)) break;
+        if (!mbar_wait(&bars[kFree + (c & 1)], (c >> 1) & 1, abort_flag)) break;
         tma_store_3d(&tmo, smem + L::kOffV + (c & 1) * L::kV, 0, t_begin + kC * c, bh);
         bulk_commit_group();
         bulk_wait_read_all();
-        mbar_arrive(&bars[kVEmpty + (c & 1)]);
+        mbar_arrive(&bars[kStored + (c & 1)]);
       }
       bulk_wait_all();
     }

@@ -90,29 +90,49 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// a + b as a rounded sum and its error.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return make_float2(s, (a - (s - t)) + (b - t));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  const float2 s = two_sum(a.x, b.x);
+  const float l = s.y + (a.y + b.y);
+  const float h = s.x + l;
+  return make_float2(h, l - (h - s.x));
+}
 // Gates of one chunk by one warp, two tokens a lane; gx, gy are their log decays.
 __device__ __forceinline__ void make_gates(Gates &s, float gx, float gy, float bx, float by) {
+  constexpr float kLog2e = 1.44269504088896340736f, kLog2eRest = 1.92596299112661746887e-8f;
   const int lane = threadIdx.x % 32;
-  const double x = (double)(gx < kMinLogDecay ? kMinLogDecay : gx) * 1.4426950408889634;
-  const double y = (double)(gy < kMinLogDecay ? kMinLogDecay : gy) * 1.4426950408889634;
-  double sum = x + y;
+  auto units = [&](float x) {                              // x / log 2 as two floats
+    x = x < kMinLogDecay ? kMinLogDecay : x;
+    const float h = x * kLog2e;
+    return make_float2(h, fmaf(x, kLog2eRest, fmaf(x, kLog2e, -h)));
+  };
+  const float2 x = units(gx), y = units(gy);
+  float2 sum = add2(x, y);
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const double up = __shfl_up_sync(0xffffffffu, sum, off);
-    if (lane >= off) sum += up;
+    const float2 up = make_float2(__shfl_up_sync(0xffffffffu, sum.x, off), __shfl_up_sync(0xffffffffu, sum.y, off));
+    if (lane >= off) sum = add2(up, sum);
   }
-  const double last = __shfl_sync(0xffffffffu, sum, 31);
-  const double block = __shfl_sync(0xffffffffu, sum, lane | 3);
-  const double G[2] = {sum - y, sum};
+  // the first token of the lane, from the sum before it: no difference of sums
+  float2 before = make_float2(__shfl_up_sync(0xffffffffu, sum.x, 1), __shfl_up_sync(0xffffffffu, sum.y, 1));
+  if (lane == 0) before = make_float2(0.f, 0.f);
+  auto from = [&](int l) {
+    return make_float2(__shfl_sync(0xffffffffu, sum.x, l), __shfl_sync(0xffffffffu, sum.y, l));
+  };
+  const float2 last = from(31), block = from(lane | 3);
+  const float2 G[2] = {add2(before, x), sum};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = 2 * lane + i;
-    const float hi = (float)G[i];
-    s.hi[t] = hi;
-    s.lo[t] = (float)(G[i] - (double)hi);
-    s.from_start[t] = exp2f((float)G[i]);
-    s.to_end[t] = exp2f((float)(last - G[i]));
-    s.to_block[t] = exp2f((float)(block - G[i]));
+    s.hi[t] = G[i].x;
+    s.lo[t] = G[i].y;
+    s.from_start[t] = exp2_fast(G[i].x + G[i].y);
+    s.to_end[t] = exp2_fast((last.x - G[i].x) + (last.y - G[i].y));
+    s.to_block[t] = exp2_fast((block.x - G[i].x) + (block.y - G[i].y));
     s.beta[t] = i ? by : bx;
   }
 }
@@ -135,18 +155,16 @@ __device__ __forceinline__ RowDecay row_decay(const Gates &g, int t, int skip) {
   }
   return d;
 }
-// Columns 8 block .. 8 block + 7 of the row times x. `before`: the block lies
-// before every row of the warp.
-__device__ __forceinline__ void decay8(const Gates &g, const RowDecay &d, int block, bool before,
-                                       const uint32_t *x, float (&out)[8]) {
+// Columns 8 block .. 8 block + 7 of the row times x.
+__device__ __forceinline__ void decay8(const Gates &g, const RowDecay &d, int block, const uint32_t (&x)[8],
+                                       float (&out)[8]) {
   const float f = exp2_fast((d.hi - g.hi[8 * block + 7]) + (d.lo - g.lo[8 * block + 7]));
   const float4 e0 = *reinterpret_cast<const float4 *>(&g.to_block[8 * block]);
   const float4 e1 = *reinterpret_cast<const float4 *>(&g.to_block[8 * block + 4]);
   const float e[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float w = f * e[j];
-    if (!before) w = block < d.block ? w : (block == d.block ? d.own[j] : 0.f);
+    const float w = block < d.block ? f * e[j] : (block == d.block ? d.own[j] : 0.f);
     out[j] = w * __uint_as_float(x[j]);
   }
 }
@@ -154,14 +172,15 @@ __device__ __forceinline__ void decay8(const Gates &g, const RowDecay &d, int bl
 // (I + L)^-1 of a chunk, in `Lm` (row stride kLs), by blocks of 16, 32, 64:
 //   [[A, 0], [X, B]]^-1 = [[A', 0], [-B' X A', B']].
 // The 16-blocks by forward substitution, the products on the warp's tensor
-// instructions in three TF32 products an fp32 pair (x = hi + lo up to 2^-22):
+// instructions in three TF32 products an fp32 pair (x = hi + lo up to 2^-20):
 // on the CUDA cores every operand of these small products would be a shared-
 // memory broadcast, which fills the 128 B/cycle return path with one value.
 // Block substitution is as stable as the triangular solve itself, where
 // repeated squaring of L would not be (powers of L grow with repeated keys).
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+  // by truncation: the conversion instruction runs at an eighth of this rate
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));           // the tensor core drops its low bits
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -176,7 +195,7 @@ __device__ __forceinline__ void product16(const float *A, int ra, int ca, const 
   const int g = threadIdx.x % 32 / 4, t = threadIdx.x % 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < K; k += 8) {
     uint32_t ah[4], al[4], bh[2][2], bl[2][2];
 #pragma unroll
@@ -270,7 +289,7 @@ __device__ __forceinline__ void store_inverse(const float *Lm, const Gates &g, u
                                               uint8_t *lo_tile) {
   const int i = threadIdx.x % 128, t = i / 2, half = i % 2;
   const bool zero = t < 32 && half == 1;
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     const int s0 = 32 * half + 8 * c;
     float x[8];
