@@ -4,7 +4,7 @@
 //
 // One block of four warps a chunk: [K; Q] K^T by tcgen05 (K rows on TMEM lanes
 // 0-63, Q rows on 64-127), thread = row; the K rows become L and are inverted
-// by blocks, the Q rows become P. Four blocks share an SM and hide one
+// by blocks, the Q rows become P. Six blocks share an SM and hide one
 // another's latencies. Loops are kept rolled: straight code beyond 32 KB runs
 // from the second instruction cache at 2.4 cycles an instruction (measured),
 // and the same work unrolled to 40 KB took twice as long. Inside the chains'
@@ -25,16 +25,17 @@ constexpr int kSolveThreads = 128;
 template <int DK> struct SolveLayout {
   static constexpr int NP = DK / 64;
   static constexpr int kKq = 2 * NP * kPanel;
-  // the tiles of the record take the place of K and Q once the products are done
-  static constexpr int kTiles = 4 * kPanel;
-  static constexpr int kOffL = kKq > kTiles ? kKq : kTiles;
-  static constexpr int kOffGates = kOffL + kC * kLs * 4;
+  // K and Q, then in their place P's tiles and L, then M's tiles in L's
+  static constexpr int kOffP = 0, kOffL = 2 * kPanel;
+  static constexpr int kLBytes = kC * kLs * 4;
+  static constexpr int kWork = kOffL + kLBytes > kKq ? kOffL + kLBytes : kKq;
+  static constexpr int kOffGates = (kWork + 127) / 128 * 128;
   static constexpr int kOffBars = kOffGates + (int)sizeof(Gates);
   static constexpr int kBytes = kOffBars + 64 + 1024;
 };
 
 template <int DK, bool BETA>
-__global__ void __launch_bounds__(kSolveThreads, 4)
+__global__ void __launch_bounds__(kSolveThreads, 6)
 gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                    const float *__restrict__ g, const float *__restrict__ beta,
                    uint8_t *__restrict__ records, unsigned *__restrict__ status, int H, int Hk, int T,
@@ -99,7 +100,7 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   {
     const int diag = w & 1, t = 32 * diag + lane;          // token of the row
     const uint32_t row = tbase + ((uint32_t)(32 * w) << 16);
-    uint8_t *tile = smem + 2 * kPanel;                     // P hi, lo
+    uint8_t *tile = smem + L::kOffP;                       // P hi, lo
     const RowDecay d = row_decay(gt, t, w < 2);
     const float b_t = gt.beta[t];
     const int seen = 4 + 4 * diag;                         // blocks of 8 tokens not behind the warp's rows
@@ -129,7 +130,7 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   }
   __syncthreads();
   invert_corner(Lm);
-  store_inverse<BETA>(Lm, gt, smem, smem + kPanel);
+  store_inverse<BETA>(Lm, gt, smem + L::kOffL, smem + L::kOffL + kPanel);
   fence_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -138,7 +139,8 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   if (threadIdx.x == 0) {
     uint8_t *rec = records + (size_t)blockIdx.x * kRecBytes;
     bulk_store(rec, gt.from_start, kRecGates);             // from_start, to_end
-    bulk_store(rec + kRecM, smem, 4 * kPanel);
+    bulk_store(rec + kRecP, smem + L::kOffP, 2 * kPanel);
+    bulk_store(rec + kRecM, smem + L::kOffL, 2 * kPanel);
     bulk_commit_group();
     if (!ok) flag_status(status, kStatusDeviceTimeout);
     bulk_wait_read_all();

@@ -189,6 +189,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       return true;
     };
 
+    // The outputs of a chunk leave while the next one's K S runs (d_k = 128), or,
+    // where that is as short as P D before it, after its R (d_k = 64).
     for (int c = 0; c <= n; ++c) {
       const int st = c & 1;
       if (c < n) {
@@ -201,7 +203,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tc_fence_before();
         warp_arrive(&bars[kSReady]);
       }
-      if (OUT && c > 0 && !(ok = outputs(c - 1))) break;
+      if (OUT && c > 0 && (DK == 128 || c == n) && !(ok = outputs(c - 1))) break;
       if (c == n) break;
 
       // R = V - e^G (K S)
@@ -234,6 +236,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       tc_fence_before();
       warp_arrive(&bars[kRReady]);
+      if (OUT && DK == 64 && c > 0 && !(ok = outputs(c - 1))) break;
       // e^G (Q S) to where P D is added to it, so that the next chunk's Q S
       // need not wait for this chunk's outputs
       if (OUT && active) {

@@ -195,7 +195,7 @@ __device__ __forceinline__ void product16(const float *A, int ra, int ca, const 
   const int g = threadIdx.x % 32 / 4, t = threadIdx.x % 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
   for (int k = 0; k < K; k += 8) {
     uint32_t ah[4], al[4], bh[2][2], bl[2][2];
 #pragma unroll
@@ -284,23 +284,28 @@ __device__ __forceinline__ void store_split8(uint8_t *hi_tile, uint8_t *lo_tile,
 }
 
 // The inverse times diag(beta) (BETA) as bf16 hi / lo tiles, two threads a row.
+// The tiles may lie over Lm.
 template <bool BETA>
 __device__ __forceinline__ void store_inverse(const float *Lm, const Gates &g, uint8_t *hi_tile,
                                               uint8_t *lo_tile) {
   const int i = threadIdx.x % 128, t = i / 2, half = i % 2;
   const bool zero = t < 32 && half == 1;
-#pragma unroll 1
+  float4 m[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m[j] = *reinterpret_cast<const float4 *>(Lm + t * kLs + 32 * half + 4 * j);
+  __syncthreads();
+#pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int s0 = 32 * half + 8 * c;
     float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      const float4 m = *reinterpret_cast<const float4 *>(Lm + t * kLs + s0 + j);
-      const float4 b = *reinterpret_cast<const float4 *>(&g.beta[s0 + j]);
-      x[j] = zero ? 0.f : (BETA ? m.x * b.x : m.x);
-      x[j + 1] = zero ? 0.f : (BETA ? m.y * b.y : m.y);
-      x[j + 2] = zero ? 0.f : (BETA ? m.z * b.z : m.z);
-      x[j + 3] = zero ? 0.f : (BETA ? m.w * b.w : m.w);
+    for (int j = 0; j < 2; ++j) {
+      const float4 y = m[2 * c + j];
+      const float4 b = BETA ? *reinterpret_cast<const float4 *>(&g.beta[32 * half + 8 * c + 4 * j])
+                            : make_float4(1.f, 1.f, 1.f, 1.f);
+      x[4 * j] = zero ? 0.f : y.x * b.x;
+      x[4 * j + 1] = zero ? 0.f : y.y * b.y;
+      x[4 * j + 2] = zero ? 0.f : y.z * b.z;
+      x[4 * j + 3] = zero ? 0.f : y.w * b.w;
     }
     store_split8(hi_tile, lo_tile, t, 4 * half + c, x);
   }
