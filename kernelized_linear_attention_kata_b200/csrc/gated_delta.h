@@ -37,6 +37,7 @@ struct GatedDeltaLaunch {
   unsigned *status = nullptr;
   int G = 1, seg_chunks = 0;
   float *F = nullptr, *B = nullptr, *seg_starts = nullptr;
+  uint8_t *img_S = nullptr, *img_D = nullptr, *img_dS = nullptr, *img_dR = nullptr;   // gradient, [BH][N]
   uint8_t *records = nullptr;      // what the solve leaves of each chunk [BH][N]
 };
 
@@ -56,7 +57,16 @@ template <typename Tin> cudaError_t simt_gated_delta_backward(const GatedDeltaLa
 bool gd_tc_shape(int d_k, int d_v);
 void gd_tc_split(long long BH, int N, int sms, int *G, int *seg_chunks);
 size_t gd_tc_record_bytes();
-cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k, bool with_beta);
+cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k);
+// Tensor-core gradient (same shapes): the saved images of states and writes.
+cudaError_t gd_tc_save(const GatedDeltaLaunch &a, int d_k, int d_v);
+cudaError_t gd_tc_reverse(const GatedDeltaLaunch &a, int d_k, int d_v);
+cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v);
+cudaError_t gd_tc_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
+// dq, dk of shared heads: the sums of the value heads' parts.
+cudaError_t gd_sum_groups(const GatedDeltaLaunch &a, int d_k, bool bf16);
+size_t gd_tc_state_image(int d_k, int d_v);
+size_t gd_tc_write_image(int d_v);
 cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v);
 template <typename Tin> cudaError_t gated_delta_step(const GatedDeltaStep &a, int d_k, int d_v);
 

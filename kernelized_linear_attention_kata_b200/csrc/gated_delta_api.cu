@@ -65,40 +65,52 @@ int sm_count() {
   return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
 }
 
+// The tensor-core forward's regions (the gradient's first pass needs them
+// too); false when the device cannot be asked for its size.
+bool place_chain(GatedDeltaLaunch &a, int d_k, int d_v, Regions &r) {
+  const int sms = sm_count();
+  if (sms <= 0) return false;
+  if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, sms, &a.G, &a.seg_chunks);
+  a.records = r.take_bytes((size_t)a.BH * a.N * gd_tc_record_bytes());
+  if (a.G > 1) {
+    a.F = r.take((size_t)a.BH * (a.G - 1) * d_k * d_k);
+    a.B = r.take((size_t)a.BH * (a.G - 1) * d_k * d_v);
+    a.seg_starts = r.take((size_t)a.BH * a.G * d_k * d_v);
+  }
+  return true;
+}
+
 // 0 when the device cannot be asked for its size
 size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, void *ws) {
   Regions r{static_cast<unsigned char *>(ws)};
-  if (on_tensor_cores(d_k, d_v, dtype)) {
-    const int sms = sm_count();
-    if (sms <= 0) return 0;
-    if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, sms, &a.G, &a.seg_chunks);
-    a.records = r.take_bytes((size_t)a.BH * a.N * gd_tc_record_bytes());
-    if (a.G > 1) {
-      a.F = r.take((size_t)a.BH * (a.G - 1) * d_k * d_k);
-      a.B = r.take((size_t)a.BH * (a.G - 1) * d_k * d_v);
-      a.seg_starts = r.take((size_t)a.BH * a.G * d_k * d_v);
-    }
-    return r.used;
-  }
+  if (on_tensor_cores(d_k, d_v, dtype)) return place_chain(a, d_k, d_v, r) ? r.used : 0;
   const size_t square = (size_t)a.BH * a.N * kGdChunk * kGdChunk;
   a.M = r.take(square);
   a.P = r.take(square);
   return r.used;
 }
 
-size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, void *ws) {
+size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, void *ws) {
   Regions r{static_cast<unsigned char *>(ws)};
   const size_t chunks = (size_t)a.BH * a.N, tokens = (size_t)a.BH * a.T;
+  if (a.H != a.Hk) {
+    a.dq_part = r.take(tokens * d_k);
+    a.dk_part = r.take(tokens * d_k);
+  }
+  if (on_tensor_cores(d_k, d_v, dtype)) {
+    if (!place_chain(a, d_k, d_v, r)) return 0;
+    a.img_S = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
+    a.img_dS = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
+    a.img_D = r.take_bytes(chunks * gd_tc_write_image(d_v));
+    a.img_dR = r.take_bytes(chunks * gd_tc_write_image(d_v));
+    return r.used;
+  }
   a.M = r.take(chunks * kGdChunk * kGdChunk);
   a.P = r.take(chunks * kGdChunk * kGdChunk);
   a.starts = r.take(chunks * d_k * d_v);
   a.ends = r.take(chunks * d_k * d_v);
   a.writes = r.take(tokens * d_v);
   a.dR = r.take(tokens * d_v);
-  if (a.H != a.Hk) {
-    a.dq_part = r.take(tokens * d_k);
-    a.dk_part = r.take(tokens * d_k);
-  }
   return r.used;
 }
 
@@ -176,7 +188,7 @@ size_t kata_bwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_
                                             kata_dtype_t dtype) {
   if (check_shape(B, H_k, H, T, d_k, d_v, dtype) != KATA_OK) return 0;
   GatedDeltaLaunch a = describe(B, H_k, H, T);
-  return place_backward(a, d_k, d_v, nullptr);
+  return place_backward(a, d_k, d_v, dtype, nullptr);
 }
 
 kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, const float *g,
@@ -188,20 +200,25 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
   const kata_status_t shape = check_shape(B, H_k, H, T, d_k, d_v, dtype);
   if (shape != KATA_OK) return shape;
   GatedDeltaLaunch a = describe(B, H_k, H, T);
-  const kata_status_t ws =
-      check_workspace(workspace, workspace_bytes, place_backward(a, d_k, d_v, workspace));
+  const size_t need = place_backward(a, d_k, d_v, dtype, workspace);
+  if (need == 0) return KATA_ERR_CUDA;
+  const kata_status_t ws = check_workspace(workspace, workspace_bytes, need);
   if (ws != KATA_OK) return ws;
   a.stream = reinterpret_cast<cudaStream_t>(stream_);
   const size_t state = (size_t)a.BH * d_k * d_v;
   if (overlap(dS, dS0, state) || overlap(S0, dS0, state)) return KATA_ERR_INVALID_ARGUMENT;
+  const bool tc = on_tensor_cores(d_k, d_v, dtype);
   if (a.BH > 0 && T > 0 &&
-      (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta))
+      (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta ||
+       (tc && !aligned16({q, k, v, dout, dq, dk, dv}))))
     return KATA_ERR_INVALID_ARGUMENT;
   if (cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
   if (a.BH == 0 || T == 0) return pass_state(dS, dS0, state, a.stream);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
   a.dout = dout; a.dS = dS; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
-  const cudaError_t e = dtype == KATA_DTYPE_F32
+  a.status = static_cast<unsigned *>(workspace);
+  const cudaError_t e = tc ? gd_tc_backward(a, d_k, d_v)
+                        : dtype == KATA_DTYPE_F32
                             ? simt_gated_delta_backward<float>(a, d_k, d_v)
                             : simt_gated_delta_backward<__nv_bfloat16>(a, d_k, d_v);
   return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;

@@ -1,0 +1,434 @@
+// The gradient of the gated delta rule on the tensor cores (bf16, d_k and d_v
+// in {64, 128}): the reverse chain, then the gradients of all chunks at once.
+//
+// The forward chain has saved each chunk's starting state S and writes D. With
+// dS' the gradient of a chunk's last state, last chunk first:
+//   dD = P^T dO + e^{G_C - G} (K dS'),  dR = M^T dD,  dV = beta dR,
+//   dS = e^{G_C} dS' + Q^T (e^G dO) - K^T (e^G dV).
+// As in the forward chain everything with a value axis is transposed (thread =
+// value column = TMEM lane), the state's gradient stays in registers, and
+// fp32 operands enter as two bf16 halves:
+//   K dS'      A = dS'^T (TMEM)          B = K tile, K-major
+//   P^T dO     A = dO tile, MN-major     B = [P hi; P lo] tiles, MN-major
+//   M^T dD     A = dD^T (TMEM)           B = [M hi; M lo], MN-major
+//   Q^T (..)   A = (e^G dO)^T (TMEM)     B = Q tile, MN-major
+//   K^T (..)   A = -(e^G dV)^T (TMEM)    B = K tile, MN-major
+// P^T dO of the next chunk and Q^T (e^G dO) run in the gaps of the chain. dS'
+// and dR are saved as bf16 halves for the second kernel.
+//
+// Warps (384 threads): 0-7 the value columns (two warpgroups, each half of the
+// keys or tokens), 8 the MMA issuer, 9 the loads, 10 the saves, 11 dV's stores.
+#include "common.cuh"
+#include "gated_delta_tc.cuh"
+#include "profile.h"
+#include "tma_host.h"
+
+namespace kata {
+namespace {
+
+using namespace gdtc;
+
+constexpr int kThreads = 384;
+constexpr int kStateWarps = 8;
+constexpr uint32_t kTmemCols = 512;
+// Columns: dS' operand and update accumulator; K dS', then dD; P^T dO in two
+// accumulators; M^T dD in two, the first then -(e^G dV); e^G dO.
+constexpr uint32_t kColS = 0, kColU = 128, kColX = 192, kColD = 320, kColG = 448;
+
+template <int DK, int DV> struct Layout {
+  static constexpr int NP = DK / 64, NV = DV / 64;
+  static constexpr int kKq = 2 * NP * kPanel;              // [K p0][Q p0][K p1][Q p1]
+  static constexpr int kTiles = 4 * kPanel;                // M hi, lo, P hi, lo
+  static constexpr int kDo = NV * kPanel;                  // dO panels, then dV in their place
+  static constexpr int kOffKq = 0;
+  static constexpr int kOffTiles = 2 * kKq;
+  static constexpr int kOffDo = kOffTiles + 2 * kTiles;
+  static constexpr int kStateHalf = (int)state_image(DK, DV) / 2, kWrites = (int)write_image(DV);
+  static constexpr int kOffStage = kOffDo + 2 * kDo;
+  static constexpr int kOffGates = kOffStage + (kStateHalf > kWrites ? kStateHalf : kWrites);
+  static constexpr int kOffBars = kOffGates + 2 * kRecGates;
+  static constexpr int kBytes = kOffBars + 512 + 1024;
+  // with d_v = 64 the dO operand's lanes 64-127 (not used) read the 8 KB behind it
+  static_assert(kOffDo + 2 * kDo + kPanel <= kOffBars + 512, "operand rows stay in shared memory");
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+enum {
+  kLoaded = 0, kFree = 2, kStored = 4, kSReady = 6, kXDone, kUDone, kDReady, kRDone, kZReady, kSDone,
+  kStaged, kSaved, kDvReady, kEnd, kNumBars
+};
+static_assert(8 * kNumBars + 8 <= 512, "barrier area");
+
+struct Args {
+  const float *dS;                 // nullable: the last state's gradient
+  float *dS0;                      // nullable
+  const uint8_t *records;
+  uint8_t *img_dS, *img_dR;
+  unsigned *status;
+  int H, Hk, T, N;
+};
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmdo, const __grid_constant__ CUtensorMap tmdv,
+                  const Args a) {
+  using L = Layout<DK, DV>;
+  constexpr int NP = L::NP, NV = L::NV;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBars);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const float *gates = reinterpret_cast<const float *>(smem + L::kOffGates);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int bh = blockIdx.x;
+  const int kh = bh / a.H * a.Hk + bh % a.H / (a.H / a.Hk);
+  const int n = a.N;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      uint32_t count = 1;
+      if (i == kFree || i == kFree + 1 || i == kSReady || i == kDReady || i == kZReady || i == kStaged ||
+          i == kDvReady)
+        count = kStateWarps;
+      mbar_init(&bars[i], count);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp < kStateWarps) {
+    // ------------------------------------------------------------ value columns
+    const int h = warp / 4;
+    const int r = 32 * (warp % 4) + lane;
+    const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
+    const bool active = r < DV;
+    constexpr int HK = DK / 2;
+    float2 S[HK / 2];                                      // dS'
+    {
+      const float *src = a.dS ? a.dS + (size_t)bh * DK * DV : nullptr;
+      auto entry = [&](int k) { return src && active ? src[(size_t)k * DV + r] : 0.f; };
+#pragma unroll
+      for (int i = 0; i < HK / 2; ++i) S[i] = make_float2(entry(HK * h + 2 * i), entry(HK * h + 2 * i + 1));
+    }
+    const uint32_t col_s = tbase + lane_off + kColS + HK * h;
+    const uint32_t col_half = tbase + lane_off + 32 * h;
+    uint8_t *stage = smem + L::kOffStage;
+    auto stage_free = [&](int use) -> bool {
+      return use == 0 || warp_wait(&bars[kSaved], (use - 1) & 1, abort_flag);
+    };
+    auto staged = [&]() {
+      fence_async_smem();
+      warp_arrive(&bars[kStaged]);
+    };
+    bool ok = true;
+
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      if (!(ok = warp_wait(&bars[kLoaded + st], (i >> 1) & 1, abort_flag))) break;
+      if (active) {
+#pragma unroll
+        for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      warp_arrive(&bars[kSReady]);
+      if (!(ok = stage_free(3 * i))) break;
+      if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
+      staged();
+
+      // e^G dO; its place in shared memory later takes dV
+      const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC, *beta = to_end + kC;
+      uint8_t *col = smem + L::kOffDo + st * L::kDo + (r / 64) * kPanel + (r % 8) * 2;
+      const int chunk = r % 64 / 8;
+      auto at = [&](int t) { return reinterpret_cast<uint16_t *>(col + sw128(t, chunk)); };
+      if (active) {
+        float2 y[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float4 f = gate4(from_start, 32 * h + 2 * j);
+          const int t = 32 * h + 2 * j;
+          y[j] = __fmul2_rn(make_float2(f.x, f.y), as_float2((uint32_t)*at(t) << 16, (uint32_t)*at(t + 1) << 16));
+          y[j + 1] = __fmul2_rn(make_float2(f.z, f.w),
+                                as_float2((uint32_t)*at(t + 2) << 16, (uint32_t)*at(t + 3) << 16));
+        }
+        put32(col_half + kColG, y);
+      }
+
+      // dD = P^T dO + e^{G_C - G} (K dS')
+      if (!(ok = warp_wait(&bars[kXDone], i & 1, abort_flag))) break;
+      if (!(ok = warp_wait(&bars[kUDone], i & 1, abort_flag))) break;
+      tc_fence_after();
+      if (active) {
+        uint32_t x[32], y[32];
+        float2 z[16];
+        tmem_ld32(col_half + kColX, x);
+        tmem_ld32(col_half + kColX + 64, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          z[j] = __fadd2_rn(as_float2(x[2 * j], x[2 * j + 1]), as_float2(y[2 * j], y[2 * j + 1]));
+        tmem_ld32(col_half + kColU, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float4 f = gate4(to_end, 32 * h + 2 * j);
+          z[j] = __ffma2_rn(make_float2(f.x, f.y), as_float2(x[2 * j], x[2 * j + 1]), z[j]);
+          z[j + 1] = __ffma2_rn(make_float2(f.z, f.w), as_float2(x[2 * j + 2], x[2 * j + 3]), z[j + 1]);
+        }
+        put32(col_half + kColU, z);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      warp_arrive(&bars[kDReady]);
+      if (!(ok = stage_free(3 * i + 1))) break;
+      if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
+      staged();
+
+      // dR = M^T dD, dV = beta dR
+      if (!(ok = warp_wait(&bars[kRDone], i & 1, abort_flag))) break;
+      tc_fence_after();
+      float2 d[16];
+      if (active) {
+        uint32_t x[32], y[32];
+        float2 z[16];
+        tmem_ld32(col_half + kColD, x);
+        tmem_ld32(col_half + kColD + 64, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float4 f = gate4(from_start, 32 * h + 2 * j), b = gate4(beta, 32 * h + 2 * j);
+          d[j] = __fadd2_rn(as_float2(x[2 * j], x[2 * j + 1]), as_float2(y[2 * j], y[2 * j + 1]));
+          d[j + 1] = __fadd2_rn(as_float2(x[2 * j + 2], x[2 * j + 3]), as_float2(y[2 * j + 2], y[2 * j + 3]));
+          z[j] = __fmul2_rn(make_float2(-f.x * b.x, -f.y * b.y), d[j]);
+          z[j + 1] = __fmul2_rn(make_float2(-f.z * b.z, -f.w * b.w), d[j + 1]);
+        }
+        put32(col_half + kColD, z);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      warp_arrive(&bars[kZReady]);
+      const float whole = from_start[kC - 1];
+      if (!(ok = stage_free(3 * i + 2))) break;
+      if (active) {
+        stage_row<4>(stage, DV, r, 32 * h, d, false);
+        stage_row<4>(stage + (size_t)DV * 128, DV, r, 32 * h, d, true);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int t = 32 * h + 2 * j;
+          *reinterpret_cast<__nv_bfloat16 *>(at(t)) = __float2bfloat16_rn(beta[t] * d[j].x);
+          *reinterpret_cast<__nv_bfloat16 *>(at(t + 1)) = __float2bfloat16_rn(beta[t + 1] * d[j].y);
+        }
+      }
+      staged();                                            // fences dV's writes too
+      warp_arrive(&bars[kDvReady]);
+
+      // dS = e^{G_C} dS' + Q^T (e^G dO) - K^T (e^G dV)
+      if (!(ok = warp_wait(&bars[kSDone], i & 1, abort_flag))) break;
+      tc_fence_after();
+      if (active) {
+        const float2 w2 = make_float2(whole, whole);
+#pragma unroll
+        for (int b = 0; b < HK / 32; ++b) {
+          uint32_t x[32];
+          tmem_ld32(col_s + 32 * b, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            S[16 * b + j] = __ffma2_rn(w2, S[16 * b + j], as_float2(x[2 * j], x[2 * j + 1]));
+        }
+      }
+      warp_arrive(&bars[kFree + st]);
+    }
+    if (active && ok && a.dS0) {
+      float *dst = a.dS0 + (size_t)bh * DK * DV;
+#pragma unroll
+      for (int i = 0; i < HK / 2; ++i) {
+        dst[(size_t)(HK * h + 2 * i) * DV + r] = S[i].x;
+        dst[(size_t)(HK * h + 2 * i + 1) * DV + r] = S[i].y;
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t id_u = idesc_bf16(128, 64, false, false);       // K-major right operand
+    constexpr uint32_t id_x = idesc_bf16(128, 128, true, true);        // both MN-major
+    constexpr uint32_t id_r128 = idesc_bf16(128, 128, false, true), id_r64 = idesc_bf16(128, 64, false, true);
+    constexpr uint32_t id_up = idesc_bf16(128, DK, false, true);
+    const bool leader = lane == 0;
+    const uint32_t base = smem_u32(smem);
+    auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
+    // P^T dO of round i, in two accumulators
+    auto issue_x = [&](int i) -> bool {
+      const int st = i & 1;
+      if (!warp_wait(&bars[kLoaded + st], (i >> 1) & 1, abort_flag)) return false;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t d_do = smem_desc(base + L::kOffDo + st * L::kDo, kPanel, 1024, kSw128);
+        const uint64_t d_p = smem_desc(base + L::kOffTiles + st * L::kTiles + 2 * kPanel, kPanel, 1024, kSw128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tbase + kColX, adv(d_do, k * 2048), adv(d_p, k * 2048), id_x, k > 0);
+        mma_commit(&bars[kXDone]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = n == 0 || issue_x(0);
+    for (int i = 0; i < n && ok; ++i) {
+      const int st = i & 1;
+      const uint64_t d_k = smem_desc(base + L::kOffKq + st * L::kKq, 16, 1024, kSw128);
+      const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, 2 * kPanel, 1024, kSw128);
+      const uint64_t d_q_mn = adv(d_k_mn, kPanel);
+      const uint64_t d_m = smem_desc(base + L::kOffTiles + st * L::kTiles, kPanel, 1024, kSw128);
+      if (!(ok = warp_wait(&bars[kSReady], i & 1, abort_flag))) break;
+      tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k)
+            mma_ts(tbase + kColU, tbase + kColS + 16 * k + 8 * lo, adv(d_k, (k / 4) * 2 * kPanel + (k % 4) * 32),
+                   id_u, lo > 0 || k > 0);
+        mma_commit(&bars[kUDone]);
+      }
+      if (!(ok = warp_wait(&bars[kDReady], i & 1, abort_flag))) break;
+      tc_fence_after();
+      if (leader) {
+        // dD hi against [M hi; M lo] in two accumulators, dD lo against M hi
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tbase + kColD, tbase + kColU + 16 * k + 8 * lo, adv(d_m, k * 2048), lo ? id_r64 : id_r128,
+                   lo > 0 || k > 0);
+        mma_commit(&bars[kRDone]);
+        // dS' has been read (its products are done, or dD would not be ready)
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tbase + kColS, tbase + kColG + 16 * k + 8 * lo, adv(d_q_mn, k * 2048), id_up, lo > 0 || k > 0);
+      }
+      if (!(ok = warp_wait(&bars[kZReady], i & 1, abort_flag))) break;
+      tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tbase + kColS, tbase + kColD + 16 * k + 8 * lo, adv(d_k_mn, k * 2048), id_up, 1);
+        mma_commit(&bars[kSDone]);
+      }
+      __syncwarp();
+      if (i + 1 < n) ok = issue_x(i + 1);                  // in the gap before the next K dS'
+    }
+    if (!ok && leader) {
+      mma_commit(&bars[kEnd]);
+      drain(&bars[kEnd], 0);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- loads, last chunk first
+      tma_prefetch_desc(&tmk);
+      tma_prefetch_desc(&tmq);
+      tma_prefetch_desc(&tmdo);
+      int sent = 0;
+      for (int i = 0; i < n; ++i) {
+        const int st = i & 1, c = n - 1 - i, row = kC * c;
+        if (i >= 2 && (!mbar_wait(&bars[kFree + st], ((i >> 1) - 1) & 1, abort_flag) ||
+                       !mbar_wait(&bars[kStored + st], ((i >> 1) - 1) & 1, abort_flag)))
+          break;
+        uint8_t *kq = smem + L::kOffKq + st * L::kKq, *dO = smem + L::kOffDo + st * L::kDo;
+        const uint8_t *rec = a.records + ((size_t)bh * a.N + c) * kRecBytes;
+        mbar_arrive_expect_tx(&bars[kLoaded + st], L::kKq + kRecGates + L::kTiles + L::kDo);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          tma_load_3d(kq + 2 * p * kPanel, &tmk, &bars[kLoaded + st], 64 * p, row, kh);
+          tma_load_3d(kq + (2 * p + 1) * kPanel, &tmq, &bars[kLoaded + st], 64 * p, row, kh);
+        }
+#pragma unroll
+        for (int p = 0; p < NV; ++p) tma_load_3d(dO + p * kPanel, &tmdo, &bars[kLoaded + st], 64 * p, row, bh);
+        bulk_load(smem + L::kOffGates + st * kRecGates, rec, kRecGates, &bars[kLoaded + st]);
+        bulk_load(smem + L::kOffTiles + st * L::kTiles, rec + kRecM, L::kTiles, &bars[kLoaded + st]);
+        sent = i + 1;
+      }
+      if (*abort_flag)
+        for (int i = sent > 2 ? sent - 2 : 0; i < sent; ++i) drain(&bars[kLoaded + (i & 1)], (i >> 1) & 1);
+    }
+  } else if (warp == 10) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- saves: dS' hi, lo, dR
+      for (int use = 0; use < 3 * n; ++use) {
+        if (!mbar_wait(&bars[kStaged], use & 1, abort_flag)) break;
+        const int part = use % 3;
+        const size_t at = (size_t)bh * a.N + (n - 1 - use / 3);
+        if (part < 2)
+          bulk_store(a.img_dS + at * state_image(DK, DV) + part * L::kStateHalf, smem + L::kOffStage, L::kStateHalf);
+        else
+          bulk_store(a.img_dR + at * write_image(DV), smem + L::kOffStage, L::kWrites);
+        bulk_commit_group();
+        bulk_wait_read_all();
+        mbar_arrive(&bars[kSaved]);
+      }
+      bulk_wait_all();
+    }
+  } else {
+    if (lane == 0) {
+      // ---------------------------------------------------------- dV's stores
+      tma_prefetch_desc(&tmdv);
+      for (int i = 0; i < n; ++i) {
+        if (!mbar_wait(&bars[kDvReady], i & 1, abort_flag)) break;
+#pragma unroll
+        for (int p = 0; p < NV; ++p)
+          tma_store_3d(&tmdv, smem + L::kOffDo + (i & 1) * L::kDo + p * kPanel, 64 * p, kC * (n - 1 - i), bh);
+        bulk_commit_group();
+        bulk_wait_read_all();
+        mbar_arrive(&bars[kStored + (i & 1)]);
+      }
+      bulk_wait_all();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tbase, kTmemCols);
+  if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
+}
+
+template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a) {
+  CUtensorMap tq, tk, tdo, tdv;
+  const long long BHk = a.BH / a.H * a.Hk;
+  if (!make_tma_3d_bf16_box(&tq, a.q, DK, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tk, a.k, DK, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tdo, a.dout, DV, a.T, a.BH, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tdv, a.dv, DV, a.T, a.BH, 64, kC, true))
+    return cudaErrorInvalidValue;
+  constexpr int bytes = Layout<DK, DV>::kBytes;
+  auto kern = gd_reverse_kernel<DK, DV>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const Args x{a.dS, a.dS0, a.records, a.img_dS, a.img_dR, a.status, a.H, a.Hk, a.T, a.N};
+  ProfileScope prof("gd_tc_reverse", a.stream);
+  kern<<<(unsigned)a.BH, kThreads, bytes, a.stream>>>(tq, tk, tdo, tdv, x);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t gd_tc_reverse(const GatedDeltaLaunch &a, int d_k, int d_v) {
+  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a) : launch<64, 128>(a);
+  return d_v == 64 ? launch<128, 64>(a) : launch<128, 128>(a);
+}
+
+}  // namespace kata

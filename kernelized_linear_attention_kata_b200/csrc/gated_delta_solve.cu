@@ -34,7 +34,7 @@ template <int DK> struct SolveLayout {
   static constexpr int kBytes = kOffBars + 64 + 1024;
 };
 
-template <int DK, bool BETA>
+template <int DK>
 __global__ void __launch_bounds__(kSolveThreads, 6)
 gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                    const float *__restrict__ g, const float *__restrict__ beta,
@@ -130,7 +130,7 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   }
   __syncthreads();
   invert_corner(Lm);
-  store_inverse<BETA>(Lm, gt, smem + L::kOffL, smem + L::kOffL + kPanel);
+  store_inverse(Lm, smem + L::kOffL, smem + L::kOffL + kPanel);
   fence_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -138,7 +138,7 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   if (w == 2) tmem_dealloc(tbase, 64);
   if (threadIdx.x == 0) {
     uint8_t *rec = records + (size_t)blockIdx.x * kRecBytes;
-    bulk_store(rec, gt.from_start, kRecGates);             // from_start, to_end
+    bulk_store(rec, gt.from_start, kRecGates);             // from_start, to_end, beta
     bulk_store(rec + kRecP, smem + L::kOffP, 2 * kPanel);
     bulk_store(rec + kRecM, smem + L::kOffL, 2 * kPanel);
     bulk_commit_group();
@@ -147,14 +147,14 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   }
 }
 
-template <int DK, bool BETA> cudaError_t launch(const GatedDeltaLaunch &a) {
+template <int DK> cudaError_t launch(const GatedDeltaLaunch &a) {
   using L = SolveLayout<DK>;
   CUtensorMap tq, tk;
   const long long BHk = a.BH / a.H * a.Hk;
   if (!make_tma_3d_bf16_box(&tq, a.q, DK, a.T, BHk, 64, kC, true) ||
       !make_tma_3d_bf16_box(&tk, a.k, DK, a.T, BHk, 64, kC, true))
     return cudaErrorInvalidValue;
-  auto kern = gd_solve_tc_kernel<DK, BETA>;
+  auto kern = gd_solve_tc_kernel<DK>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   ProfileScope prof("gd_tc_solve", a.stream);
@@ -167,9 +167,6 @@ template <int DK, bool BETA> cudaError_t launch(const GatedDeltaLaunch &a) {
 
 size_t gd_tc_record_bytes() { return kRecBytes; }
 
-cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k, bool with_beta) {
-  if (d_k == 64) return with_beta ? launch<64, true>(a) : launch<64, false>(a);
-  return with_beta ? launch<128, true>(a) : launch<128, false>(a);
-}
+cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k) { return d_k == 64 ? launch<64>(a) : launch<128>(a); }
 
 }  // namespace kata

@@ -4,7 +4,7 @@
 // Per chunk, from its starting state S [d_k, d_v] (fp32), with G the running
 // sum of g, W_ts = e^{G_t - G_s} (s <= t), M = (I + L)^-1, L_ts = beta_t W_ts
 // k_t.k_s (s < t) and P_ts = W_ts q_t.k_s (s <= t):
-//   R = V - e^G (K S),  D = M diag(beta) R,
+//   R = beta (V - e^G (K S)),  D = M R,
 //   O = e^G (Q S) + P D,  S' = e^{G_C} S + K^T (e^{G_C - G} D).
 //
 // Everything with a value axis is held transposed: thread r of a warpgroup
@@ -14,7 +14,7 @@
 // Q, M, P) is a shared-memory tile, and the state itself stays in registers
 // from the first chunk to the last:
 //   [K; Q] S      A = S^T (TMEM)           B = K, Q tiles, K-major
-//   M beta R      A = R^T (TMEM)           B = M diag(beta) tile
+//   M R           A = R^T (TMEM)           B = M tile
 //   K^T D~        A = (e^{G_C-G} D)^T      B = K tile, MN-major
 //   P D           A = D^T                  B = P tile
 // fp32 operands enter as two bf16 halves (hi + lo, 16 bits); q, k and v are
@@ -29,7 +29,8 @@
 // segments: each but the last is first walked for its effect on a state, S_end =
 // F S_start + B (the same kernel without outputs, once on V from S = 0 and once
 // with V = 0 from S = I), a small kernel joins them, and the segments then run
-// side by side.
+// side by side. For the gradient the same kernel without outputs saves every
+// chunk's S and D (gated_delta_bwd_tc.cu).
 //
 // An issuing thread gets an MMA out every 75-95 cycles whatever its N, so N is
 // 128 wherever two tiles lie side by side: K and Q rows, the two 64-key panels
@@ -57,14 +58,23 @@ constexpr uint32_t kTmemCols = 512;
 // rewrites only the columns it has read.
 constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColD = 256, kColDl = 320, kColO = 384;
 
-template <int DK, int DV> struct Layout {
+// kOut: outputs of segments 0 .. G - 1. kEffect: the effect of segments 0 .. G - 2
+// on a state; blockIdx picks the kind (0: B, from V and S = 0; 1: F, from S = I).
+// kSave: each chunk's starting state and writes for the gradient.
+enum Mode { kOut, kEffect, kSave };
+
+template <int DK, int DV, int MODE> struct Layout {
   static constexpr int NP = DK / 64;                       // panels of a K or Q tile
-  static constexpr int kKq = 2 * NP * kPanel;              // [K p0][Q p0][K p1][Q p1]
+  static constexpr int kStride = (MODE == kOut ? 2 : 1) * kPanel;   // [K p0][Q p0][K p1][Q p1] or K alone
+  static constexpr int kKq = NP * kStride;
+  static constexpr int kTiles = (MODE == kOut ? 4 : 2) * kPanel;    // M hi, lo, P hi, lo
   static constexpr int kV = kC * DV * 2;                   // V, then the outputs in its place
   static constexpr int kOffKq = 0;
-  static constexpr int kOffTiles = 2 * kKq;                // two stages of M hi, lo, P hi, lo
-  static constexpr int kOffV = kOffTiles + 8 * kPanel;
-  static constexpr int kOffGates = kOffV + 2 * kV;         // two stages
+  static constexpr int kOffTiles = 2 * kKq;                // two stages of all three
+  static constexpr int kOffV = kOffTiles + 2 * kTiles;
+  static constexpr int kOffStage = kOffV + 2 * kV;         // what is being saved: half an image
+  static constexpr int kStateHalf = (int)state_image(DK, DV) / 2, kWrites = (int)write_image(DV);
+  static constexpr int kOffGates = kOffStage + (MODE != kSave ? 0 : kStateHalf > kWrites ? kStateHalf : kWrites);
   static constexpr int kOffBars = kOffGates + 2 * kRecGates;
   static constexpr int kBytes = kOffBars + 512 + 1024;     // barriers, alignment slack
   static_assert(kBytes <= 232448, "shared memory budget");
@@ -75,13 +85,14 @@ template <int DK, int DV> struct Layout {
 // the loads and fold them into their own arrivals.
 enum {
   kKqFull = 0, kVFull = 2, kFree = 4, kStored = 6, kSReady = 8, kKsDone, kRReady, kDDone, kDtReady, kDlReady,
-  kUDone, kODone, kEnd, kNumBars
+  kUDone, kODone, kStaged, kSaved, kEnd, kNumBars
 };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
 
 struct Args {
   const float *g, *beta, *S0;
   float *S_out;
+  uint8_t *img_S, *img_D;          // kSave
   float *F, *B;                    // segments' effects [BH][G - 1][..]: kind 1 and kind 0
   const uint8_t *records;          // [BH][N]
   const float *starts;             // segments' starting states [BH][G][d_k][d_v], 1 .. G - 1 used
@@ -89,15 +100,14 @@ struct Args {
   int H, Hk, T, N, G, seg_chunks;
 };
 
-// OUT: outputs of segments 0 .. G - 1. !OUT: the effect of segments 0 .. G - 2
-// on a state; blockIdx picks the kind (0: B, from V and S = 0; 1: F, from S = I).
-template <int DK, int DV, bool OUT>
+template <int DK, int DV, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
              const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
              const Args a) {
-  using L = Layout<DK, DV>;
+  using L = Layout<DK, DV, MODE>;
   constexpr int NP = L::NP;
+  constexpr bool OUT = MODE == kOut, SAVE = MODE == kSave;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
@@ -107,9 +117,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   const float *gates = reinterpret_cast<const float *>(smem + L::kOffGates);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int segs = OUT ? a.G : a.G - 1;
-  const int kind = OUT ? 0 : (int)(blockIdx.x % 2);
-  const int job = OUT ? (int)blockIdx.x : (int)(blockIdx.x / 2);
+  const int segs = MODE == kEffect ? a.G - 1 : a.G;
+  const int kind = MODE == kEffect ? (int)(blockIdx.x % 2) : 0;
+  const int job = MODE == kEffect ? (int)(blockIdx.x / 2) : (int)blockIdx.x;
   const int seg = job % segs;
   const int bh = job / segs;
   const int kh = bh / a.H * a.Hk + bh % a.H / (a.H / a.Hk);
@@ -117,12 +127,13 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   const int t_left = a.T - t_begin;
   const int nall = t_left <= 0 ? 0 : (t_left - 1) / kC + 1;
   const int n = nall < a.seg_chunks ? nall : a.seg_chunks;
-  const bool values = OUT || kind == 0;                    // V is read
+  const bool values = MODE != kEffect || kind == 0;                    // V is read
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kFree || i == kFree + 1 || i == kSReady || i == kRReady || i == kDtReady || i == kDlReady)
+      if (i == kFree || i == kFree + 1 || i == kSReady || i == kRReady || i == kDtReady || i == kDlReady ||
+          i == kStaged)
         count = kStateWarps;
       mbar_init(&bars[i], count);
     }
@@ -149,7 +160,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     float2 S[HK / 2];
     {
       const float *src = nullptr;
-      if (OUT)
+      if (MODE != kEffect)
         src = seg == 0 ? (a.S0 ? a.S0 + (size_t)bh * DK * DV : nullptr)
                        : a.starts + ((size_t)bh * a.G + seg) * DK * DV;
       auto entry = [&](int k) {
@@ -162,14 +173,15 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     const uint32_t col_half = tbase + lane_off + 32 * h;           // + a 64-token region
     bool ok = true;
 
-    // 32 values of a row as an operand, in 16-deep steps of hi, then lo
-    auto put32 = [&](uint32_t col, const float2 *x) {
-      uint32_t y[32];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) split2(x[i], y[16 * (i / 8) + i % 8], y[16 * (i / 8) + 8 + i % 8]);
-      tmem_st32(col, y);
+    // the staging buffer takes three parts a chunk: S hi, S lo, D
+    uint8_t *stage = smem + L::kOffStage;
+    auto stage_free = [&](int use) -> bool {
+      return use == 0 || warp_wait(&bars[kSaved], (use - 1) & 1, abort_flag);
     };
-    auto gate4 = [](const float *g, int i) { return *reinterpret_cast<const float4 *>(g + i); };
+    auto staged = [&]() {
+      fence_async_smem();
+      warp_arrive(&bars[kStaged]);
+    };
     // outputs of chunk c, o_t = e^{G_t} (Q S)_t + (P D)_t, 32 tokens a thread,
     // into the places its values of V were read from
     auto outputs = [&](int c) -> bool {
@@ -203,12 +215,17 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tc_fence_before();
         warp_arrive(&bars[kSReady]);
       }
+      if (SAVE) {
+        if (!(ok = stage_free(3 * c))) break;
+        if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
+        staged();
+      }
       if (OUT && c > 0 && (DK == 128 || c == n) && !(ok = outputs(c - 1))) break;
       if (c == n) break;
 
-      // R = V - e^G (K S)
+      // R = beta (V - e^G (K S))
       if (values && !(ok = warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag))) break;
-      const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC;
+      const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC, *beta = to_end + kC;
       uint32_t V[16];                                      // two tokens a register
       {
         const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + st * L::kV) + 32 * h * DV + r;
@@ -225,11 +242,13 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const float4 f = gate4(from_start, 32 * h + 2 * i);
+          const float4 f = gate4(from_start, 32 * h + 2 * i), b = gate4(beta, 32 * h + 2 * i);
           y[i] = __ffma2_rn(make_float2(-f.x, -f.y), as_float2(x[2 * i], x[2 * i + 1]),
                             as_float2(V[i] << 16, V[i] & 0xffff0000u));
           y[i + 1] = __ffma2_rn(make_float2(-f.z, -f.w), as_float2(x[2 * i + 2], x[2 * i + 3]),
                                 as_float2(V[i + 1] << 16, V[i + 1] & 0xffff0000u));
+          y[i] = __fmul2_rn(make_float2(b.x, b.y), y[i]);
+          y[i + 1] = __fmul2_rn(make_float2(b.z, b.w), y[i + 1]);
         }
         put32(col_half + kColKS, y);
         tmem_wait_st();
@@ -253,6 +272,12 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         }
         tmem_st32(col_half + kColO, x);
         tmem_wait_st();
+      }
+
+      if (SAVE) {
+        if (!(ok = stage_free(3 * c + 1))) break;
+        if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
+        staged();
       }
 
       // D, from its two accumulators: scaled for the update first, as it is
@@ -289,6 +314,15 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         warp_arrive(&bars[kDlReady]);
       }
 
+      if (SAVE) {
+        if (!(ok = stage_free(3 * c + 2))) break;
+        if (active) {
+          stage_row<4>(stage, DV, r, 32 * h, d, false);
+          stage_row<4>(stage + (size_t)DV * 128, DV, r, 32 * h, d, true);
+        }
+        staged();
+      }
+
       // S' = e^{G_C} S + K^T D~
       if (!(ok = warp_wait(&bars[kUDone], c & 1, abort_flag))) break;
       tc_fence_after();
@@ -307,8 +341,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     if (active && ok) {
       float *dst = nullptr;
       int ld = DV;
-      if (OUT) {
-        if (seg == a.G - 1 && a.S_out) dst = a.S_out + (size_t)bh * DK * DV;
+      if (MODE != kEffect) {
+        if (OUT && seg == a.G - 1 && a.S_out) dst = a.S_out + (size_t)bh * DK * DV;
       } else if (kind == 0) {
         dst = a.B + ((size_t)bh * segs + seg) * DK * DV;
       } else {
@@ -339,8 +373,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     for (int c = 0; c < n; ++c) {
       const int st = c & 1;
       const uint64_t d_kq = smem_desc(base + L::kOffKq + st * L::kKq, 16, 1024, kSw128);
-      const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, 2 * kPanel, 1024, kSw128);
-      const uint64_t d_m = smem_desc(base + L::kOffTiles + st * 4 * kPanel, 16, 1024, kSw128);
+      const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, L::kStride, 1024, kSw128);
+      const uint64_t d_m = smem_desc(base + L::kOffTiles + st * L::kTiles, 16, 1024, kSw128);
       const uint64_t d_p = adv(d_m, 2 * kPanel);
       if (!(ok = warp_wait(&bars[kSReady], c & 1, abort_flag))) break;
       tc_fence_after();
@@ -351,7 +385,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k)
-            mma_ts(tbase + kColKS, tbase + kColS + 16 * k + 8 * lo, adv(d_kq, (k / 4) * 2 * kPanel + (k % 4) * 32),
+            mma_ts(tbase + kColKS, tbase + kColS + 16 * k + 8 * lo, adv(d_kq, (k / 4) * L::kStride + (k % 4) * 32),
                    OUT ? id_128 : id_64, lo > 0 || k > 0);
         mma_commit(&bars[kKsDone]);
       }
@@ -403,21 +437,20 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       if (OUT) tma_prefetch_desc(&tmq);
       if (values) tma_prefetch_desc(&tmv);
       const uint8_t *rec = a.records + ((size_t)bh * a.N + (size_t)seg * a.seg_chunks) * kRecBytes;
-      constexpr uint32_t tiles = (OUT ? 4 : 2) * kPanel;
       int sent = 0;
       for (int c = 0; c < n; ++c) {
         const int st = c & 1, row = t_begin + kC * c;
         if (c >= 2 && !mbar_wait(&bars[kFree + st], ((c >> 1) - 1) & 1, abort_flag)) break;
         uint8_t *kq = smem + L::kOffKq + st * L::kKq;
-        mbar_arrive_expect_tx(&bars[kKqFull + st], (OUT ? L::kKq : L::kKq / 2) + kRecGates + tiles);
+        mbar_arrive_expect_tx(&bars[kKqFull + st], L::kKq + kRecGates + L::kTiles);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          tma_load_3d(kq + 2 * p * kPanel, &tmk, &bars[kKqFull + st], 64 * p, row, kh);
-          if (OUT) tma_load_3d(kq + (2 * p + 1) * kPanel, &tmq, &bars[kKqFull + st], 64 * p, row, kh);
+          tma_load_3d(kq + p * L::kStride, &tmk, &bars[kKqFull + st], 64 * p, row, kh);
+          if (OUT) tma_load_3d(kq + p * L::kStride + kPanel, &tmq, &bars[kKqFull + st], 64 * p, row, kh);
         }
         bulk_load(smem + L::kOffGates + st * kRecGates, rec + (size_t)c * kRecBytes, kRecGates,
                   &bars[kKqFull + st]);
-        bulk_load(smem + L::kOffTiles + st * 4 * kPanel, rec + (size_t)c * kRecBytes + kRecM, tiles,
+        bulk_load(smem + L::kOffTiles + st * L::kTiles, rec + (size_t)c * kRecBytes + kRecM, L::kTiles,
                   &bars[kKqFull + st]);
         sent = c + 1;
         if (values) {
@@ -442,6 +475,24 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         bulk_commit_group();
         bulk_wait_read_all();
         mbar_arrive(&bars[kStored + (c & 1)]);
+      }
+      bulk_wait_all();
+    }
+  } else if (SAVE && warp == 10) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- saves
+      const size_t first = (size_t)bh * a.N + (size_t)seg * a.seg_chunks;
+      for (int use = 0; use < 3 * n; ++use) {
+        if (!mbar_wait(&bars[kStaged], use & 1, abort_flag)) break;
+        const int part = use % 3;
+        const size_t at = first + use / 3;
+        if (part < 2)
+          bulk_store(a.img_S + at * state_image(DK, DV) + part * L::kStateHalf, smem + L::kOffStage, L::kStateHalf);
+        else
+          bulk_store(a.img_D + at * write_image(DV), smem + L::kOffStage, L::kWrites);
+        bulk_commit_group();
+        bulk_wait_read_all();
+        mbar_arrive(&bars[kSaved]);
       }
       bulk_wait_all();
     }
@@ -496,40 +547,43 @@ gd_join_kernel(const float *__restrict__ F, const float *__restrict__ B, const f
   }
 }
 
+template <int DK, int DV, int MODE>
+cudaError_t run_chain(const char *name, const GatedDeltaLaunch &a, const CUtensorMap *maps, const Args &x,
+                      long long blocks) {
+  constexpr int bytes = Layout<DK, DV, MODE>::kBytes;
+  auto kern = gd_tc_kernel<DK, DV, MODE>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  ProfileScope prof(name, a.stream);
+  kern<<<(unsigned)blocks, kThreads, bytes, a.stream>>>(maps[0], maps[1], maps[2], maps[3], x);
+  return cudaGetLastError();
+}
+
+// The solve, the segments' starting states, then the outputs or the saves.
 template <int DK, int DV>
-cudaError_t launch(const GatedDeltaLaunch &a) {
-  using L = Layout<DK, DV>;
-  CUtensorMap tq, tk, tv, to;
+cudaError_t launch(const GatedDeltaLaunch &a, bool save) {
+  CUtensorMap m[4];
   const long long BHk = a.BH / a.H * a.Hk;
-  if (!make_tma_3d_bf16_box(&tq, a.q, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tk, a.k, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tv, a.v, DV, a.T, a.BH, DV, kC, false) ||
-      !make_tma_3d_bf16_box(&to, a.o, DV, a.T, a.BH, DV, kC, false))
+  void *o = save ? const_cast<void *>(a.v) : a.o;          // no outputs: the map is not used
+  if (!make_tma_3d_bf16_box(&m[0], a.q, DK, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&m[1], a.k, DK, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&m[2], a.v, DV, a.T, a.BH, DV, kC, false) ||
+      !make_tma_3d_bf16_box(&m[3], o, DV, a.T, a.BH, DV, kC, false))
     return cudaErrorInvalidValue;
-  Args x{a.g, a.beta, a.S0, a.S_out, a.F, a.B, a.records, a.seg_starts,
-         a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks};
-  cudaError_t se = gd_tc_solve(a, DK, true);
-  if (se != cudaSuccess) return se;
+  const Args x{a.g, a.beta, a.S0, a.S_out, a.img_S, a.img_D, a.F, a.B, a.records, a.seg_starts,
+               a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks};
+  cudaError_t e = gd_tc_solve(a, DK);
+  if (e != cudaSuccess) return e;
   if (a.G > 1) {
-    auto kern = gd_tc_kernel<DK, DV, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    e = run_chain<DK, DV, kEffect>("gd_tc_segment", a, m, x, a.BH * (a.G - 1) * 2);
     if (e != cudaSuccess) return e;
-    {
-      ProfileScope prof("gd_tc_segment", a.stream);
-      kern<<<(unsigned)(a.BH * (a.G - 1) * 2), kThreads, L::kBytes, a.stream>>>(tq, tk, tv, to, x);
-    }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ProfileScope prof("gd_join", a.stream);
     gd_join_kernel<DK><<<(unsigned)(a.BH * (DV / kJoinCols)), 256, 0, a.stream>>>(
         a.F, a.B, a.S0, a.seg_starts, a.G, DV);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  auto kern = gd_tc_kernel<DK, DV, true>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-  if (e != cudaSuccess) return e;
-  ProfileScope prof("gd_tc_forward", a.stream);
-  kern<<<(unsigned)(a.BH * a.G), kThreads, L::kBytes, a.stream>>>(tq, tk, tv, to, x);
-  return cudaGetLastError();
+  return save ? run_chain<DK, DV, kSave>("gd_tc_save", a, m, x, a.BH * a.G)
+              : run_chain<DK, DV, kOut>("gd_tc_forward", a, m, x, a.BH * a.G);
 }
 
 }  // namespace
@@ -559,8 +613,14 @@ void gd_tc_split(long long BH, int N, int sms, int *G, int *seg_chunks) {
 }
 
 cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v) {
-  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a) : launch<64, 128>(a);
-  return d_v == 64 ? launch<128, 64>(a) : launch<128, 128>(a);
+  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a, false) : launch<64, 128>(a, false);
+  return d_v == 64 ? launch<128, 64>(a, false) : launch<128, 128>(a, false);
 }
+cudaError_t gd_tc_save(const GatedDeltaLaunch &a, int d_k, int d_v) {
+  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a, true) : launch<64, 128>(a, true);
+  return d_v == 64 ? launch<128, 64>(a, true) : launch<128, 128>(a, true);
+}
+size_t gd_tc_state_image(int d_k, int d_v) { return state_image(d_k, d_v); }
+size_t gd_tc_write_image(int d_v) { return write_image(d_v); }
 
 }  // namespace kata

@@ -60,10 +60,10 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *smem_src, uint
 }
 
 // What the chains need of a chunk beside q, k and v, as the solve leaves it in
-// the workspace: e^{G_t} and e^{G_C - G_t}, then 64 x 64 bf16 tiles in the
-// layout of an MMA operand (128-byte rows, 128B swizzle), each as hi and lo:
-// M (times diag(beta) for the forward), then P.
-constexpr int kRecGates = 2 * kC * 4;
+// the workspace: e^{G_t}, e^{G_C - G_t} and beta_t, then 64 x 64 bf16 tiles in
+// the layout of an MMA operand (128-byte rows, 128B swizzle), each as hi and
+// lo: M, then P.
+constexpr int kRecGates = 3 * kC * 4;
 constexpr int kRecM = kRecGates, kRecP = kRecM + 2 * kPanel, kRecBytes = kRecP + 2 * kPanel;
 
 // Byte offset of 16-byte chunk c of row r in a 128-byte-row tile, 128B swizzle.
@@ -80,9 +80,9 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) {
 struct Gates {
   float from_start[kC];              // e^{G_t}
   float to_end[kC];                  // e^{G_C - G_t}
+  float beta[kC];
   float hi[kC], lo[kC];              // G_t
   float to_block[kC];                // e^{G_a - G_t}, a = t | 7
-  float beta[kC];
 };
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -283,11 +283,8 @@ __device__ __forceinline__ void store_split8(uint8_t *hi_tile, uint8_t *lo_tile,
   *reinterpret_cast<uint4 *>(lo_tile + sw128(row, c)) = l;
 }
 
-// The inverse times diag(beta) (BETA) as bf16 hi / lo tiles, two threads a row.
-// The tiles may lie over Lm.
-template <bool BETA>
-__device__ __forceinline__ void store_inverse(const float *Lm, const Gates &g, uint8_t *hi_tile,
-                                              uint8_t *lo_tile) {
+// The inverse as bf16 hi / lo tiles, two threads a row. The tiles may lie over Lm.
+__device__ __forceinline__ void store_inverse(const float *Lm, uint8_t *hi_tile, uint8_t *lo_tile) {
   const int i = threadIdx.x % 128, t = i / 2, half = i % 2;
   const bool zero = t < 32 && half == 1;
   float4 m[8];
@@ -296,20 +293,42 @@ __device__ __forceinline__ void store_inverse(const float *Lm, const Gates &g, u
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    float x[8];
+    const float4 a = m[2 * c], b = m[2 * c + 1];
+    float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float4 y = m[2 * c + j];
-      const float4 b = BETA ? *reinterpret_cast<const float4 *>(&g.beta[32 * half + 8 * c + 4 * j])
-                            : make_float4(1.f, 1.f, 1.f, 1.f);
-      x[4 * j] = zero ? 0.f : y.x * b.x;
-      x[4 * j + 1] = zero ? 0.f : y.y * b.y;
-      x[4 * j + 2] = zero ? 0.f : y.z * b.z;
-      x[4 * j + 3] = zero ? 0.f : y.w * b.w;
-    }
+    for (int j = 0; j < 8; ++j) x[j] = zero ? 0.f : x[j];
     store_split8(hi_tile, lo_tile, t, 4 * half + c, x);
   }
 }
+
+// 32 values of a thread's row (one TMEM lane) as an operand, in 16-deep steps
+// of hi, then lo.
+__device__ __forceinline__ void put32(uint32_t col, const float2 *x) {
+  uint32_t y[32];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) split2(x[i], y[16 * (i / 8) + i % 8], y[16 * (i / 8) + 8 + i % 8]);
+  tmem_st32(col, y);
+}
+// 8 x COUNT values of row `row` of a saved image (128-byte rows, 64 values a
+// panel of `rows` rows), from value `first`; the hi or the lo halves.
+template <int COUNT>
+__device__ __forceinline__ void stage_row(uint8_t *image, int rows, int row, int first, const float2 *x, bool lo_half) {
+#pragma unroll
+  for (int j = 0; j < COUNT; ++j) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2(x[4 * j + i], h[i], l[i]);
+    const int at = first + 8 * j;
+    *reinterpret_cast<uint4 *>(image + (size_t)(at / 64) * rows * 128 + sw128(row, at % 64 / 8)) =
+        lo_half ? make_uint4(l[0], l[1], l[2], l[3]) : make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+__device__ __forceinline__ float4 gate4(const float *g, int i) { return *reinterpret_cast<const float4 *>(g + i); }
+
+// Saved images of a chunk for its gradients: a state (or its gradient) [d_v
+// rows][d_k] and the writes (or theirs) [d_v rows][64 tokens], hi, then lo.
+constexpr size_t state_image(int dk, int dv) { return (size_t)dk * dv * 4; }
+constexpr size_t write_image(int dv) { return (size_t)kC * dv * 4; }
 
 }  // namespace gdtc
 }  // namespace kata

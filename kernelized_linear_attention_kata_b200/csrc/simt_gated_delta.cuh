@@ -648,18 +648,5 @@ gd_grads_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin 
   }
 }
 
-// dq, dk of a shared head: the sum of its value heads' parts, in head order.
-template <typename Tin>
-__global__ void gd_group_sum_kernel(const float *__restrict__ part, Tin *__restrict__ out, int group,
-                                    size_t head, size_t total) {
-  for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < total;
-       e += (size_t)gridDim.x * blockDim.x) {
-    const float *src = part + (e / head) * group * head + e % head;
-    float sum = 0.f;
-    for (int h = 0; h < group; ++h) sum += src[(size_t)h * head];
-    out[e] = from_f<Tin>(sum);
-  }
-}
-
 }  // namespace gd
 }  // namespace kata

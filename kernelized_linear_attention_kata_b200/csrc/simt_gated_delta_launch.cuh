@@ -2,6 +2,8 @@
 // element type in simt_gated_delta_{f32,bf16}.cu.
 #pragma once
 
+#include <type_traits>
+
 #include "simt_gated_delta.cuh"
 
 namespace kata {
@@ -68,18 +70,7 @@ cudaError_t backward(const GatedDeltaLaunch &a, int d_v) {
         a.Hk, a.T, a.N, d_v);
     GD_TRY(cudaGetLastError());
   }
-  if (a.dq_part) {
-    const size_t head = (size_t)a.T * DK, total = head * (size_t)(a.BH / (a.H / a.Hk));
-    const size_t want = (total + 255) / 256;
-    const unsigned grid = (unsigned)(want < 4096 ? want : 4096);
-    ProfileScope prof("gd_group_sum", a.stream);
-    gd_group_sum_kernel<<<grid, 256, 0, a.stream>>>(a.dq_part, static_cast<Tin *>(a.dq), a.H / a.Hk,
-                                                    head, total);
-    gd_group_sum_kernel<<<grid, 256, 0, a.stream>>>(a.dk_part, static_cast<Tin *>(a.dk), a.H / a.Hk,
-                                                    head, total);
-    GD_TRY(cudaGetLastError());
-  }
-  return cudaSuccess;
+  return a.dq_part ? gd_sum_groups(a, DK, std::is_same<Tin, __nv_bfloat16>::value) : cudaSuccess;
 }
 
 }  // namespace gd
