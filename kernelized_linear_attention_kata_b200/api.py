@@ -240,58 +240,72 @@ def fwd_delta(q, k, v, beta, feature="psd", return_state=False, S0=None):
 
 
 def _gated_shapes(q, k, v, g, beta, token_axis):
-    """(B, H_k, H, T, d_k, d_v) of a gated delta rule's inputs, checked; T is
-    None for the one-token step (no token axis)."""
+    """(B, H_k, H, T, d_k, d_v) of a gated delta rule's inputs, checked; the
+    one-token step's have no token axis and no T."""
+    qs, vs, dt = q.shape, v.shape, q.dtype
     n = 4 if token_axis else 3
-    tok = ", T" if token_axis else ""
-    if q.dim() != n or k.shape != q.shape or v.dim() != n or v.shape[0] != q.shape[0] or \
-            v.shape[2:-1] != q.shape[2:-1]:
+    if len(qs) != n or k.shape != qs or len(vs) != n or vs[0] != qs[0] or (token_axis and vs[2] != qs[2]):
+        tok = ", T" if token_axis else ""
         raise ValueError(f"expected q, k [B, H_k{tok}, d_k] and v [B, H{tok}, d_v]; got "
-                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
-    if not (k.dtype == v.dtype == q.dtype):
+                         f"{tuple(qs)}, {tuple(k.shape)}, {tuple(vs)}")
+    if k.dtype != dt or v.dtype != dt:
         raise TypeError("q, k, v must share one dtype")
-    B, H_k, H = q.shape[0], q.shape[1], v.shape[1]
+    H_k, H = qs[1], vs[1]
     if H and (H_k == 0 or H % H_k):
         raise ValueError(f"the {H} value heads must be a multiple of the {H_k} key heads")
-    for t, name in ((g, "g"), (beta, "beta")):
-        if t.shape != v.shape[:-1]:
-            raise ValueError(f"{name} must be {list(v.shape[:-1])} fp32, got {list(t.shape)}")
-    return B, H_k, H, (q.shape[2] if token_axis else None), q.shape[-1], v.shape[-1]
+    tokens = vs[:-1]
+    if g.shape != tokens or beta.shape != tokens:
+        raise ValueError(f"g and beta must be {list(tokens)} fp32, got {list(g.shape)} and {list(beta.shape)}")
+    return (qs[0], H_k, H, qs[2], qs[3], vs[3]) if token_axis else (qs[0], H_k, H, qs[2], vs[2])
 
 
 def _like(t, shape, dtype, name):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name} must be {list(shape)} {dtype}, got {list(t.shape)} {t.dtype}")
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+def _ptr(t, name, index, dtype):
+    """Device pointer of a contiguous tensor on CUDA device `index` (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index or index < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, q is not")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 class _On:
     """The device of a call's tensors and the stream it runs on (the device's
     current stream unless one is given). What is allocated inside belongs to
     that stream, so the caching allocator does not hand it out again while the
-    call's kernels still use it."""
+    call's kernels still use it. A token of decoding is a call of a few
+    microseconds: the guards are entered only where they change something."""
 
-    def __init__(self, device, stream):
-        self.device, self.given = device, stream
+    __slots__ = ("index", "given", "guards")
+
+    def __init__(self, index, stream):
+        if stream is not None and stream.device_index != index:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
+        self.index, self.given, self.guards = index, stream, ()
 
     def __enter__(self):
-        self.guard = torch.cuda.device(self.device)
-        self.guard.__enter__()
-        self.stream = self.given if self.given is not None else torch.cuda.current_stream(self.device)
-        self.inner = torch.cuda.stream(self.given) if self.given is not None else None
-        if self.inner is not None:
-            self.inner.__enter__()
-        return self.stream.cuda_stream
+        if torch.cuda.current_device() != self.index:
+            self.guards = (torch.cuda.device(self.index),)
+            self.guards[0].__enter__()
+        if self.given is None:
+            return torch.cuda.current_stream(self.index).cuda_stream
+        self.guards += (torch.cuda.stream(self.given),)
+        self.guards[-1].__enter__()
+        return self.given.cuda_stream
 
     def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
-        return self.guard.__exit__(*exc)
+        for guard in reversed(self.guards):
+            guard.__exit__(*exc)
 
 
 def fwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, dtype=torch.bfloat16) -> int:
@@ -302,15 +316,15 @@ def bwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, dtype=torch.bfloat16
     return int(lib().kata_bwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, _DTYPES[dtype]))
 
 
-def _gated_workspace(workspace, bytes_fn, shape, q):
+def _gated_workspace(workspace, bytes_fn, shape, q, index):
     if workspace is None:
         n = bytes_fn(*shape, q.dtype)
         if n == 0:
             raise ValueError("unsupported shape for the gated delta rule: B, H_k, H, T, d_k, d_v = "
                              f"{shape}")
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    _same_device(q, workspace)
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+    return (_ptr(workspace, "workspace", index, workspace.dtype),
+            workspace.numel() * workspace.element_size(), workspace)
 
 
 def kata_fwd_gated_delta(q, k, v, g, beta, o, S0=None, S_out=None, workspace=None, stream=None):
@@ -318,16 +332,16 @@ def kata_fwd_gated_delta(q, k, v, g, beta, o, S0=None, S_out=None, workspace=Non
     [B, H_k, T, d_k], v, o [B, H, T, d_v], g (log decays) and beta (write
     strengths) fp32 [B, H, T]; S0 / S_out optional fp32 [B, H, d_k, d_v]."""
     shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
-    dt = _dtype(q)
-    _like(o, v.shape, q.dtype, "o")
-    for t, name in ((S0, "S0"), (S_out, "S_out")):
-        _like(t, (B, H, d_k, d_v), torch.float32, name)
-    _same_device(q, k, v, g, beta, o, S0, S_out)
-    ptrs = (_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g", torch.float32),
-            _dev(beta, "beta", torch.float32), _dev(o, "o"))
-    with _On(q.device, stream) as s:
-        ws, n, workspace = _gated_workspace(workspace, fwd_gated_delta_workspace_bytes, shape, q)
-        st = lib().kata_fwd_gated_delta(*ptrs, *shape, dt, _opt(S0, "S0"), _opt(S_out, "S_out"), ws, n, s)
+    dt, f32, code, i = q.dtype, torch.float32, _dtype(q), q.get_device()
+    _like(o, v.shape, dt, "o")
+    _like(S0, (B, H, d_k, d_v), f32, "S0")
+    _like(S_out, (B, H, d_k, d_v), f32, "S_out")
+    ptrs = (_ptr(q, "q", i, dt), _ptr(k, "k", i, dt), _ptr(v, "v", i, dt), _ptr(g, "g", i, f32),
+            _ptr(beta, "beta", i, f32), _ptr(o, "o", i, dt))
+    states = _ptr(S0, "S0", i, f32), _ptr(S_out, "S_out", i, f32)
+    with _On(i, stream) as s:
+        ws, n, workspace = _gated_workspace(workspace, fwd_gated_delta_workspace_bytes, shape, q, i)
+        st = lib().kata_fwd_gated_delta(*ptrs, *shape, code, *states, ws, n, s)
     check("kata_fwd_gated_delta", st)
     return o
 
@@ -338,21 +352,19 @@ def kata_bwd_gated_delta(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0=None,
     given, dS0, from dout = dL/do and optionally dS = dL/dS_out (see
     include/kata.h)."""
     shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
-    dt = _dtype(q)
-    for t, like, dtype, name in ((dout, v, q.dtype, "dout"), (dq, q, q.dtype, "dq"),
-                                 (dk, k, q.dtype, "dk"), (dv, v, q.dtype, "dv"),
-                                 (dg, g, torch.float32, "dg"), (dbeta, g, torch.float32, "dbeta")):
+    dt, f32, code, i = q.dtype, torch.float32, _dtype(q), q.get_device()
+    for t, like, dtype, name in ((dout, v, dt, "dout"), (dq, q, dt, "dq"), (dk, k, dt, "dk"), (dv, v, dt, "dv"),
+                                 (dg, g, f32, "dg"), (dbeta, g, f32, "dbeta")):
         _like(t, like.shape, dtype, name)
     for t, name in ((S0, "S0"), (dS, "dS"), (dS0, "dS0")):
-        _like(t, (B, H, d_k, d_v), torch.float32, name)
-    _same_device(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0, dS, dS0)
-    ptrs = (_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g", torch.float32),
-            _dev(beta, "beta", torch.float32), _dev(dout, "dout"), _opt(S0, "S0"), _opt(dS, "dS"),
-            _dev(dq, "dq"), _dev(dk, "dk"), _dev(dv, "dv"), _dev(dg, "dg"), _dev(dbeta, "dbeta"),
-            _opt(dS0, "dS0"))
-    with _On(q.device, stream) as s:
-        ws, n, workspace = _gated_workspace(workspace, bwd_gated_delta_workspace_bytes, shape, q)
-        st = lib().kata_bwd_gated_delta(*ptrs, *shape, dt, ws, n, s)
+        _like(t, (B, H, d_k, d_v), f32, name)
+    ptrs = (_ptr(q, "q", i, dt), _ptr(k, "k", i, dt), _ptr(v, "v", i, dt), _ptr(g, "g", i, f32),
+            _ptr(beta, "beta", i, f32), _ptr(dout, "dout", i, dt), _ptr(S0, "S0", i, f32),
+            _ptr(dS, "dS", i, f32), _ptr(dq, "dq", i, dt), _ptr(dk, "dk", i, dt), _ptr(dv, "dv", i, dt),
+            _ptr(dg, "dg", i, f32), _ptr(dbeta, "dbeta", i, f32), _ptr(dS0, "dS0", i, f32))
+    with _On(i, stream) as s:
+        ws, n, workspace = _gated_workspace(workspace, bwd_gated_delta_workspace_bytes, shape, q, i)
+        st = lib().kata_bwd_gated_delta(*ptrs, *shape, code, ws, n, s)
     check("kata_bwd_gated_delta", st)
     return dq, dk, dv, dg, dbeta, dS0
 
@@ -360,15 +372,14 @@ def kata_bwd_gated_delta(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0=None,
 def kata_gated_delta_step(q, k, v, g, beta, S, y, stream=None):
     """In-place one-token step of the gated delta rule: q, k [B, H_k, d_k],
     v, y [B, H, d_v], g, beta fp32 [B, H]; S fp32 [B, H, d_k, d_v] updated."""
-    B, H_k, H, _, d_k, d_v = _gated_shapes(q, k, v, g, beta, False)
-    dt = _dtype(q)
-    _like(y, v.shape, q.dtype, "y")
-    _like(S, (B, H, d_k, d_v), torch.float32, "S")
-    _same_device(q, k, v, g, beta, S, y)
-    ptrs = (_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g", torch.float32),
-            _dev(beta, "beta", torch.float32), _dev(S, "S"), _dev(y, "y"))
-    with _On(q.device, stream) as s:
-        st = lib().kata_gated_delta_step(*ptrs, B, H_k, H, d_k, d_v, dt, s)
+    B, H_k, H, d_k, d_v = _gated_shapes(q, k, v, g, beta, False)
+    dt, f32, code, i = q.dtype, torch.float32, _dtype(q), q.get_device()
+    _like(y, v.shape, dt, "y")
+    _like(S, (B, H, d_k, d_v), f32, "S")
+    ptrs = (_ptr(q, "q", i, dt), _ptr(k, "k", i, dt), _ptr(v, "v", i, dt), _ptr(g, "g", i, f32),
+            _ptr(beta, "beta", i, f32), _ptr(S, "S", i, f32), _ptr(y, "y", i, dt))
+    with _On(i, stream) as s:
+        st = lib().kata_gated_delta_step(*ptrs, B, H_k, H, d_k, d_v, code, s)
     check("kata_gated_delta_step", st)
     return y
 

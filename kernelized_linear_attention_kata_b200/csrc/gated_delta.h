@@ -10,6 +10,9 @@
 namespace kata {
 
 constexpr int kGdChunk = 64;     // tokens a chunk, in every kernel of the family
+// SMs of a B200. Sizes the split of a sequence into segments; a constant, so that
+// a workspace's size follows from the shape alone, with or without a device.
+constexpr int kGdSms = 148;
 
 // Tensors [B, heads, T, d], contiguous; value head h reads query / key head
 // h / (H / Hk). BH = B * H value heads, N = ceil(T / kGdChunk) chunks.
@@ -55,7 +58,7 @@ template <typename Tin> cudaError_t simt_gated_delta(const GatedDeltaLaunch &a, 
 template <typename Tin> cudaError_t simt_gated_delta_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
 // Tensor-core forward (bf16, d_k and d_v in {64, 128}, 16-byte aligned q, k, v).
 bool gd_tc_shape(int d_k, int d_v);
-void gd_tc_split(long long BH, int N, int sms, int *G, int *seg_chunks);
+void gd_tc_split(long long BH, int N, int *G, int *seg_chunks);
 size_t gd_tc_record_bytes();
 cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k);
 // Tensor-core gradient (same shapes): the saved images of states and writes.

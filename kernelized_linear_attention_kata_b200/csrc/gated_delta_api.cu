@@ -59,31 +59,23 @@ bool aligned16(std::initializer_list<const void *> ps) {
   return true;
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
-}
-
-// The tensor-core forward's regions (the gradient's first pass needs them
-// too); false when the device cannot be asked for its size.
-bool place_chain(GatedDeltaLaunch &a, int d_k, int d_v, Regions &r) {
-  const int sms = sm_count();
-  if (sms <= 0) return false;
-  if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, sms, &a.G, &a.seg_chunks);
+// The tensor-core forward's regions (the gradient's first pass needs them too).
+void place_chain(GatedDeltaLaunch &a, int d_k, int d_v, Regions &r) {
+  if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, &a.G, &a.seg_chunks);
   a.records = r.take_bytes((size_t)a.BH * a.N * gd_tc_record_bytes());
   if (a.G > 1) {
     a.F = r.take((size_t)a.BH * (a.G - 1) * d_k * d_k);
     a.B = r.take((size_t)a.BH * (a.G - 1) * d_k * d_v);
     a.seg_starts = r.take((size_t)a.BH * a.G * d_k * d_v);
   }
-  return true;
 }
 
-// 0 when the device cannot be asked for its size
 size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, void *ws) {
   Regions r{static_cast<unsigned char *>(ws)};
-  if (on_tensor_cores(d_k, d_v, dtype)) return place_chain(a, d_k, d_v, r) ? r.used : 0;
+  if (on_tensor_cores(d_k, d_v, dtype)) {
+    place_chain(a, d_k, d_v, r);
+    return r.used;
+  }
   const size_t square = (size_t)a.BH * a.N * kGdChunk * kGdChunk;
   a.M = r.take(square);
   a.P = r.take(square);
@@ -98,7 +90,7 @@ size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype,
     a.dk_part = r.take(tokens * d_k);
   }
   if (on_tensor_cores(d_k, d_v, dtype)) {
-    if (!place_chain(a, d_k, d_v, r)) return 0;
+    place_chain(a, d_k, d_v, r);
     a.img_S = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
     a.img_dS = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
     a.img_D = r.take_bytes(chunks * gd_tc_write_image(d_v));
@@ -164,7 +156,6 @@ kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, 
   if (shape != KATA_OK) return shape;
   GatedDeltaLaunch a = describe(B, H_k, H, T);
   const size_t need = place_forward(a, d_k, d_v, dtype, workspace);
-  if (need == 0) return KATA_ERR_CUDA;
   const kata_status_t ws = check_workspace(workspace, workspace_bytes, need);
   if (ws != KATA_OK) return ws;
   a.stream = reinterpret_cast<cudaStream_t>(stream_);
@@ -201,7 +192,6 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
   if (shape != KATA_OK) return shape;
   GatedDeltaLaunch a = describe(B, H_k, H, T);
   const size_t need = place_backward(a, d_k, d_v, dtype, workspace);
-  if (need == 0) return KATA_ERR_CUDA;
   const kata_status_t ws = check_workspace(workspace, workspace_bytes, need);
   if (ws != KATA_OK) return ws;
   a.stream = reinterpret_cast<cudaStream_t>(stream_);

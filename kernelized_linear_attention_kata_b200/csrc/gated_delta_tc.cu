@@ -595,7 +595,8 @@ bool gd_tc_shape(int d_k, int d_v) {
 // Segments a head, by the time they should take: a chunk of the effect pass
 // costs about 3/4 of an output chunk, a wave runs one block an SM, and every
 // segment adds a join step of about two chunks' time.
-void gd_tc_split(long long BH, int N, int sms, int *G, int *seg_chunks) {
+void gd_tc_split(long long BH, int N, int *G, int *seg_chunks) {
+  constexpr int sms = kGdSms;
   int best = 1;
   double least = 1e300;
   for (int g = 1; g <= 64 && (g == 1 || (long long)g * BH <= sms); ++g) {
