@@ -424,10 +424,10 @@ KATA_API kata_status_t kata_fwd_delta(const void *q, const void *k, const void *
  *   workspace          device, >= kata_fwd_gated_delta_workspace_bytes(...),
  *                      256-byte aligned, contents on entry ignored, not shared by
  *                      calls that run concurrently; kata_workspace_status applies.
- * d_k, d_v in {16, 32, 64, 128}; any T. T = 0 copies S0 to S_out. bf16 with
- * d_k and d_v in {64, 128} runs on the tensor cores (fp32 operands of a product
- * as two bf16 halves, 16 bits; fp32 sums and state) and takes 16-byte aligned q,
- * k, v, o (KATA_ERR_INVALID_ARGUMENT otherwise); the rest in fp32 on the CUDA cores.
+ * d_k, d_v in {16, 32, 64, 128}; any T. T = 0 copies S0 to S_out. bf16 runs
+ * on the tensor cores (fp32 operands of a product as two bf16 halves, 16 bits;
+ * fp32 sums and state) and takes 16-byte aligned q, k, v, o
+ * (KATA_ERR_INVALID_ARGUMENT otherwise); fp32 on the CUDA cores.
  * A NaN or infinity in a token reaches the whole of its chunk and all later
  * tokens of its head.
  */

@@ -54,14 +54,19 @@ struct GatedDeltaStep {
   cudaStream_t stream;
 };
 
-template <typename Tin> cudaError_t simt_gated_delta(const GatedDeltaLaunch &a, int d_k, int d_v);
-template <typename Tin> cudaError_t simt_gated_delta_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
-// Tensor-core forward (bf16, d_k and d_v in {64, 128}, 16-byte aligned q, k, v).
-bool gd_tc_shape(int d_k, int d_v);
+// CUDA-core kernels (fp32).
+cudaError_t simt_gated_delta(const GatedDeltaLaunch &a, int d_k, int d_v);
+cudaError_t simt_gated_delta_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
+// Tensor-core forward (bf16, 16-byte aligned q, k, v, o).
+// The kernels' head sizes: 64 or 128.
+constexpr int gd_padded(int d) { return d <= 64 ? 64 : 128; }
+#define GD_TC_DISPATCH(FN)                                                    \
+  (gd_padded(d_k) == 64 ? (gd_padded(d_v) == 64 ? FN(64, 64) : FN(64, 128)) \
+                        : (gd_padded(d_v) == 64 ? FN(128, 64) : FN(128, 128)))
 void gd_tc_split(long long BH, int N, int *G, int *seg_chunks);
 size_t gd_tc_record_bytes();
 cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k);
-// Tensor-core gradient (same shapes): the saved images of states and writes.
+// Tensor-core gradient: the saved images of states and writes.
 cudaError_t gd_tc_save(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_reverse(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v);

@@ -46,12 +46,9 @@ struct Regions {
   float *take(size_t floats) { return reinterpret_cast<float *>(take_bytes(floats * sizeof(float))); }
 };
 
-// bf16 with d_k and d_v in {64, 128} runs on the tensor cores. The choice is
-// made from type and sizes alone, so the workspace needs nothing for the other
-// kernels; TMA loads make 16-byte alignment a condition there.
-bool on_tensor_cores(int d_k, int d_v, kata_dtype_t dtype) {
-  return dtype == KATA_DTYPE_BF16 && gd_tc_shape(d_k, d_v);
-}
+// bf16 runs on the tensor cores (TMA loads make 16-byte alignment a condition),
+// fp32 on the CUDA cores.
+bool on_tensor_cores(kata_dtype_t dtype) { return dtype == KATA_DTYPE_BF16; }
 
 bool aligned16(std::initializer_list<const void *> ps) {
   for (const void *p : ps)
@@ -64,15 +61,16 @@ void place_chain(GatedDeltaLaunch &a, int d_k, int d_v, Regions &r) {
   if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, &a.G, &a.seg_chunks);
   a.records = r.take_bytes((size_t)a.BH * a.N * gd_tc_record_bytes());
   if (a.G > 1) {
-    a.F = r.take((size_t)a.BH * (a.G - 1) * d_k * d_k);
-    a.B = r.take((size_t)a.BH * (a.G - 1) * d_k * d_v);
-    a.seg_starts = r.take((size_t)a.BH * a.G * d_k * d_v);
+    const size_t dk = gd_padded(d_k), dv = gd_padded(d_v);
+    a.F = r.take((size_t)a.BH * (a.G - 1) * dk * dk);
+    a.B = r.take((size_t)a.BH * (a.G - 1) * dk * dv);
+    a.seg_starts = r.take((size_t)a.BH * a.G * dk * dv);
   }
 }
 
 size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, void *ws) {
   Regions r{static_cast<unsigned char *>(ws)};
-  if (on_tensor_cores(d_k, d_v, dtype)) {
+  if (on_tensor_cores(dtype)) {
     place_chain(a, d_k, d_v, r);
     return r.used;
   }
@@ -89,7 +87,7 @@ size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype,
     a.dq_part = r.take(tokens * d_k);
     a.dk_part = r.take(tokens * d_k);
   }
-  if (on_tensor_cores(d_k, d_v, dtype)) {
+  if (on_tensor_cores(dtype)) {
     place_chain(a, d_k, d_v, r);
     a.img_S = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
     a.img_dS = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
@@ -161,7 +159,7 @@ kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, 
   a.stream = reinterpret_cast<cudaStream_t>(stream_);
   const size_t state = (size_t)a.BH * d_k * d_v;
   if (overlap(S0, S_out, state)) return KATA_ERR_INVALID_ARGUMENT;
-  const bool tc = on_tensor_cores(d_k, d_v, dtype);
+  const bool tc = on_tensor_cores(dtype);
   if (a.BH > 0 && T > 0 &&
       (!q || !k || !v || !g || !beta || !o || (tc && !aligned16({q, k, v, o}))))
     return KATA_ERR_INVALID_ARGUMENT;
@@ -169,9 +167,7 @@ kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, 
   if (a.BH == 0 || T == 0) return pass_state(S0, S_out, state, a.stream);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.o = o; a.S0 = S0; a.S_out = S_out;
   a.status = static_cast<unsigned *>(workspace);
-  const cudaError_t e = tc ? gd_tc_forward(a, d_k, d_v)
-                        : dtype == KATA_DTYPE_F32 ? simt_gated_delta<float>(a, d_k, d_v)
-                                                  : simt_gated_delta<__nv_bfloat16>(a, d_k, d_v);
+  const cudaError_t e = tc ? gd_tc_forward(a, d_k, d_v) : simt_gated_delta(a, d_k, d_v);
   return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
 }
 
@@ -197,7 +193,7 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
   a.stream = reinterpret_cast<cudaStream_t>(stream_);
   const size_t state = (size_t)a.BH * d_k * d_v;
   if (overlap(dS, dS0, state) || overlap(S0, dS0, state)) return KATA_ERR_INVALID_ARGUMENT;
-  const bool tc = on_tensor_cores(d_k, d_v, dtype);
+  const bool tc = on_tensor_cores(dtype);
   if (a.BH > 0 && T > 0 &&
       (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta ||
        (tc && !aligned16({q, k, v, dout, dq, dk, dv}))))
@@ -207,10 +203,7 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
   a.dout = dout; a.dS = dS; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
   a.status = static_cast<unsigned *>(workspace);
-  const cudaError_t e = tc ? gd_tc_backward(a, d_k, d_v)
-                        : dtype == KATA_DTYPE_F32
-                            ? simt_gated_delta_backward<float>(a, d_k, d_v)
-                            : simt_gated_delta_backward<__nv_bfloat16>(a, d_k, d_v);
+  const cudaError_t e = tc ? gd_tc_backward(a, d_k, d_v) : simt_gated_delta_backward(a, d_k, d_v);
   return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
 }
 

@@ -1,5 +1,5 @@
-// The gradient of the gated delta rule on the tensor cores (bf16, d_k and d_v
-// in {64, 128}): the reverse chain, then the gradients of all chunks at once.
+// The gradient of the gated delta rule on the tensor cores (bf16; head sizes below
+// 64 or 128 are padded with zeros as in the forward): the reverse chain, then the gradients of all chunks at once.
 //
 // The forward chain has saved each chunk's starting state S and writes D. With
 // dS' the gradient of a chunk's last state, last chunk first:
@@ -65,6 +65,7 @@ struct Args {
   uint8_t *img_dS, *img_dR;
   unsigned *status;
   int H, Hk, T, N;
+  int dk, dv;                      // the tensors' head sizes, <= DK, DV
 };
 
 template <int DK, int DV>
@@ -116,8 +117,8 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     constexpr int HK = DK / 2;
     float2 S[HK / 2];                                      // dS'
     {
-      const float *src = a.dS ? a.dS + (size_t)bh * DK * DV : nullptr;
-      auto entry = [&](int k) { return src && active ? src[(size_t)k * DV + r] : 0.f; };
+      const float *src = a.dS ? a.dS + (size_t)bh * a.dk * a.dv : nullptr;
+      auto entry = [&](int k) { return src && r < a.dv && k < a.dk ? src[(size_t)k * a.dv + r] : 0.f; };
 #pragma unroll
       for (int i = 0; i < HK / 2; ++i) S[i] = make_float2(entry(HK * h + 2 * i), entry(HK * h + 2 * i + 1));
     }
@@ -250,13 +251,14 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       }
       warp_arrive(&bars[kFree + st]);
     }
-    if (active && ok && a.dS0) {
-      float *dst = a.dS0 + (size_t)bh * DK * DV;
+    if (r < a.dv && ok && a.dS0) {
+      float *dst = a.dS0 + (size_t)bh * a.dk * a.dv;
 #pragma unroll
-      for (int i = 0; i < HK / 2; ++i) {
-        dst[(size_t)(HK * h + 2 * i) * DV + r] = S[i].x;
-        dst[(size_t)(HK * h + 2 * i + 1) * DV + r] = S[i].y;
-      }
+      for (int i = 0; i < HK / 2; ++i)
+        if (HK * h + 2 * i < a.dk) {                       // even
+          dst[(size_t)(HK * h + 2 * i) * a.dv + r] = S[i].x;
+          dst[(size_t)(HK * h + 2 * i + 1) * a.dv + r] = S[i].y;
+        }
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
@@ -406,19 +408,19 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
   if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
 }
 
-template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a) {
+template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v) {
   CUtensorMap tq, tk, tdo, tdv;
   const long long BHk = a.BH / a.H * a.Hk;
-  if (!make_tma_3d_bf16_box(&tq, a.q, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tk, a.k, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tdo, a.dout, DV, a.T, a.BH, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tdv, a.dv, DV, a.T, a.BH, 64, kC, true))
+  if (!make_tma_3d_bf16_box(&tq, a.q, d_k, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tk, a.k, d_k, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tdo, a.dout, d_v, a.T, a.BH, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tdv, a.dv, d_v, a.T, a.BH, 64, kC, true))
     return cudaErrorInvalidValue;
   constexpr int bytes = Layout<DK, DV>::kBytes;
   auto kern = gd_reverse_kernel<DK, DV>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const Args x{a.dS, a.dS0, a.records, a.img_dS, a.img_dR, a.status, a.H, a.Hk, a.T, a.N};
+  const Args x{a.dS, a.dS0, a.records, a.img_dS, a.img_dR, a.status, a.H, a.Hk, a.T, a.N, d_k, d_v};
   ProfileScope prof("gd_tc_reverse", a.stream);
   kern<<<(unsigned)a.BH, kThreads, bytes, a.stream>>>(tq, tk, tdo, tdv, x);
   return cudaGetLastError();
@@ -427,8 +429,9 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a) {
 }  // namespace
 
 cudaError_t gd_tc_reverse(const GatedDeltaLaunch &a, int d_k, int d_v) {
-  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a) : launch<64, 128>(a);
-  return d_v == 64 ? launch<128, 64>(a) : launch<128, 128>(a);
+#define GD_RUN(DK, DV) launch<DK, DV>(a, d_k, d_v)
+  return GD_TC_DISPATCH(GD_RUN);
+#undef GD_RUN
 }
 
 }  // namespace kata

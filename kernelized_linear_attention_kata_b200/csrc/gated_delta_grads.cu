@@ -1,6 +1,5 @@
 // The gradient of the gated delta rule, second kernel: dq, dk, dg and dbeta of
-// every chunk from what the chains saved at its borders (bf16, d_k and d_v in
-// {64, 128}). With X = dR S^T, Y = dO S^T, Z = D dS'^T (64 x d_k), W_ts =
+// every chunk from what the chains saved at its borders (bf16; padded head sizes). With X = dR S^T, Y = dO S^T, Z = D dS'^T (64 x d_k), W_ts =
 // e^{G_t - G_s} and dP = dO D^T, dL = -dR D^T:
 //   dq = e^G Y + (dP W) K,
 //   dk = -beta e^G X + e^{G_C - G} Z + (dP W)^T Q + (A + A^T) K,  A = dL beta W,
@@ -101,6 +100,7 @@ struct Args {
   float *dg, *dbeta, *dq_part, *dk_part;
   unsigned *status;
   int H, Hk, T, N;
+  int dk;                          // the tensors' d_k, <= DK
   long long jobs;
 };
 
@@ -464,9 +464,12 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         if (t < left_t0)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const size_t at = (tok + t) * DK + HC * ch + 8 * n + q2;
-            *reinterpret_cast<float2 *>(a.dq_part + at) = make_float2(Y[n][2 * hrow], Y[n][2 * hrow + 1]);
-            *reinterpret_cast<float2 *>(a.dk_part + at) = make_float2(X[n][2 * hrow], X[n][2 * hrow + 1]);
+            const int col = HC * ch + 8 * n + q2;
+            const size_t at = (tok + t) * a.dk + col;
+            if (col < a.dk) {
+              *reinterpret_cast<float2 *>(a.dq_part + at) = make_float2(Y[n][2 * hrow], Y[n][2 * hrow + 1]);
+              *reinterpret_cast<float2 *>(a.dk_part + at) = make_float2(X[n][2 * hrow], X[n][2 * hrow + 1]);
+            }
           }
       }
       if (tid == 0 && job + gridDim.x < a.jobs) load_qk(job + gridDim.x);
@@ -513,15 +516,15 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   }
 }
 
-template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a) {
+template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v) {
   CUtensorMap tq, tk, tv, tdo, tdq, tdk;
   const long long BHk = a.BH / a.H * a.Hk;
-  if (!make_tma_3d_bf16_box(&tq, a.q, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tk, a.k, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tv, a.v, DV, a.T, a.BH, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tdo, a.dout, DV, a.T, a.BH, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tdq, a.dq, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tdk, a.dk, DK, a.T, BHk, 64, kC, true))
+  if (!make_tma_3d_bf16_box(&tq, a.q, d_k, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tk, a.k, d_k, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tv, a.v, d_v, a.T, a.BH, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tdo, a.dout, d_v, a.T, a.BH, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tdq, a.dq, d_k, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tdk, a.dk, d_k, a.T, BHk, 64, kC, true))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -532,7 +535,7 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a) {
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   const Args x{a.g, a.beta, a.img_S, a.img_D, a.img_dS, a.img_dR, a.dg, a.dbeta, a.dq_part, a.dk_part,
-               a.status, a.H, a.Hk, a.T, a.N, a.BH * a.N};
+               a.status, a.H, a.Hk, a.T, a.N, d_k, a.BH * a.N};
   ProfileScope prof("gd_tc_grads", a.stream);
   kern<<<(unsigned)(x.jobs < sms ? x.jobs : sms), kThreads, bytes, a.stream>>>(tq, tk, tv, tdo, tdq, tdk, x);
   return cudaGetLastError();
@@ -541,8 +544,9 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a) {
 }  // namespace
 
 cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v) {
-  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a) : launch<64, 128>(a);
-  return d_v == 64 ? launch<128, 64>(a) : launch<128, 128>(a);
+#define GD_RUN(DK, DV) launch<DK, DV>(a, d_k, d_v)
+  return GD_TC_DISPATCH(GD_RUN);
+#undef GD_RUN
 }
 
 cudaError_t gd_tc_backward(const GatedDeltaLaunch &a, int d_k, int d_v) {

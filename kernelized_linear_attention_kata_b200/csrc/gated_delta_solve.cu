@@ -1,5 +1,4 @@
-// The chunk-local part of the gated delta rule, all chunks at once (bf16, d_k in
-// {64, 128}): M = (I + L)^-1 and P of each 64-token chunk as MMA operands, with
+// The chunk-local part of the gated delta rule, all chunks at once (bf16): M = (I + L)^-1 and P of each 64-token chunk as MMA operands, with
 // its decays, into the workspace (the record of gated_delta_tc.cuh).
 //
 // One block of four warps a chunk: [K; Q] K^T by tcgen05 (K rows on TMEM lanes
@@ -147,12 +146,12 @@ gd_solve_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   }
 }
 
-template <int DK> cudaError_t launch(const GatedDeltaLaunch &a) {
+template <int DK> cudaError_t launch(const GatedDeltaLaunch &a, int d_k) {
   using L = SolveLayout<DK>;
   CUtensorMap tq, tk;
   const long long BHk = a.BH / a.H * a.Hk;
-  if (!make_tma_3d_bf16_box(&tq, a.q, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&tk, a.k, DK, a.T, BHk, 64, kC, true))
+  if (!make_tma_3d_bf16_box(&tq, a.q, d_k, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&tk, a.k, d_k, a.T, BHk, 64, kC, true))
     return cudaErrorInvalidValue;
   auto kern = gd_solve_tc_kernel<DK>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
@@ -167,6 +166,8 @@ template <int DK> cudaError_t launch(const GatedDeltaLaunch &a) {
 
 size_t gd_tc_record_bytes() { return kRecBytes; }
 
-cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k) { return d_k == 64 ? launch<64>(a) : launch<128>(a); }
+cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k) { 
+  return gd_padded(d_k) == 64 ? launch<64>(a, d_k) : launch<128>(a, d_k);
+ }
 
 }  // namespace kata

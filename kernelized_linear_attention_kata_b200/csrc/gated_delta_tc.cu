@@ -1,5 +1,6 @@
 // The gated delta rule's chunked forward on the tensor cores (tcgen05 / TMEM /
-// TMA): bf16, d_k and d_v in {64, 128}, chunks of C = 64 tokens.
+// TMA): bf16, chunks of C = 64 tokens. Head sizes DK, DV in {64, 128}: smaller
+// ones are padded by the tile loads' zero fill, and the stores leave the rest out.
 //
 // Per chunk, from its starting state S [d_k, d_v] (fp32), with G the running
 // sum of g, W_ts = e^{G_t - G_s} (s <= t), M = (I + L)^-1, L_ts = beta_t W_ts
@@ -98,6 +99,7 @@ struct Args {
   const float *starts;             // segments' starting states [BH][G][d_k][d_v], 1 .. G - 1 used
   unsigned *status;
   int H, Hk, T, N, G, seg_chunks;
+  int dk, dv;                      // the tensors' head sizes, <= DK, DV
 };
 
 template <int DK, int DV, int MODE>
@@ -160,11 +162,13 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     float2 S[HK / 2];
     {
       const float *src = nullptr;
+      const bool given = seg == 0;                         // by the caller, in its own head sizes
+      const int rows = given ? a.dk : DK, ld = given ? a.dv : DV;
       if (MODE != kEffect)
-        src = seg == 0 ? (a.S0 ? a.S0 + (size_t)bh * DK * DV : nullptr)
-                       : a.starts + ((size_t)bh * a.G + seg) * DK * DV;
+        src = given ? (a.S0 ? a.S0 + (size_t)bh * rows * ld : nullptr)
+                    : a.starts + ((size_t)bh * a.G + seg) * DK * DV;
       auto entry = [&](int k) {
-        return src && active ? src[(size_t)k * DV + r] : (kind == 1 && k == r ? 1.f : 0.f);
+        return src ? (r < ld && k < rows ? src[(size_t)k * ld + r] : 0.f) : (kind == 1 && k == r ? 1.f : 0.f);
       };
 #pragma unroll
       for (int i = 0; i < HK / 2; ++i) S[i] = make_float2(entry(HK * h + 2 * i), entry(HK * h + 2 * i + 1));
@@ -340,9 +344,11 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     }
     if (active && ok) {
       float *dst = nullptr;
-      int ld = DV;
+      int ld = DV, rows = DK;
       if (MODE != kEffect) {
-        if (OUT && seg == a.G - 1 && a.S_out) dst = a.S_out + (size_t)bh * DK * DV;
+        ld = a.dv;
+        rows = a.dk;
+        if (OUT && seg == a.G - 1 && a.S_out && r < ld) dst = a.S_out + (size_t)bh * rows * ld;
       } else if (kind == 0) {
         dst = a.B + ((size_t)bh * segs + seg) * DK * DV;
       } else {
@@ -351,10 +357,11 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       if (dst) {
 #pragma unroll
-        for (int i = 0; i < HK / 2; ++i) {
-          dst[(size_t)(HK * h + 2 * i) * ld + r] = S[i].x;
-          dst[(size_t)(HK * h + 2 * i + 1) * ld + r] = S[i].y;
-        }
+        for (int i = 0; i < HK / 2; ++i)
+          if (HK * h + 2 * i < rows) {                     // even
+            dst[(size_t)(HK * h + 2 * i) * ld + r] = S[i].x;
+            dst[(size_t)(HK * h + 2 * i + 1) * ld + r] = S[i].y;
+          }
       }
     }
   } else if (warp == 8) {
@@ -511,14 +518,16 @@ constexpr int kJoinCols = 16;
 template <int DK>
 __global__ void __launch_bounds__(256)
 gd_join_kernel(const float *__restrict__ F, const float *__restrict__ B, const float *__restrict__ S0,
-               float *__restrict__ starts, int G, int DV) {
+               float *__restrict__ starts, int G, int DV, int dk, int dv) {
   __shared__ float S[DK][kJoinCols + 1];
   const int nb = DV / kJoinCols, bh = blockIdx.x / nb, c0 = blockIdx.x % nb * kJoinCols;
   const int tid = threadIdx.x, col = tid % kJoinCols, row = tid / kJoinCols;    // rows row + 16 i
   constexpr int PER = DK / 16;
   for (int e = tid; e < DK * kJoinCols; e += 256)
     S[e / kJoinCols][e % kJoinCols] =
-        S0 ? S0[((size_t)bh * DK + e / kJoinCols) * DV + c0 + e % kJoinCols] : 0.f;
+        S0 && e / kJoinCols < dk && c0 + e % kJoinCols < dv
+            ? S0[((size_t)bh * dk + e / kJoinCols) * dv + c0 + e % kJoinCols]
+            : 0.f;
   for (int j = 0; j + 1 < G; ++j) {
     const float *f = F + ((size_t)bh * (G - 1) + j) * DK * DK;
     const float *b = B + ((size_t)bh * (G - 1) + j) * DK * DV;
@@ -561,25 +570,25 @@ cudaError_t run_chain(const char *name, const GatedDeltaLaunch &a, const CUtenso
 
 // The solve, the segments' starting states, then the outputs or the saves.
 template <int DK, int DV>
-cudaError_t launch(const GatedDeltaLaunch &a, bool save) {
+cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v, bool save) {
   CUtensorMap m[4];
   const long long BHk = a.BH / a.H * a.Hk;
   void *o = save ? const_cast<void *>(a.v) : a.o;          // no outputs: the map is not used
-  if (!make_tma_3d_bf16_box(&m[0], a.q, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&m[1], a.k, DK, a.T, BHk, 64, kC, true) ||
-      !make_tma_3d_bf16_box(&m[2], a.v, DV, a.T, a.BH, DV, kC, false) ||
-      !make_tma_3d_bf16_box(&m[3], o, DV, a.T, a.BH, DV, kC, false))
+  if (!make_tma_3d_bf16_box(&m[0], a.q, d_k, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&m[1], a.k, d_k, a.T, BHk, 64, kC, true) ||
+      !make_tma_3d_bf16_box(&m[2], a.v, d_v, a.T, a.BH, DV, kC, false) ||
+      !make_tma_3d_bf16_box(&m[3], o, d_v, a.T, a.BH, DV, kC, false))
     return cudaErrorInvalidValue;
   const Args x{a.g, a.beta, a.S0, a.S_out, a.img_S, a.img_D, a.F, a.B, a.records, a.seg_starts,
-               a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks};
-  cudaError_t e = gd_tc_solve(a, DK);
+               a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks, d_k, d_v};
+  cudaError_t e = gd_tc_solve(a, d_k);
   if (e != cudaSuccess) return e;
   if (a.G > 1) {
     e = run_chain<DK, DV, kEffect>("gd_tc_segment", a, m, x, a.BH * (a.G - 1) * 2);
     if (e != cudaSuccess) return e;
     ProfileScope prof("gd_join", a.stream);
     gd_join_kernel<DK><<<(unsigned)(a.BH * (DV / kJoinCols)), 256, 0, a.stream>>>(
-        a.F, a.B, a.S0, a.seg_starts, a.G, DV);
+        a.F, a.B, a.S0, a.seg_starts, a.G, DV, d_k, d_v);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return save ? run_chain<DK, DV, kSave>("gd_tc_save", a, m, x, a.BH * a.G)
@@ -587,10 +596,6 @@ cudaError_t launch(const GatedDeltaLaunch &a, bool save) {
 }
 
 }  // namespace
-
-bool gd_tc_shape(int d_k, int d_v) {
-  return (d_k == 64 || d_k == 128) && (d_v == 64 || d_v == 128);
-}
 
 // Segments a head, by the time they should take: a chunk of the effect pass
 // costs about 3/4 of an output chunk, a wave runs one block an SM, and every
@@ -614,14 +619,16 @@ void gd_tc_split(long long BH, int N, int *G, int *seg_chunks) {
 }
 
 cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v) {
-  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a, false) : launch<64, 128>(a, false);
-  return d_v == 64 ? launch<128, 64>(a, false) : launch<128, 128>(a, false);
+#define GD_RUN(DK, DV) launch<DK, DV>(a, d_k, d_v, false)
+  return GD_TC_DISPATCH(GD_RUN);
+#undef GD_RUN
 }
 cudaError_t gd_tc_save(const GatedDeltaLaunch &a, int d_k, int d_v) {
-  if (d_k == 64) return d_v == 64 ? launch<64, 64>(a, true) : launch<64, 128>(a, true);
-  return d_v == 64 ? launch<128, 64>(a, true) : launch<128, 128>(a, true);
+#define GD_RUN(DK, DV) launch<DK, DV>(a, d_k, d_v, true)
+  return GD_TC_DISPATCH(GD_RUN);
+#undef GD_RUN
 }
-size_t gd_tc_state_image(int d_k, int d_v) { return state_image(d_k, d_v); }
-size_t gd_tc_write_image(int d_v) { return write_image(d_v); }
+size_t gd_tc_state_image(int d_k, int d_v) { return state_image(gd_padded(d_k), gd_padded(d_v)); }
+size_t gd_tc_write_image(int d_v) { return write_image(gd_padded(d_v)); }
 
 }  // namespace kata

@@ -1,6 +1,4 @@
-// The gated delta rule on the CUDA cores, fp32 arithmetic for both element
-// types: the path of fp32 tensors and of the head sizes the tensor-core
-// kernels do not take.
+// The gated delta rule on the CUDA cores: the path of fp32 tensors.
 //
 //   S_t = e^{g_t} S_{t-1} + k_t d_t^T,  d_t = beta_t (v_t - e^{g_t} S_{t-1}^T k_t),
 //   o_t = S_t^T q_t.
@@ -112,11 +110,11 @@ struct Gemm {
 };
 
 // rows [t0, t0 + 64) of a [T][d] tensor, columns [c0, c0 + W), zeros behind T
-template <int W, int LD, typename Tin>
-__device__ __forceinline__ void load_rows(float *dst, const Tin *src, int t0, int T, int d, int c0) {
+template <int W, int LD>
+__device__ __forceinline__ void load_rows(float *dst, const float *src, int t0, int T, int d, int c0) {
   for (int e = threadIdx.x; e < kC * W; e += kThreads) {
     const int t = e / W, c = e % W;
-    dst[t * LD + c] = t0 + t < T ? to_f(src[(size_t)(t0 + t) * d + c0 + c]) : 0.f;
+    dst[t * LD + c] = t0 + t < T ? src[(size_t)(t0 + t) * d + c0 + c] : 0.f;
   }
 }
 
@@ -169,9 +167,9 @@ struct SolveSmem {
   Gates gates;
 };
 
-template <int DK, typename Tin>
+template <int DK>
 __global__ void __launch_bounds__(kThreads)
-gd_solve_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const float *__restrict__ g,
+gd_solve_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ g,
                 const float *__restrict__ beta, float *__restrict__ M, float *__restrict__ P, int H,
                 int Hk, int T, int N) {
   extern __shared__ __align__(16) float sm[];
@@ -240,12 +238,12 @@ __device__ __forceinline__ void load_square(float *dst, const float *src) {
         reinterpret_cast<const float4 *>(src)[e];
 }
 
-template <int DK, int CB, typename Tin>
+template <int DK, int CB>
 __global__ void __launch_bounds__(kThreads)
-gd_chain_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
+gd_chain_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
                 const float *__restrict__ g, const float *__restrict__ beta,
                 const float *__restrict__ M, const float *__restrict__ P, const float *__restrict__ S0,
-                Tin *__restrict__ o, float *__restrict__ S_out, float *__restrict__ starts,
+                float *__restrict__ o, float *__restrict__ S_out, float *__restrict__ starts,
                 float *__restrict__ writes, int H, int Hk, int T, int N, int DV) {
   extern __shared__ __align__(16) float sm[];
   ChainSmem<DK, CB> &s = *reinterpret_cast<ChainSmem<DK, CB> *>(sm);
@@ -310,7 +308,7 @@ gd_chain_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin 
           const int t = GD::row(i);
           if (t0 + t < T)
             o[(at.v + t0 + t) * DV + c0 + GD::col(j)] =
-                from_f<Tin>(fmaf(s.gates.from_start[t], qs[i][j], d[i][j]));
+                (fmaf(s.gates.from_start[t], qs[i][j], d[i][j]));
         }
       __syncthreads();                                   // P D has read D
     }
@@ -337,13 +335,13 @@ gd_chain_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin 
 // ---------------------------------------------------------------------------
 // The reverse chain: dS through the chunks, last first, for CB value columns.
 // ---------------------------------------------------------------------------
-template <int DK, int CB, typename Tin>
+template <int DK, int CB>
 __global__ void __launch_bounds__(kThreads)
-gd_chain_reverse_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k,
-                        const Tin *__restrict__ dout, const float *__restrict__ g,
+gd_chain_reverse_kernel(const float *__restrict__ q, const float *__restrict__ k,
+                        const float *__restrict__ dout, const float *__restrict__ g,
                         const float *__restrict__ beta, const float *__restrict__ M,
                         const float *__restrict__ P, const float *__restrict__ dS,
-                        Tin *__restrict__ dv, float *__restrict__ dR, float *__restrict__ ends,
+                        float *__restrict__ dv, float *__restrict__ dR, float *__restrict__ ends,
                         float *__restrict__ dS0, int H, int Hk, int T, int N, int DV) {
   extern __shared__ __align__(16) float sm[];
   ChainSmem<DK, CB> &s = *reinterpret_cast<ChainSmem<DK, CB> *>(sm);
@@ -397,7 +395,7 @@ gd_chain_reverse_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k,
         s.D[t * LS + c] = -s.gates.from_start[t] * x;
         s.R[t * LS + c] *= s.gates.from_start[t];
         if (t0 + t < T) {
-          dv[(at.v + t0 + t) * DV + c0 + c] = from_f<Tin>(x);
+          dv[(at.v + t0 + t) * DV + c0 + c] = (x);
           dR[(at.v + t0 + t) * DV + c0 + c] = d[i][j];
         }
       }
@@ -447,13 +445,13 @@ template <int NX> __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-template <int DK, int CB, typename Tin>
+template <int DK, int CB>
 __global__ void __launch_bounds__(kThreads)
-gd_grads_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
-                const Tin *__restrict__ dout, const float *__restrict__ g,
+gd_grads_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
+                const float *__restrict__ dout, const float *__restrict__ g,
                 const float *__restrict__ beta, const float *__restrict__ starts,
                 const float *__restrict__ ends, const float *__restrict__ writes,
-                const float *__restrict__ dRg, Tin *__restrict__ dq, Tin *__restrict__ dk,
+                const float *__restrict__ dRg, float *__restrict__ dq, float *__restrict__ dk,
                 float *__restrict__ dq_part, float *__restrict__ dk_part, float *__restrict__ dg,
                 float *__restrict__ dbeta, int H, int Hk, int T, int N, int DV) {
   extern __shared__ __align__(16) float sm[];
@@ -498,7 +496,7 @@ gd_grads_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin 
     float rv = 0.f;
     if (t0 + t < T)
       for (int c = tid % 4; c < CB; c += 4)
-        rv = fmaf(s.dR[t * LS + c], to_f(v[(at.v + t0 + t) * DV + c0 + c]), rv);
+        rv = fmaf(s.dR[t * LS + c], v[(at.v + t0 + t) * DV + c0 + c], rv);
     rv = row_sum<4>(rv);
     if (tid % 4 == 0) s.row_v[t] += rv;
   }
@@ -641,8 +639,8 @@ gd_grads_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin 
         dq_part[(at.v + t0 + t) * DK + c] = x;
         dk_part[(at.v + t0 + t) * DK + c] = y;
       } else {
-        dq[(at.k + t0 + t) * DK + c] = from_f<Tin>(x);
-        dk[(at.k + t0 + t) * DK + c] = from_f<Tin>(y);
+        dq[(at.k + t0 + t) * DK + c] = (x);
+        dk[(at.k + t0 + t) * DK + c] = (y);
       }
     }
   }
