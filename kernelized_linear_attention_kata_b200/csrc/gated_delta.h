@@ -35,11 +35,13 @@ struct GatedDeltaLaunch {
   float *starts = nullptr, *ends = nullptr;     // [BH][N][d_k][d_v]: S and dS at the chunks' borders
   float *writes = nullptr, *dR = nullptr;       // [BH][T][d_v]
   float *dq_part = nullptr, *dk_part = nullptr; // [BH][T][d_k], only where heads share keys
-  // tensor-core kernels: G segments of seg_chunks chunks a head; what the first
-  // G - 1 do to a state, S_end = F S_start + B, and the starting states
+  // tensor-core kernels: G segments of seg_chunks chunks a head. A segment takes
+  // a state S to F S + B and, back, its gradient E to F^T E + B'.
   unsigned *status = nullptr;
   int G = 1, seg_chunks = 0;
-  float *F = nullptr, *B = nullptr, *seg_starts = nullptr;
+  float *F = nullptr;              // of segments 1 .. G - 2 [BH][G - 2]
+  float *starts_seg = nullptr;     // [BH][G], 1 .. G - 1 used: B of the segment before, then the state
+  float *ends_seg = nullptr;       // gradient [BH][G], 0 .. G - 2 used: B' of the segment behind, then dS
   uint8_t *img_S = nullptr, *img_D = nullptr, *img_dS = nullptr, *img_dR = nullptr;   // gradient, [BH][N]
   uint8_t *records = nullptr;      // what the solve leaves of each chunk [BH][N]
 };
@@ -63,12 +65,15 @@ constexpr int gd_padded(int d) { return d <= 64 ? 64 : 128; }
 #define GD_TC_DISPATCH(FN)                                                    \
   (gd_padded(d_k) == 64 ? (gd_padded(d_v) == 64 ? FN(64, 64) : FN(64, 128)) \
                         : (gd_padded(d_v) == 64 ? FN(128, 64) : FN(128, 128)))
-void gd_tc_split(long long BH, int N, int *G, int *seg_chunks);
+void gd_tc_split(long long BH, int N, bool gradient, int *G, int *seg_chunks);
 size_t gd_tc_record_bytes();
 cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k);
 // Tensor-core gradient: the saved images of states and writes.
+cudaError_t gd_tc_effect(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_save(const GatedDeltaLaunch &a, int d_k, int d_v);
+cudaError_t gd_tc_reverse_effect(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_reverse(const GatedDeltaLaunch &a, int d_k, int d_v);
+cudaError_t gd_tc_join(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
 // dq, dk of shared heads: the sums of the value heads' parts.

@@ -57,21 +57,21 @@ bool aligned16(std::initializer_list<const void *> ps) {
 }
 
 // The tensor-core forward's regions (the gradient's first pass needs them too).
-void place_chain(GatedDeltaLaunch &a, int d_k, int d_v, Regions &r) {
-  if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, &a.G, &a.seg_chunks);
+void place_chain(GatedDeltaLaunch &a, int d_k, int d_v, bool gradient, Regions &r) {
+  if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, gradient, &a.G, &a.seg_chunks);
   a.records = r.take_bytes((size_t)a.BH * a.N * gd_tc_record_bytes());
   if (a.G > 1) {
     const size_t dk = gd_padded(d_k), dv = gd_padded(d_v);
-    a.F = r.take((size_t)a.BH * (a.G - 1) * dk * dk);
-    a.B = r.take((size_t)a.BH * (a.G - 1) * dk * dv);
-    a.seg_starts = r.take((size_t)a.BH * a.G * dk * dv);
+    a.F = r.take((size_t)a.BH * (a.G - 2) * dk * dk);
+    a.starts_seg = r.take((size_t)a.BH * a.G * dk * dv);
+    if (gradient) a.ends_seg = r.take((size_t)a.BH * a.G * dk * dv);
   }
 }
 
 size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, void *ws) {
   Regions r{static_cast<unsigned char *>(ws)};
   if (on_tensor_cores(dtype)) {
-    place_chain(a, d_k, d_v, r);
+    place_chain(a, d_k, d_v, false, r);
     return r.used;
   }
   const size_t square = (size_t)a.BH * a.N * kGdChunk * kGdChunk;
@@ -88,7 +88,7 @@ size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype,
     a.dk_part = r.take(tokens * d_k);
   }
   if (on_tensor_cores(dtype)) {
-    place_chain(a, d_k, d_v, r);
+    place_chain(a, d_k, d_v, true, r);
     a.img_S = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
     a.img_dS = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
     a.img_D = r.take_bytes(chunks * gd_tc_write_image(d_v));

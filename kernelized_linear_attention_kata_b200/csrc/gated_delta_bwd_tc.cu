@@ -14,7 +14,9 @@
 //   Q^T (..)   A = (e^G dO)^T (TMEM)     B = Q tile, MN-major
 //   K^T (..)   A = -(e^G dV)^T (TMEM)    B = K tile, MN-major
 // P^T dO of the next chunk and Q^T (e^G dO) run in the gaps of the chain. dS'
-// and dR are saved as bf16 halves for the second kernel.
+// and dR are saved as bf16 halves for the second kernel. Where the sequence is
+// cut into segments, a segment passes F^T dS' + B' on: F is the forward's, B' what
+// the same chain leaves from dO and dS' = 0.
 //
 // Warps (384 threads): 0-7 the value columns (two warpgroups, each half of the
 // keys or tokens), 8 the MMA issuer, 9 the loads, 10 the saves, 11 dV's stores.
@@ -63,12 +65,16 @@ struct Args {
   float *dS0;                      // nullable
   const uint8_t *records;
   uint8_t *img_dS, *img_dR;
+  float *ends;                     // segments' [BH][G][DK][DV], 0 .. G - 2 used
   unsigned *status;
-  int H, Hk, T, N;
+  int H, Hk, T, N, G, seg_chunks;
   int dk, dv;                      // the tensors' head sizes, <= DK, DV
 };
 
-template <int DK, int DV>
+// EFFECT: what segments 1 .. G - 1 add to the gradient they pass on, from dO and dS' =
+// 0 (the last: from dS, which makes it the gradient itself), into `ends` of the
+// segment before. Otherwise all segments, from `ends`.
+template <int DK, int DV, bool EFFECT>
 __global__ void __launch_bounds__(kThreads, 1)
 gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmdo, const __grid_constant__ CUtensorMap tmdv,
@@ -84,9 +90,11 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
   const float *gates = reinterpret_cast<const float *>(smem + L::kOffGates);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int bh = blockIdx.x;
+  const int segs = EFFECT ? a.G - 1 : a.G;
+  const int bh = blockIdx.x / segs, seg = blockIdx.x % segs + (EFFECT ? 1 : 0);
   const int kh = bh / a.H * a.Hk + bh % a.H / (a.H / a.Hk);
-  const int n = a.N;
+  const int first = seg * a.seg_chunks;                    // chunks first .. first + n - 1
+  const int n = a.N - first < a.seg_chunks ? a.N - first : a.seg_chunks;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
@@ -117,8 +125,14 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     constexpr int HK = DK / 2;
     float2 S[HK / 2];                                      // dS'
     {
-      const float *src = a.dS ? a.dS + (size_t)bh * a.dk * a.dv : nullptr;
-      auto entry = [&](int k) { return src && r < a.dv && k < a.dk ? src[(size_t)k * a.dv + r] : 0.f; };
+      const bool given = seg == a.G - 1;                   // by the caller, in its own head sizes
+      const int rows = given ? a.dk : DK, ld = given ? a.dv : DV;
+      const float *src = nullptr;
+      if (given)
+        src = a.dS ? a.dS + (size_t)bh * rows * ld : nullptr;
+      else if (!EFFECT)
+        src = a.ends + ((size_t)bh * a.G + seg) * DK * DV;
+      auto entry = [&](int k) { return src && r < ld && k < rows ? src[(size_t)k * ld + r] : 0.f; };
 #pragma unroll
       for (int i = 0; i < HK / 2; ++i) S[i] = make_float2(entry(HK * h + 2 * i), entry(HK * h + 2 * i + 1));
     }
@@ -144,9 +158,11 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       }
       tc_fence_before();
       warp_arrive(&bars[kSReady]);
-      if (!(ok = stage_free(3 * i))) break;
-      if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
-      staged();
+      if (!EFFECT) {
+        if (!(ok = stage_free(3 * i))) break;
+        if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
+        staged();
+      }
 
       // e^G dO; its place in shared memory later takes dV
       const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC, *beta = to_end + kC;
@@ -192,9 +208,11 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       }
       tc_fence_before();
       warp_arrive(&bars[kDReady]);
-      if (!(ok = stage_free(3 * i + 1))) break;
-      if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
-      staged();
+      if (!EFFECT) {
+        if (!(ok = stage_free(3 * i + 1))) break;
+        if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
+        staged();
+      }
 
       // dR = M^T dD, dV = beta dR
       if (!(ok = warp_wait(&bars[kRDone], i & 1, abort_flag))) break;
@@ -220,19 +238,21 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       tc_fence_before();
       warp_arrive(&bars[kZReady]);
       const float whole = from_start[kC - 1];
-      if (!(ok = stage_free(3 * i + 2))) break;
-      if (active) {
-        stage_row<4>(stage, DV, r, 32 * h, d, false);
-        stage_row<4>(stage + (size_t)DV * 128, DV, r, 32 * h, d, true);
+      if (!EFFECT) {
+        if (!(ok = stage_free(3 * i + 2))) break;
+        if (active) {
+          stage_row<4>(stage, DV, r, 32 * h, d, false);
+          stage_row<4>(stage + (size_t)DV * 128, DV, r, 32 * h, d, true);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int t = 32 * h + 2 * j;
-          *reinterpret_cast<__nv_bfloat16 *>(at(t)) = __float2bfloat16_rn(beta[t] * d[j].x);
-          *reinterpret_cast<__nv_bfloat16 *>(at(t + 1)) = __float2bfloat16_rn(beta[t + 1] * d[j].y);
+          for (int j = 0; j < 16; ++j) {
+            const int t = 32 * h + 2 * j;
+            *reinterpret_cast<__nv_bfloat16 *>(at(t)) = __float2bfloat16_rn(beta[t] * d[j].x);
+            *reinterpret_cast<__nv_bfloat16 *>(at(t + 1)) = __float2bfloat16_rn(beta[t + 1] * d[j].y);
+          }
         }
+        staged();                                          // fences dV's writes too
+        warp_arrive(&bars[kDvReady]);
       }
-      staged();                                            // fences dV's writes too
-      warp_arrive(&bars[kDvReady]);
 
       // dS = e^{G_C} dS' + Q^T (e^G dO) - K^T (e^G dV)
       if (!(ok = warp_wait(&bars[kSDone], i & 1, abort_flag))) break;
@@ -251,13 +271,18 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       }
       warp_arrive(&bars[kFree + st]);
     }
-    if (r < a.dv && ok && a.dS0) {
-      float *dst = a.dS0 + (size_t)bh * a.dk * a.dv;
+    float *dst = nullptr;
+    const int rows = EFFECT ? DK : a.dk, ld = EFFECT ? DV : a.dv;
+    if (EFFECT)
+      dst = a.ends + ((size_t)bh * a.G + seg - 1) * DK * DV;
+    else if (seg == 0 && a.dS0)
+      dst = a.dS0 + (size_t)bh * rows * ld;
+    if (r < ld && ok && dst) {
 #pragma unroll
       for (int i = 0; i < HK / 2; ++i)
-        if (HK * h + 2 * i < a.dk) {                       // even
-          dst[(size_t)(HK * h + 2 * i) * a.dv + r] = S[i].x;
-          dst[(size_t)(HK * h + 2 * i + 1) * a.dv + r] = S[i].y;
+        if (HK * h + 2 * i < rows) {                       // even
+          dst[(size_t)(HK * h + 2 * i) * ld + r] = S[i].x;
+          dst[(size_t)(HK * h + 2 * i + 1) * ld + r] = S[i].y;
         }
     }
   } else if (warp == 8) {
@@ -346,9 +371,9 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       tma_prefetch_desc(&tmdo);
       int sent = 0;
       for (int i = 0; i < n; ++i) {
-        const int st = i & 1, c = n - 1 - i, row = kC * c;
+        const int st = i & 1, c = first + n - 1 - i, row = kC * c;
         if (i >= 2 && (!mbar_wait(&bars[kFree + st], ((i >> 1) - 1) & 1, abort_flag) ||
-                       !mbar_wait(&bars[kStored + st], ((i >> 1) - 1) & 1, abort_flag)))
+                       (!EFFECT && !mbar_wait(&bars[kStored + st], ((i >> 1) - 1) & 1, abort_flag))))
           break;
         uint8_t *kq = smem + L::kOffKq + st * L::kKq, *dO = smem + L::kOffDo + st * L::kDo;
         const uint8_t *rec = a.records + ((size_t)bh * a.N + c) * kRecBytes;
@@ -367,13 +392,13 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       if (*abort_flag)
         for (int i = sent > 2 ? sent - 2 : 0; i < sent; ++i) drain(&bars[kLoaded + (i & 1)], (i >> 1) & 1);
     }
-  } else if (warp == 10) {
+  } else if (!EFFECT && warp == 10) {
     if (lane == 0) {
       // ---------------------------------------------------------- saves: dS' hi, lo, dR
       for (int use = 0; use < 3 * n; ++use) {
         if (!mbar_wait(&bars[kStaged], use & 1, abort_flag)) break;
         const int part = use % 3;
-        const size_t at = (size_t)bh * a.N + (n - 1 - use / 3);
+        const size_t at = (size_t)bh * a.N + (first + n - 1 - use / 3);
         if (part < 2)
           bulk_store(a.img_dS + at * state_image(DK, DV) + part * L::kStateHalf, smem + L::kOffStage, L::kStateHalf);
         else
@@ -384,7 +409,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       }
       bulk_wait_all();
     }
-  } else {
+  } else if (!EFFECT) {
     if (lane == 0) {
       // ---------------------------------------------------------- dV's stores
       tma_prefetch_desc(&tmdv);
@@ -392,7 +417,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         if (!mbar_wait(&bars[kDvReady], i & 1, abort_flag)) break;
 #pragma unroll
         for (int p = 0; p < NV; ++p)
-          tma_store_3d(&tmdv, smem + L::kOffDo + (i & 1) * L::kDo + p * kPanel, 64 * p, kC * (n - 1 - i), bh);
+          tma_store_3d(&tmdv, smem + L::kOffDo + (i & 1) * L::kDo + p * kPanel, 64 * p, kC * (first + n - 1 - i), bh);
         bulk_commit_group();
         bulk_wait_read_all();
         mbar_arrive(&bars[kStored + (i & 1)]);
@@ -408,7 +433,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
   if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
 }
 
-template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v) {
+template <int DK, int DV, bool EFFECT> cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v) {
   CUtensorMap tq, tk, tdo, tdv;
   const long long BHk = a.BH / a.H * a.Hk;
   if (!make_tma_3d_bf16_box(&tq, a.q, d_k, a.T, BHk, 64, kC, true) ||
@@ -417,19 +442,26 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k,
       !make_tma_3d_bf16_box(&tdv, a.dv, d_v, a.T, a.BH, 64, kC, true))
     return cudaErrorInvalidValue;
   constexpr int bytes = Layout<DK, DV>::kBytes;
-  auto kern = gd_reverse_kernel<DK, DV>;
+  auto kern = gd_reverse_kernel<DK, DV, EFFECT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const Args x{a.dS, a.dS0, a.records, a.img_dS, a.img_dR, a.status, a.H, a.Hk, a.T, a.N, d_k, d_v};
-  ProfileScope prof("gd_tc_reverse", a.stream);
-  kern<<<(unsigned)a.BH, kThreads, bytes, a.stream>>>(tq, tk, tdo, tdv, x);
+  const Args x{a.dS, a.dS0, a.records, a.img_dS, a.img_dR, a.ends_seg, a.status, a.H, a.Hk, a.T, a.N, a.G,
+               a.seg_chunks, d_k, d_v};
+  ProfileScope prof(EFFECT ? "gd_tc_reverse_segment" : "gd_tc_reverse", a.stream);
+  kern<<<(unsigned)(a.BH * (EFFECT ? a.G - 1 : a.G)), kThreads, bytes, a.stream>>>(tq, tk, tdo, tdv, x);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+cudaError_t gd_tc_reverse_effect(const GatedDeltaLaunch &a, int d_k, int d_v) {
+  if (a.G == 1) return cudaSuccess;
+#define GD_RUN(DK, DV) launch<DK, DV, true>(a, d_k, d_v)
+  return GD_TC_DISPATCH(GD_RUN);
+#undef GD_RUN
+}
 cudaError_t gd_tc_reverse(const GatedDeltaLaunch &a, int d_k, int d_v) {
-#define GD_RUN(DK, DV) launch<DK, DV>(a, d_k, d_v)
+#define GD_RUN(DK, DV) launch<DK, DV, false>(a, d_k, d_v)
   return GD_TC_DISPATCH(GD_RUN);
 #undef GD_RUN
 }

@@ -550,7 +550,11 @@ cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v) {
 }
 
 cudaError_t gd_tc_backward(const GatedDeltaLaunch &a, int d_k, int d_v) {
-  cudaError_t e = gd_tc_save(a, d_k, d_v);
+  cudaError_t e = gd_tc_solve(a, d_k);
+  if (e == cudaSuccess) e = gd_tc_effect(a, d_k, d_v);
+  if (e == cudaSuccess) e = gd_tc_reverse_effect(a, d_k, d_v);
+  if (e == cudaSuccess) e = gd_tc_join(a, d_k, d_v);
+  if (e == cudaSuccess) e = gd_tc_save(a, d_k, d_v);
   if (e == cudaSuccess) e = gd_tc_reverse(a, d_k, d_v);
   if (e == cudaSuccess) e = gd_tc_grads(a, d_k, d_v);
   if (e == cudaSuccess && a.dq_part) e = gd_sum_groups(a, d_k, true);

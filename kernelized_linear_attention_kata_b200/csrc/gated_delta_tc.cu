@@ -59,8 +59,10 @@ constexpr uint32_t kTmemCols = 512;
 // rewrites only the columns it has read.
 constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColD = 256, kColDl = 320, kColO = 384;
 
-// kOut: outputs of segments 0 .. G - 1. kEffect: the effect of segments 0 .. G - 2
-// on a state; blockIdx picks the kind (0: B, from V and S = 0; 1: F, from S = I).
+// kOut: outputs of segments 0 .. G - 1. kEffect: the effect of segments on a
+// state, of two kinds: first the blocks for B of segments 0 .. G - 2, from V and S = 0
+// (segment 0: from S0, which makes its B the next one's starting state), then
+// those for F of segments 1 .. G - 2, from S = I without V.
 // kSave: each chunk's starting state and writes for the gradient.
 enum Mode { kOut, kEffect, kSave };
 
@@ -94,12 +96,13 @@ struct Args {
   const float *g, *beta, *S0;
   float *S_out;
   uint8_t *img_S, *img_D;          // kSave
-  float *F, *B;                    // segments' effects [BH][G - 1][..]: kind 1 and kind 0
+  float *F;                        // segments' effects, kind 1; kind 0 goes to starts
   const uint8_t *records;          // [BH][N]
-  const float *starts;             // segments' starting states [BH][G][d_k][d_v], 1 .. G - 1 used
+  float *starts;                   // segments' starting states [BH][G][DK][DV], 1 .. G - 1 used
   unsigned *status;
   int H, Hk, T, N, G, seg_chunks;
   int dk, dv;                      // the tensors' head sizes, <= DK, DV
+  int kind0;                       // kEffect: blocks of the first kind
 };
 
 template <int DK, int DV, int MODE>
@@ -119,10 +122,10 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   const float *gates = reinterpret_cast<const float *>(smem + L::kOffGates);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int segs = MODE == kEffect ? a.G - 1 : a.G;
-  const int kind = MODE == kEffect ? (int)(blockIdx.x % 2) : 0;
-  const int job = MODE == kEffect ? (int)(blockIdx.x / 2) : (int)blockIdx.x;
-  const int seg = job % segs;
+  const int kind = MODE == kEffect && (int)blockIdx.x >= a.kind0 ? 1 : 0;
+  const int segs = MODE == kEffect ? a.G - 1 - kind : a.G;
+  const int job = (int)blockIdx.x - (kind ? a.kind0 : 0);
+  const int seg = job % segs + kind;
   const int bh = job / segs;
   const int kh = bh / a.H * a.Hk + bh % a.H / (a.H / a.Hk);
   const int t_begin = seg * a.seg_chunks * kC;
@@ -164,9 +167,10 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       const float *src = nullptr;
       const bool given = seg == 0;                         // by the caller, in its own head sizes
       const int rows = given ? a.dk : DK, ld = given ? a.dv : DV;
-      if (MODE != kEffect)
-        src = given ? (a.S0 ? a.S0 + (size_t)bh * rows * ld : nullptr)
-                    : a.starts + ((size_t)bh * a.G + seg) * DK * DV;
+      if (given)
+        src = a.S0 ? a.S0 + (size_t)bh * rows * ld : nullptr;
+      else if (MODE != kEffect)
+        src = a.starts + ((size_t)bh * a.G + seg) * DK * DV;
       auto entry = [&](int k) {
         return src ? (r < ld && k < rows ? src[(size_t)k * ld + r] : 0.f) : (kind == 1 && k == r ? 1.f : 0.f);
       };
@@ -350,9 +354,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         rows = a.dk;
         if (OUT && seg == a.G - 1 && a.S_out && r < ld) dst = a.S_out + (size_t)bh * rows * ld;
       } else if (kind == 0) {
-        dst = a.B + ((size_t)bh * segs + seg) * DK * DV;
+        dst = a.starts + ((size_t)bh * a.G + seg + 1) * DK * DV;
       } else {
-        dst = a.F + ((size_t)bh * segs + seg) * DK * DK;
+        dst = a.F + ((size_t)bh * segs + seg - 1) * DK * DK;
         ld = DK;
       }
       if (dst) {
@@ -512,50 +516,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
 }
 
-// Starting states of the segments, S_{j+1} = F_j S_j + B_j: one block a head
-// and kJoinCols value columns, S in shared memory, F read row by row.
-constexpr int kJoinCols = 16;
-template <int DK>
-__global__ void __launch_bounds__(256)
-gd_join_kernel(const float *__restrict__ F, const float *__restrict__ B, const float *__restrict__ S0,
-               float *__restrict__ starts, int G, int DV, int dk, int dv) {
-  __shared__ float S[DK][kJoinCols + 1];
-  const int nb = DV / kJoinCols, bh = blockIdx.x / nb, c0 = blockIdx.x % nb * kJoinCols;
-  const int tid = threadIdx.x, col = tid % kJoinCols, row = tid / kJoinCols;    // rows row + 16 i
-  constexpr int PER = DK / 16;
-  for (int e = tid; e < DK * kJoinCols; e += 256)
-    S[e / kJoinCols][e % kJoinCols] =
-        S0 && e / kJoinCols < dk && c0 + e % kJoinCols < dv
-            ? S0[((size_t)bh * dk + e / kJoinCols) * dv + c0 + e % kJoinCols]
-            : 0.f;
-  for (int j = 0; j + 1 < G; ++j) {
-    const float *f = F + ((size_t)bh * (G - 1) + j) * DK * DK;
-    const float *b = B + ((size_t)bh * (G - 1) + j) * DK * DV;
-    float acc[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = b[(size_t)(row + 16 * i) * DV + c0 + col];
-    __syncthreads();
-#pragma unroll 4
-    for (int k = 0; k < DK; k += 4) {
-      const float s0 = S[k][col], s1 = S[k + 1][col], s2 = S[k + 2][col], s3 = S[k + 3][col];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float4 x = *reinterpret_cast<const float4 *>(f + (size_t)(row + 16 * i) * DK + k);
-        acc[i] = fmaf(x.x, s0, acc[i]);
-        acc[i] = fmaf(x.y, s1, acc[i]);
-        acc[i] = fmaf(x.z, s2, acc[i]);
-        acc[i] = fmaf(x.w, s3, acc[i]);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      S[row + 16 * i][col] = acc[i];
-      starts[(((size_t)bh * G + j + 1) * DK + row + 16 * i) * DV + c0 + col] = acc[i];
-    }
-  }
-}
-
 template <int DK, int DV, int MODE>
 cudaError_t run_chain(const char *name, const GatedDeltaLaunch &a, const CUtensorMap *maps, const Args &x,
                       long long blocks) {
@@ -568,49 +528,41 @@ cudaError_t run_chain(const char *name, const GatedDeltaLaunch &a, const CUtenso
   return cudaGetLastError();
 }
 
-// The solve, the segments' starting states, then the outputs or the saves.
-template <int DK, int DV>
-cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v, bool save) {
+template <int DK, int DV, int MODE>
+cudaError_t launch(const char *name, const GatedDeltaLaunch &a, int d_k, int d_v) {
   CUtensorMap m[4];
   const long long BHk = a.BH / a.H * a.Hk;
-  void *o = save ? const_cast<void *>(a.v) : a.o;          // no outputs: the map is not used
+  void *o = MODE == kOut ? a.o : const_cast<void *>(a.v);  // no outputs: the map is not used
   if (!make_tma_3d_bf16_box(&m[0], a.q, d_k, a.T, BHk, 64, kC, true) ||
       !make_tma_3d_bf16_box(&m[1], a.k, d_k, a.T, BHk, 64, kC, true) ||
       !make_tma_3d_bf16_box(&m[2], a.v, d_v, a.T, a.BH, DV, kC, false) ||
       !make_tma_3d_bf16_box(&m[3], o, d_v, a.T, a.BH, DV, kC, false))
     return cudaErrorInvalidValue;
-  const Args x{a.g, a.beta, a.S0, a.S_out, a.img_S, a.img_D, a.F, a.B, a.records, a.seg_starts,
-               a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks, d_k, d_v};
-  cudaError_t e = gd_tc_solve(a, d_k);
-  if (e != cudaSuccess) return e;
-  if (a.G > 1) {
-    e = run_chain<DK, DV, kEffect>("gd_tc_segment", a, m, x, a.BH * (a.G - 1) * 2);
-    if (e != cudaSuccess) return e;
-    ProfileScope prof("gd_join", a.stream);
-    gd_join_kernel<DK><<<(unsigned)(a.BH * (DV / kJoinCols)), 256, 0, a.stream>>>(
-        a.F, a.B, a.S0, a.seg_starts, a.G, DV, d_k, d_v);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  return save ? run_chain<DK, DV, kSave>("gd_tc_save", a, m, x, a.BH * a.G)
-              : run_chain<DK, DV, kOut>("gd_tc_forward", a, m, x, a.BH * a.G);
+  const int kind0 = (int)(a.BH * (a.G - 1));
+  const Args x{a.g, a.beta, a.S0, a.S_out, a.img_S, a.img_D, a.F, a.records, a.starts_seg,
+               a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks, d_k, d_v, kind0};
+  return run_chain<DK, DV, MODE>(name, a, m, x, MODE == kEffect ? kind0 + a.BH * (a.G - 2) : a.BH * a.G);
 }
 
 }  // namespace
 
-// Segments a head, by the time they should take: a chunk of the effect pass
-// costs about 3/4 of an output chunk, a wave runs one block an SM, and every
-// segment adds a join step of about two chunks' time.
-void gd_tc_split(long long BH, int N, int *G, int *seg_chunks) {
-  constexpr int sms = kGdSms;
+// Segments a head, by the time they should take in chunks of the output pass
+// (3.6 us): a wave runs one block an SM; an effect chunk costs 0.9; the gradient's
+// save, reverse and reverse effect chunks 1.3, 1.5 and 1.2; a join step 0.8, and a
+// further launch 2.
+void gd_tc_split(long long BH, int N, bool gradient, int *G, int *seg_chunks) {
   int best = 1;
   double least = 1e300;
-  for (int g = 1; g <= 64 && (g == 1 || (long long)g * BH <= sms); ++g) {
+  auto waves = [](long long blocks) { return (double)((blocks + kGdSms - 1) / kGdSms); };
+  for (int g = 1; g <= 64 && (g == 1 || (long long)g * BH <= kGdSms); ++g) {
     const int per = (N + g - 1) / g, used = per > 0 ? (N + per - 1) / per : 1;
     if (used != g) continue;
-    const double out = (double)((BH * g + sms - 1) / sms) * per;
-    const double effect = g > 1 ? 0.75 * (double)((2 * BH * (g - 1) + sms - 1) / sms) * per + 2.0 * g + 6.0 : 0.0;
-    if (out + effect < least) {
-      least = out + effect;
+    double time = (gradient ? 1.3 + 1.5 : 1.0) * waves(BH * g) * per;
+    if (g > 1)
+      time += (0.9 * waves(BH * (2 * g - 3)) + (gradient ? 1.2 * waves(BH * (g - 1)) : 0.0)) * per +
+              (g > 2 ? 2.0 + 0.8 * (g - 2) : 0.0) + (gradient ? 4.0 : 2.0);
+    if (time < least) {
+      least = time;
       best = g;
     }
   }
@@ -618,13 +570,24 @@ void gd_tc_split(long long BH, int N, int *G, int *seg_chunks) {
   *seg_chunks = (N + best - 1) / best;
 }
 
-cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v) {
-#define GD_RUN(DK, DV) launch<DK, DV>(a, d_k, d_v, false)
+cudaError_t gd_tc_effect(const GatedDeltaLaunch &a, int d_k, int d_v) {
+  if (a.G == 1) return cudaSuccess;
+#define GD_RUN(DK, DV) launch<DK, DV, kEffect>("gd_tc_segment", a, d_k, d_v)
   return GD_TC_DISPATCH(GD_RUN);
 #undef GD_RUN
 }
 cudaError_t gd_tc_save(const GatedDeltaLaunch &a, int d_k, int d_v) {
-#define GD_RUN(DK, DV) launch<DK, DV>(a, d_k, d_v, true)
+#define GD_RUN(DK, DV) launch<DK, DV, kSave>("gd_tc_save", a, d_k, d_v)
+  return GD_TC_DISPATCH(GD_RUN);
+#undef GD_RUN
+}
+// The solve, the segments' starting states, then the outputs.
+cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v) {
+  cudaError_t e = gd_tc_solve(a, d_k);
+  if (e == cudaSuccess) e = gd_tc_effect(a, d_k, d_v);
+  if (e == cudaSuccess) e = gd_tc_join(a, d_k, d_v);
+  if (e != cudaSuccess) return e;
+#define GD_RUN(DK, DV) launch<DK, DV, kOut>("gd_tc_forward", a, d_k, d_v)
   return GD_TC_DISPATCH(GD_RUN);
 #undef GD_RUN
 }
