@@ -30,7 +30,8 @@ struct GatedDeltaLaunch {
   const float *dS = nullptr;     // nullable: the last state's gradient
   void *dq = nullptr, *dk = nullptr, *dv = nullptr;
   float *dg = nullptr, *dbeta = nullptr, *dS0 = nullptr;   // dS0 nullable
-  // workspace regions (CUDA-core kernels)
+  // workspace regions (fp32 kernels)
+  float *gates = nullptr;                       // [BH][N][3][64]
   float *M = nullptr, *P = nullptr;             // [BH][N][64][64]
   float *starts = nullptr, *ends = nullptr;     // [BH][N][d_k][d_v]: S and dS at the chunks' borders
   float *writes = nullptr, *dR = nullptr;       // [BH][T][d_v]
@@ -56,9 +57,9 @@ struct GatedDeltaStep {
   cudaStream_t stream;
 };
 
-// CUDA-core kernels (fp32).
-cudaError_t simt_gated_delta(const GatedDeltaLaunch &a, int d_k, int d_v);
-cudaError_t simt_gated_delta_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
+// fp32 kernels.
+cudaError_t gd_f32(const GatedDeltaLaunch &a, int d_k, int d_v);
+cudaError_t gd_f32_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
 // Tensor-core forward (bf16, 16-byte aligned q, k, v, o).
 // The kernels' head sizes: 64 or 128.
 constexpr int gd_padded(int d) { return d <= 64 ? 64 : 128; }

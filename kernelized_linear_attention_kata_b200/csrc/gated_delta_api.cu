@@ -47,7 +47,7 @@ struct Regions {
 };
 
 // bf16 runs on the tensor cores (TMA loads make 16-byte alignment a condition),
-// fp32 on the CUDA cores.
+// fp32 on kernels of its own.
 bool on_tensor_cores(kata_dtype_t dtype) { return dtype == KATA_DTYPE_BF16; }
 
 bool aligned16(std::initializer_list<const void *> ps) {
@@ -77,6 +77,7 @@ size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, 
   const size_t square = (size_t)a.BH * a.N * kGdChunk * kGdChunk;
   a.M = r.take(square);
   a.P = r.take(square);
+  a.gates = r.take((size_t)a.BH * a.N * 3 * kGdChunk);
   return r.used;
 }
 
@@ -97,6 +98,7 @@ size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype,
   }
   a.M = r.take(chunks * kGdChunk * kGdChunk);
   a.P = r.take(chunks * kGdChunk * kGdChunk);
+  a.gates = r.take(chunks * 3 * kGdChunk);
   a.starts = r.take(chunks * d_k * d_v);
   a.ends = r.take(chunks * d_k * d_v);
   a.writes = r.take(tokens * d_v);
@@ -167,7 +169,7 @@ kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, 
   if (a.BH == 0 || T == 0) return pass_state(S0, S_out, state, a.stream);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.o = o; a.S0 = S0; a.S_out = S_out;
   a.status = static_cast<unsigned *>(workspace);
-  const cudaError_t e = tc ? gd_tc_forward(a, d_k, d_v) : simt_gated_delta(a, d_k, d_v);
+  const cudaError_t e = tc ? gd_tc_forward(a, d_k, d_v) : gd_f32(a, d_k, d_v);
   return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
 }
 
@@ -203,7 +205,7 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
   a.dout = dout; a.dS = dS; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
   a.status = static_cast<unsigned *>(workspace);
-  const cudaError_t e = tc ? gd_tc_backward(a, d_k, d_v) : simt_gated_delta_backward(a, d_k, d_v);
+  const cudaError_t e = tc ? gd_tc_backward(a, d_k, d_v) : gd_f32_backward(a, d_k, d_v);
   return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
 }
 

@@ -1,0 +1,101 @@
+// Launchers of the gated delta rule's fp32 kernels.
+
+#include "gated_delta_f32.cuh"
+
+namespace kata {
+namespace gd {
+
+template <typename K> cudaError_t allow_smem(K kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+#define GD_TRY(expr)                          \
+  do {                                        \
+    cudaError_t e_ = (expr);                  \
+    if (e_ != cudaSuccess) return e_;         \
+  } while (0)
+
+template <int DK>
+cudaError_t solve(const GatedDeltaLaunch &a) {
+  auto kern = gd_solve_kernel<DK>;
+  GD_TRY(allow_smem(kern, sizeof(SolveSmem<DK>)));
+  ProfileScope prof("gd_f32_solve", a.stream);
+  kern<<<(unsigned)(a.BH * a.N), kThreads, sizeof(SolveSmem<DK>), a.stream>>>(
+      static_cast<const float *>(a.q), static_cast<const float *>(a.k), a.g, a.beta, a.M, a.P, a.gates, a.H,
+      a.Hk, a.T, a.N);
+  return cudaGetLastError();
+}
+
+template <int DK, int CB>
+cudaError_t chain(const GatedDeltaLaunch &a, int d_v) {
+  auto kern = gd_chain_kernel<DK, CB>;
+  constexpr size_t smem = sizeof(ChainSmem<DK, CB>);
+  GD_TRY(allow_smem(kern, smem));
+  ProfileScope prof("gd_f32_chain", a.stream);
+  kern<<<(unsigned)(a.BH * (d_v / CB)), kThreads, smem, a.stream>>>(
+      static_cast<const float *>(a.q), static_cast<const float *>(a.k), static_cast<const float *>(a.v), a.gates,
+      a.M, a.P, a.S0, static_cast<float *>(a.o), a.S_out, a.starts, a.writes, a.H, a.Hk, a.T,
+      a.N, d_v);
+  return cudaGetLastError();
+}
+
+template <int DK, int CB>
+cudaError_t reverse(const GatedDeltaLaunch &a, int d_v) {
+  auto kern = gd_chain_reverse_kernel<DK, CB>;
+  constexpr size_t smem = sizeof(ChainSmem<DK, CB>);
+  GD_TRY(allow_smem(kern, smem));
+  ProfileScope prof("gd_f32_chain_reverse", a.stream);
+  kern<<<(unsigned)(a.BH * (d_v / CB)), kThreads, smem, a.stream>>>(
+      static_cast<const float *>(a.q), static_cast<const float *>(a.k), static_cast<const float *>(a.dout),
+      a.gates, a.M, a.P, a.dS, static_cast<float *>(a.dv), a.dR, a.ends, a.dS0, a.H, a.Hk, a.T, a.N, d_v);
+  return cudaGetLastError();
+}
+
+template <int DK, int CB>
+cudaError_t grads(const GatedDeltaLaunch &a, int d_v) {
+  auto kern = gd_grads_kernel<DK, CB>;
+  constexpr size_t smem = sizeof(GradSmem<DK, CB>);
+  GD_TRY(allow_smem(kern, smem));
+  ProfileScope prof("gd_f32_grads", a.stream);
+  kern<<<(unsigned)(a.BH * a.N), kThreads, smem, a.stream>>>(
+      static_cast<const float *>(a.q), static_cast<const float *>(a.k), static_cast<const float *>(a.v),
+      static_cast<const float *>(a.dout), a.g, a.beta, a.starts, a.ends, a.writes, a.dR,
+      static_cast<float *>(a.dq), static_cast<float *>(a.dk), a.dq_part, a.dk_part, a.dg, a.dbeta, a.H, a.Hk,
+      a.T, a.N, d_v);
+  return cudaGetLastError();
+}
+
+// Value columns a block of the chains: the columns are independent, and 16
+// instead of 32 take three quarters of the time a chunk, so 16 as long as all
+// blocks still run at once.
+bool narrow(const GatedDeltaLaunch &a, int d_v) { return d_v == 16 || a.BH * (d_v / 16) <= kGdSms; }
+
+template <int DK>
+cudaError_t forward(const GatedDeltaLaunch &a, int d_v) {
+  GD_TRY(solve<DK>(a));
+  return narrow(a, d_v) ? chain<DK, 16>(a, d_v) : chain<DK, 32>(a, d_v);
+}
+
+template <int DK>
+cudaError_t backward(const GatedDeltaLaunch &a, int d_v) {
+  GD_TRY(forward<DK>(a, d_v));
+  GD_TRY((narrow(a, d_v) ? reverse<DK, 16>(a, d_v) : reverse<DK, 32>(a, d_v)));
+  GD_TRY((d_v == 16 ? grads<DK, 16>(a, d_v) : grads<DK, 32>(a, d_v)));
+  return a.dq_part ? gd_sum_groups(a, DK, false) : cudaSuccess;
+}
+
+}  // namespace gd
+
+#define GD_DISPATCH(FN)                  \
+  switch (d_k) {                         \
+    case 16: return gd::FN<16>(a, d_v);  \
+    case 32: return gd::FN<32>(a, d_v);  \
+    case 64: return gd::FN<64>(a, d_v);  \
+    case 128: return gd::FN<128>(a, d_v); \
+    default: return cudaErrorNotSupported; \
+  }
+
+cudaError_t gd_f32(const GatedDeltaLaunch &a, int d_k, int d_v) { GD_DISPATCH(forward) }
+cudaError_t gd_f32_backward(const GatedDeltaLaunch &a, int d_k, int d_v) { GD_DISPATCH(backward) }
+
+}  // namespace kata

@@ -172,14 +172,15 @@ __device__ __forceinline__ void decay8(const Gates &g, const RowDecay &d, int bl
 // (I + L)^-1 of a chunk, in `Lm` (row stride kLs), by blocks of 16, 32, 64:
 //   [[A, 0], [X, B]]^-1 = [[A', 0], [-B' X A', B']].
 // The 16-blocks by forward substitution, the products on the warp's tensor
-// instructions in three TF32 products an fp32 pair (x = hi + lo up to 2^-20):
+// instructions in three TF32 products an fp32 pair (x = hi + lo up to 2^-23):
 // on the CUDA cores every operand of these small products would be a shared-
 // memory broadcast, which fills the 128 B/cycle return path with one value.
 // Block substitution is as stable as the triangular solve itself, where
 // repeated squaring of L would not be (powers of L grow with repeated keys).
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-  // by truncation: the conversion instruction runs at an eighth of this rate
-  hi = __float_as_uint(x) & 0xffffe000u;
+  // rounded half up in the bits: the conversion instruction runs at an eighth of
+  // this rate (a NaN that the carry clears is still one in lo)
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi));           // the tensor core drops its low bits
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -207,9 +208,12 @@ __device__ __forceinline__ void product16(const float *A, int ra, int ca, const 
       for (int i = 0; i < 2; ++i) split_tf32(B[(k + t + 4 * i) * kLs + 8 * n + g], bh[n][i], bl[n][i]);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      mma_tf32(acc[n], ah, bh[n]);
-      mma_tf32(acc[n], ah, bl[n]);
-      mma_tf32(acc[n], al, bh[n]);
+      float d[4] = {0.f, 0.f, 0.f, 0.f};                   // the tensor core cuts its sums: they are added here
+      mma_tf32(d, al, bh[n]);
+      mma_tf32(d, ah, bl[n]);
+      mma_tf32(d, ah, bh[n]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] += d[i];
     }
   }
 }
