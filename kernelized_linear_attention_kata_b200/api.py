@@ -279,6 +279,11 @@ def _ptr(t, name, index, dtype):
     return t.data_ptr()
 
 
+# the device's current stream as a handle, without making a Stream of it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
     """The device of a call's tensors and the stream it runs on (the device's
     current stream unless one is given). What is allocated inside belongs to
@@ -298,7 +303,7 @@ class _On:
             self.guards = (torch.cuda.device(self.index),)
             self.guards[0].__enter__()
         if self.given is None:
-            return torch.cuda.current_stream(self.index).cuda_stream
+            return _raw_stream(self.index)
         self.guards += (torch.cuda.stream(self.given),)
         self.guards[-1].__enter__()
         return self.given.cuda_stream

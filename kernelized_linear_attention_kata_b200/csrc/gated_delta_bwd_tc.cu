@@ -55,9 +55,10 @@ template <int DK, int DV> struct Layout {
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 enum {
-  kLoaded = 0, kFree = 2, kStored = 4, kSReady = 6, kXDone, kUDone, kDReady, kRDone, kZReady, kSDone,
-  kStaged, kSaved, kDvReady, kEnd, kNumBars
+  kLoaded = 0, kFree = 2, kStored = 4, kXDone = 6, kUDone, kRDone, kSDone, kStaged, kSaved, kDvReady, kEnd, kNumBars
 };
+// hardware barriers, value warps to issuer (0 is the block's)
+enum { kSReady = 1, kDReady, kZReady };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
 
 struct Args {
@@ -99,9 +100,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kFree || i == kFree + 1 || i == kSReady || i == kDReady || i == kZReady || i == kStaged ||
-          i == kDvReady)
-        count = kStateWarps;
+      if (i == kFree || i == kFree + 1 || i == kStaged || i == kDvReady) count = kStateWarps;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -150,16 +149,16 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
 
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
-      if (!(ok = warp_wait(&bars[kLoaded + st], (i >> 1) & 1, abort_flag))) break;
+      ok &= warp_wait(&bars[kLoaded + st], (i >> 1) & 1, abort_flag);
       if (active) {
 #pragma unroll
         for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
         tmem_wait_st();
       }
       tc_fence_before();
-      warp_arrive(&bars[kSReady]);
+      hand_over(kSReady);
       if (!EFFECT) {
-        if (!(ok = stage_free(3 * i))) break;
+        ok &= stage_free(3 * i);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
         staged();
       }
@@ -183,8 +182,8 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       }
 
       // dD = P^T dO + e^{G_C - G} (K dS')
-      if (!(ok = warp_wait(&bars[kXDone], i & 1, abort_flag))) break;
-      if (!(ok = warp_wait(&bars[kUDone], i & 1, abort_flag))) break;
+      ok &= warp_wait(&bars[kXDone], i & 1, abort_flag);
+      ok &= warp_wait(&bars[kUDone], i & 1, abort_flag);
       tc_fence_after();
       if (active) {
         uint32_t x[32], y[32];
@@ -207,15 +206,15 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         tmem_wait_st();
       }
       tc_fence_before();
-      warp_arrive(&bars[kDReady]);
+      hand_over(kDReady);
       if (!EFFECT) {
-        if (!(ok = stage_free(3 * i + 1))) break;
+        ok &= stage_free(3 * i + 1);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
         staged();
       }
 
       // dR = M^T dD, dV = beta dR
-      if (!(ok = warp_wait(&bars[kRDone], i & 1, abort_flag))) break;
+      ok &= warp_wait(&bars[kRDone], i & 1, abort_flag);
       tc_fence_after();
       float2 d[16];
       if (active) {
@@ -236,10 +235,10 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         tmem_wait_st();
       }
       tc_fence_before();
-      warp_arrive(&bars[kZReady]);
+      hand_over(kZReady);
       const float whole = from_start[kC - 1];
       if (!EFFECT) {
-        if (!(ok = stage_free(3 * i + 2))) break;
+        ok &= stage_free(3 * i + 2);
         if (active) {
           stage_row<4>(stage, DV, r, 32 * h, d, false);
           stage_row<4>(stage + (size_t)DV * 128, DV, r, 32 * h, d, true);
@@ -255,7 +254,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       }
 
       // dS = e^{G_C} dS' + Q^T (e^G dO) - K^T (e^G dV)
-      if (!(ok = warp_wait(&bars[kSDone], i & 1, abort_flag))) break;
+      ok &= warp_wait(&bars[kSDone], i & 1, abort_flag);
       tc_fence_after();
       if (active) {
         const float2 w2 = make_float2(whole, whole);
@@ -295,9 +294,9 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     const uint32_t base = smem_u32(smem);
     auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
     // P^T dO of round i, in two accumulators
-    auto issue_x = [&](int i) -> bool {
+    auto issue_x = [&](int i) {
       const int st = i & 1;
-      if (!warp_wait(&bars[kLoaded + st], (i >> 1) & 1, abort_flag)) return false;
+      warp_wait(&bars[kLoaded + st], (i >> 1) & 1, abort_flag);
       tc_fence_after();
       if (leader) {
         const uint64_t d_do = smem_desc(base + L::kOffDo + st * L::kDo, kPanel, 1024, kSw128);
@@ -308,16 +307,15 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         mma_commit(&bars[kXDone]);
       }
       __syncwarp();
-      return true;
     };
-    bool ok = n == 0 || issue_x(0);
-    for (int i = 0; i < n && ok; ++i) {
+    issue_x(0);
+    for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       const uint64_t d_k = smem_desc(base + L::kOffKq + st * L::kKq, 16, 1024, kSw128);
       const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, 2 * kPanel, 1024, kSw128);
       const uint64_t d_q_mn = adv(d_k_mn, kPanel);
       const uint64_t d_m = smem_desc(base + L::kOffTiles + st * L::kTiles, kPanel, 1024, kSw128);
-      if (!(ok = warp_wait(&bars[kSReady], i & 1, abort_flag))) break;
+      take_over(kSReady);
       tc_fence_after();
       if (leader) {
 #pragma unroll
@@ -328,7 +326,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                    id_u, lo > 0 || k > 0);
         mma_commit(&bars[kUDone]);
       }
-      if (!(ok = warp_wait(&bars[kDReady], i & 1, abort_flag))) break;
+      take_over(kDReady);
       tc_fence_after();
       if (leader) {
         // dD hi against [M hi; M lo] in two accumulators, dD lo against M hi
@@ -346,7 +344,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
           for (int k = 0; k < 4; ++k)
             mma_ts(tbase + kColS, tbase + kColG + 16 * k + 8 * lo, adv(d_q_mn, k * 2048), id_up, lo > 0 || k > 0);
       }
-      if (!(ok = warp_wait(&bars[kZReady], i & 1, abort_flag))) break;
+      take_over(kZReady);
       tc_fence_after();
       if (leader) {
 #pragma unroll
@@ -357,9 +355,9 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         mma_commit(&bars[kSDone]);
       }
       __syncwarp();
-      if (i + 1 < n) ok = issue_x(i + 1);                  // in the gap before the next K dS'
+      if (i + 1 < n) issue_x(i + 1);                  // in the gap before the next K dS'
     }
-    if (!ok && leader) {
+    if (leader) {                                          // nothing in flight when tensor memory is given back
       mma_commit(&bars[kEnd]);
       drain(&bars[kEnd], 0);
     }

@@ -84,12 +84,14 @@ template <int DK, int DV, int MODE> struct Layout {
 };
 // Loaded: K, Q and the record; V. Free: the chunk's MMAs are done and its
 // outputs are in V's place (OUT), V is read (!OUT). Stored: they have left it.
-// The issuer tests few barriers (110-180 cycles each): the state warps wait for
-// the loads and fold them into their own arrivals.
+// The issuer waits for the state warps alone: they wait for the loads and fold
+// them into their own arrivals.
 enum {
-  kKqFull = 0, kVFull = 2, kFree = 4, kStored = 6, kSReady = 8, kKsDone, kRReady, kDDone, kDtReady, kDlReady,
-  kUDone, kODone, kStaged, kSaved, kEnd, kNumBars
+  kKqFull = 0, kVFull = 2, kFree = 4, kStored = 6, kKsDone = 8, kDDone, kUDone, kODone, kStaged, kSaved, kEnd,
+  kNumBars
 };
+// hardware barriers, state warps to issuer (0 is the block's)
+enum { kSReady = 1, kRReady, kDtReady, kDlReady };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
 
 struct Args {
@@ -137,9 +139,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kFree || i == kFree + 1 || i == kSReady || i == kRReady || i == kDtReady || i == kDlReady ||
-          i == kStaged)
-        count = kStateWarps;
+      if (i == kFree || i == kFree + 1 || i == kStaged) count = kStateWarps;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -192,8 +192,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     };
     // outputs of chunk c, o_t = e^{G_t} (Q S)_t + (P D)_t, 32 tokens a thread,
     // into the places its values of V were read from
-    auto outputs = [&](int c) -> bool {
-      if (!warp_wait(&bars[kODone], c & 1, abort_flag)) return false;
+    auto outputs = [&](int c) {
+      ok &= warp_wait(&bars[kODone], c & 1, abort_flag);
       tc_fence_after();
       if (active) {
         __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffV + (c & 1) * L::kV) +
@@ -206,7 +206,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       fence_async_smem();
       warp_arrive(&bars[kFree + (c & 1)]);
-      return true;
     };
 
     // The outputs of a chunk leave while the next one's K S runs (d_k = 128), or,
@@ -214,25 +213,25 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     for (int c = 0; c <= n; ++c) {
       const int st = c & 1;
       if (c < n) {
-        if (!(ok = warp_wait(&bars[kKqFull + st], (c >> 1) & 1, abort_flag))) break;
+        ok &= warp_wait(&bars[kKqFull + st], (c >> 1) & 1, abort_flag);
         if (active) {
 #pragma unroll
           for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
           tmem_wait_st();
         }
         tc_fence_before();
-        warp_arrive(&bars[kSReady]);
+        hand_over(kSReady);
       }
       if (SAVE) {
-        if (!(ok = stage_free(3 * c))) break;
+        ok &= stage_free(3 * c);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
         staged();
       }
-      if (OUT && c > 0 && (DK == 128 || c == n) && !(ok = outputs(c - 1))) break;
+      if (OUT && c > 0 && (DK == 128 || c == n)) outputs(c - 1);
       if (c == n) break;
 
       // R = beta (V - e^G (K S))
-      if (values && !(ok = warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag))) break;
+      if (values) ok &= warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag);
       const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC, *beta = to_end + kC;
       uint32_t V[16];                                      // two tokens a register
       {
@@ -241,7 +240,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         for (int i = 0; i < 16; ++i)
           V[i] = active && values ? (uint32_t)v[2 * i * DV] | (uint32_t)v[(2 * i + 1) * DV] << 16 : 0u;
       }
-      if (!(ok = warp_wait(&bars[kKsDone], c & 1, abort_flag))) break;
+      ok &= warp_wait(&bars[kKsDone], c & 1, abort_flag);
       tc_fence_after();
       if (active) {
         uint32_t x[32];
@@ -262,8 +261,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_st();
       }
       tc_fence_before();
-      warp_arrive(&bars[kRReady]);
-      if (OUT && DK == 64 && c > 0 && !(ok = outputs(c - 1))) break;
+      hand_over(kRReady);
+      if (OUT && DK == 64 && c > 0) outputs(c - 1);
       // e^G (Q S) to where P D is added to it, so that the next chunk's Q S
       // need not wait for this chunk's outputs
       if (OUT && active) {
@@ -283,14 +282,14 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
 
       if (SAVE) {
-        if (!(ok = stage_free(3 * c + 1))) break;
+        ok &= stage_free(3 * c + 1);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
         staged();
       }
 
       // D, from its two accumulators: scaled for the update first, as it is
       // for the outputs after
-      if (!(ok = warp_wait(&bars[kDDone], c & 1, abort_flag))) break;
+      ok &= warp_wait(&bars[kDDone], c & 1, abort_flag);
       tc_fence_after();
       float2 d[16];
       if (active) {
@@ -311,7 +310,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_st();
       }
       tc_fence_before();
-      warp_arrive(&bars[kDtReady]);
+      hand_over(kDtReady);
       const float whole = from_start[kC - 1];
       if (OUT) {
         if (active) {
@@ -319,11 +318,11 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           tmem_wait_st();
         }
         tc_fence_before();
-        warp_arrive(&bars[kDlReady]);
+        hand_over(kDlReady);
       }
 
       if (SAVE) {
-        if (!(ok = stage_free(3 * c + 2))) break;
+        ok &= stage_free(3 * c + 2);
         if (active) {
           stage_row<4>(stage, DV, r, 32 * h, d, false);
           stage_row<4>(stage + (size_t)DV * 128, DV, r, 32 * h, d, true);
@@ -332,7 +331,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
 
       // S' = e^{G_C} S + K^T D~
-      if (!(ok = warp_wait(&bars[kUDone], c & 1, abort_flag))) break;
+      ok &= warp_wait(&bars[kUDone], c & 1, abort_flag);
       tc_fence_after();
       if (active) {
         const float2 w2 = make_float2(whole, whole);
@@ -378,7 +377,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     constexpr uint32_t id_128 = idesc_bf16(128, 128, false, false);
     constexpr uint32_t id_up = idesc_bf16(128, DK, false, true);       // MN-major
     const bool leader = lane == 0;
-    bool ok = true;
     const uint32_t base = smem_u32(smem);
     auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
     for (int c = 0; c < n; ++c) {
@@ -387,7 +385,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, L::kStride, 1024, kSw128);
       const uint64_t d_m = smem_desc(base + L::kOffTiles + st * L::kTiles, 16, 1024, kSw128);
       const uint64_t d_p = adv(d_m, 2 * kPanel);
-      if (!(ok = warp_wait(&bars[kSReady], c & 1, abort_flag))) break;
+      take_over(kSReady);
       tc_fence_after();
       if (leader) {
         // [K; Q] S (!OUT: K S): S^T hi and lo against the K and Q rows. An
@@ -400,7 +398,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                    OUT ? id_128 : id_64, lo > 0 || k > 0);
         mma_commit(&bars[kKsDone]);
       }
-      if (!(ok = warp_wait(&bars[kRReady], c & 1, abort_flag))) break;
+      take_over(kRReady);
       tc_fence_after();
       if (leader) {
         // R^T hi against [M hi; M lo] (two accumulators), R^T lo against M hi
@@ -412,7 +410,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                    lo > 0 || k > 0);
         mma_commit(&bars[kDDone]);
       }
-      if (!(ok = warp_wait(&bars[kDtReady], c & 1, abort_flag))) break;
+      take_over(kDtReady);
       tc_fence_after();
       if (leader) {
 #pragma unroll
@@ -423,7 +421,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         mma_commit(&bars[kUDone]);
       }
       if (OUT) {
-        if (!(ok = warp_wait(&bars[kDlReady], c & 1, abort_flag))) break;
+        take_over(kDlReady);
         tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -437,7 +435,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       __syncwarp();
     }
-    if (!ok && leader) {
+    if (leader) {                                          // nothing in flight when tensor memory is given back
       mma_commit(&bars[kEnd]);
       drain(&bars[kEnd], 0);
     }

@@ -15,6 +15,7 @@ constexpr int kC = kGdChunk;         // 64 tokens a chunk
 constexpr int kPanel = 8192;         // 64 rows x 128 bytes: one 64-column bf16 panel
 constexpr int kLs = kC + 4;          // row stride of the solve's fp32 matrix
 constexpr float kMinLogDecay = -100.f;
+constexpr int kSpins = 64;           // tests of a barrier before a thread suspends
 
 // An fp32 pair as two bf16 pairs, x = hi + lo up to 2^-17 of its binade. The
 // tensor core multiplies bf16: an fp32 operand enters as hi + lo (q, k, v and
@@ -30,9 +31,26 @@ __device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
-// A wait by a whole warp: the result is the same in all lanes.
+// A wait by a whole warp: the result is the same in all lanes. Most waits of the
+// chains end within a few tests; a suspended thread comes back later than that.
+// Once a wait has given up, all others do at once: a warp of the chains then goes
+// on through its barriers and leaves garbage behind, and the block reports it.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+#pragma unroll 1
+  for (int i = 0; i < kSpins; ++i)
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(bar, parity, abort_flag));
+}
+// Hardware barrier `id` of the eight state warps and the issuer (288 threads):
+// the state warps pass, the issuer waits for them. Through an mbarrier the same
+// takes 300 cycles instead of 40, three or four times a chunk.
+__device__ __forceinline__ void hand_over(int id) {
+  __syncwarp();
+  asm volatile("bar.arrive %0, 288;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void take_over(int id) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 288;" ::"r"(id) : "memory");
 }
 // One arrival for a warp, after all its lanes got here.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
