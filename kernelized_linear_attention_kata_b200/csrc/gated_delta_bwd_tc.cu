@@ -42,20 +42,23 @@ template <int DK, int DV> struct Layout {
   static constexpr int kKq = 2 * NP * kPanel;              // [K p0][Q p0][K p1][Q p1]
   static constexpr int kTiles = 4 * kPanel;                // M hi, lo, P hi, lo
   static constexpr int kDo = NV * kPanel;                  // dO panels, then dV in their place
-  static constexpr int kOffKq = 0;
-  static constexpr int kOffTiles = 2 * kKq;
-  static constexpr int kOffDo = kOffTiles + 2 * kTiles;
   static constexpr int kStateHalf = (int)state_image(DK, DV) / 2, kWrites = (int)write_image(DV);
-  static constexpr int kOffStage = kOffDo + 2 * kDo;
-  static constexpr int kOffGates = kOffStage + (kStateHalf > kWrites ? kStateHalf : kWrites);
-  static constexpr int kOffBars = kOffGates + 2 * kRecGates;
+  static constexpr int kSaves = kStateHalf > kWrites ? kStateHalf : kWrites;
+  static constexpr int kOne = kKq + kTiles + kDo + kRecGates, kRoom = 232448 - 512 - 1024 - kSaves;
+  static constexpr int NS = kRoom / kOne < 4 ? kRoom / kOne : 4;   // stages, as in the forward
+  static constexpr int kOffKq = 0;
+  static constexpr int kOffTiles = NS * kKq;
+  static constexpr int kOffDo = kOffTiles + NS * kTiles;
+  static constexpr int kOffStage = kOffDo + NS * kDo;
+  static constexpr int kOffGates = kOffStage + kSaves;
+  static constexpr int kOffBars = kOffGates + NS * kRecGates;
   static constexpr int kBytes = kOffBars + 512 + 1024;
   // with d_v = 64 the dO operand's lanes 64-127 (not used) read the 8 KB behind it
-  static_assert(kOffDo + 2 * kDo + kPanel <= kOffBars + 512, "operand rows stay in shared memory");
+  static_assert(kOffDo + NS * kDo + kPanel <= kOffBars + 512, "operand rows stay in shared memory");
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 enum {
-  kLoaded = 0, kFree = 2, kStored = 4, kXDone = 6, kUDone, kRDone, kSDone, kStaged, kSaved, kDvReady, kEnd, kNumBars
+  kLoaded = 0, kFree = 4, kStored = 8, kXDone = 12, kUDone, kRDone, kSDone, kStaged, kSaved, kDvReady, kEnd, kNumBars
 };
 // hardware barriers, value warps to issuer (0 is the block's)
 enum { kSReady = 1, kDReady, kZReady };
@@ -81,7 +84,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                   const __grid_constant__ CUtensorMap tmdo, const __grid_constant__ CUtensorMap tmdv,
                   const Args a) {
   using L = Layout<DK, DV>;
-  constexpr int NP = L::NP, NV = L::NV;
+  constexpr int NP = L::NP, NV = L::NV, NS = L::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
@@ -100,7 +103,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kFree || i == kFree + 1 || i == kStaged || i == kDvReady) count = kStateWarps;
+      if ((i >= kFree && i < kFree + 4) || i == kStaged || i == kDvReady) count = kStateWarps;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -148,8 +151,8 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     bool ok = true;
 
     for (int i = 0; i < n; ++i) {
-      const int st = i & 1;
-      ok &= warp_wait(&bars[kLoaded + st], (i >> 1) & 1, abort_flag);
+      const int st = i % NS;
+      ok &= warp_wait(&bars[kLoaded + st], (i / NS) & 1, abort_flag);
       if (active) {
 #pragma unroll
         for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
@@ -295,8 +298,8 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
     // P^T dO of round i, in two accumulators
     auto issue_x = [&](int i) {
-      const int st = i & 1;
-      warp_wait(&bars[kLoaded + st], (i >> 1) & 1, abort_flag);
+      const int st = i % NS;
+      warp_wait(&bars[kLoaded + st], (i / NS) & 1, abort_flag);
       tc_fence_after();
       if (leader) {
         const uint64_t d_do = smem_desc(base + L::kOffDo + st * L::kDo, kPanel, 1024, kSw128);
@@ -310,7 +313,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     };
     issue_x(0);
     for (int i = 0; i < n; ++i) {
-      const int st = i & 1;
+      const int st = i % NS;
       const uint64_t d_k = smem_desc(base + L::kOffKq + st * L::kKq, 16, 1024, kSw128);
       const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, 2 * kPanel, 1024, kSw128);
       const uint64_t d_q_mn = adv(d_k_mn, kPanel);
@@ -369,9 +372,9 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       tma_prefetch_desc(&tmdo);
       int sent = 0;
       for (int i = 0; i < n; ++i) {
-        const int st = i & 1, c = first + n - 1 - i, row = kC * c;
-        if (i >= 2 && (!mbar_wait(&bars[kFree + st], ((i >> 1) - 1) & 1, abort_flag) ||
-                       (!EFFECT && !mbar_wait(&bars[kStored + st], ((i >> 1) - 1) & 1, abort_flag))))
+        const int st = i % NS, c = first + n - 1 - i, row = kC * c;
+        if (i >= NS && (!mbar_wait(&bars[kFree + st], (i / NS - 1) & 1, abort_flag) ||
+                        (!EFFECT && !mbar_wait(&bars[kStored + st], (i / NS - 1) & 1, abort_flag))))
           break;
         uint8_t *kq = smem + L::kOffKq + st * L::kKq, *dO = smem + L::kOffDo + st * L::kDo;
         const uint8_t *rec = a.records + ((size_t)bh * a.N + c) * kRecBytes;
@@ -388,7 +391,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         sent = i + 1;
       }
       if (*abort_flag)
-        for (int i = sent > 2 ? sent - 2 : 0; i < sent; ++i) drain(&bars[kLoaded + (i & 1)], (i >> 1) & 1);
+        for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) drain(&bars[kLoaded + i % NS], (i / NS) & 1);
     }
   } else if (!EFFECT && warp == 10) {
     if (lane == 0) {
@@ -415,10 +418,10 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         if (!mbar_wait(&bars[kDvReady], i & 1, abort_flag)) break;
 #pragma unroll
         for (int p = 0; p < NV; ++p)
-          tma_store_3d(&tmdv, smem + L::kOffDo + (i & 1) * L::kDo + p * kPanel, 64 * p, kC * (first + n - 1 - i), bh);
+          tma_store_3d(&tmdv, smem + L::kOffDo + i % NS * L::kDo + p * kPanel, 64 * p, kC * (first + n - 1 - i), bh);
         bulk_commit_group();
         bulk_wait_read_all();
-        mbar_arrive(&bars[kStored + (i & 1)]);
+        mbar_arrive(&bars[kStored + i % NS]);
       }
       bulk_wait_all();
     }

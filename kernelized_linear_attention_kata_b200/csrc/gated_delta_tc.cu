@@ -72,13 +72,18 @@ template <int DK, int DV, int MODE> struct Layout {
   static constexpr int kKq = NP * kStride;
   static constexpr int kTiles = (MODE == kOut ? 4 : 2) * kPanel;    // M hi, lo, P hi, lo
   static constexpr int kV = kC * DV * 2;                   // V, then the outputs in its place
-  static constexpr int kOffKq = 0;
-  static constexpr int kOffTiles = 2 * kKq;                // two stages of all three
-  static constexpr int kOffV = kOffTiles + 2 * kTiles;
-  static constexpr int kOffStage = kOffV + 2 * kV;         // what is being saved: half an image
   static constexpr int kStateHalf = (int)state_image(DK, DV) / 2, kWrites = (int)write_image(DV);
-  static constexpr int kOffGates = kOffStage + (MODE != kSave ? 0 : kStateHalf > kWrites ? kStateHalf : kWrites);
-  static constexpr int kOffBars = kOffGates + 2 * kRecGates;
+  static constexpr int kSaves = MODE != kSave ? 0 : kStateHalf > kWrites ? kStateHalf : kWrites;
+  // stages of all: as many as fit, up to 4 (a stage is free only in the middle of
+  // the next chunk, and of two the second is then needed again after 1.5 us)
+  static constexpr int kOne = kKq + kTiles + kV + kRecGates, kRoom = 232448 - 512 - 1024 - kSaves;
+  static constexpr int NS = kRoom / kOne < 4 ? kRoom / kOne : 4;
+  static constexpr int kOffKq = 0;
+  static constexpr int kOffTiles = NS * kKq;
+  static constexpr int kOffV = kOffTiles + NS * kTiles;
+  static constexpr int kOffStage = kOffV + NS * kV;        // what is being saved: half an image
+  static constexpr int kOffGates = kOffStage + kSaves;
+  static constexpr int kOffBars = kOffGates + NS * kRecGates;
   static constexpr int kBytes = kOffBars + 512 + 1024;     // barriers, alignment slack
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -87,7 +92,7 @@ template <int DK, int DV, int MODE> struct Layout {
 // The issuer waits for the state warps alone: they wait for the loads and fold
 // them into their own arrivals.
 enum {
-  kKqFull = 0, kVFull = 2, kFree = 4, kStored = 6, kKsDone = 8, kDDone, kUDone, kODone, kStaged, kSaved, kEnd,
+  kKqFull = 0, kVFull = 4, kFree = 8, kStored = 12, kKsDone = 16, kDDone, kUDone, kODone, kStaged, kSaved, kEnd,
   kNumBars
 };
 // hardware barriers, state warps to issuer (0 is the block's)
@@ -113,7 +118,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
              const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
              const Args a) {
   using L = Layout<DK, DV, MODE>;
-  constexpr int NP = L::NP;
+  constexpr int NP = L::NP, NS = L::NS;
   constexpr bool OUT = MODE == kOut, SAVE = MODE == kSave;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -139,7 +144,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kFree || i == kFree + 1 || i == kStaged) count = kStateWarps;
+      if ((i >= kFree && i < kFree + 4) || i == kStaged) count = kStateWarps;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -196,7 +201,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       ok &= warp_wait(&bars[kODone], c & 1, abort_flag);
       tc_fence_after();
       if (active) {
-        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffV + (c & 1) * L::kV) +
+        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffV + c % NS * L::kV) +
                              32 * h * DV + r;
         uint32_t x[32];
         tmem_ld32(col_half + kColO, x);
@@ -205,15 +210,15 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         for (int i = 0; i < 32; ++i) dst[i * DV] = __float2bfloat16_rn(__uint_as_float(x[i]));
       }
       fence_async_smem();
-      warp_arrive(&bars[kFree + (c & 1)]);
+      warp_arrive(&bars[kFree + c % NS]);
     };
 
     // The outputs of a chunk leave while the next one's K S runs (d_k = 128), or,
     // where that is as short as P D before it, after its R (d_k = 64).
     for (int c = 0; c <= n; ++c) {
-      const int st = c & 1;
+      const int st = c % NS;
       if (c < n) {
-        ok &= warp_wait(&bars[kKqFull + st], (c >> 1) & 1, abort_flag);
+        ok &= warp_wait(&bars[kKqFull + st], (c / NS) & 1, abort_flag);
         if (active) {
 #pragma unroll
           for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
@@ -231,7 +236,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       if (c == n) break;
 
       // R = beta (V - e^G (K S))
-      if (values) ok &= warp_wait(&bars[kVFull + st], (c >> 1) & 1, abort_flag);
+      if (values) ok &= warp_wait(&bars[kVFull + st], (c / NS) & 1, abort_flag);
       const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC, *beta = to_end + kC;
       uint32_t V[16];                                      // two tokens a register
       {
@@ -380,7 +385,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     const uint32_t base = smem_u32(smem);
     auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
     for (int c = 0; c < n; ++c) {
-      const int st = c & 1;
+      const int st = c % NS;
       const uint64_t d_kq = smem_desc(base + L::kOffKq + st * L::kKq, 16, 1024, kSw128);
       const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, L::kStride, 1024, kSw128);
       const uint64_t d_m = smem_desc(base + L::kOffTiles + st * L::kTiles, 16, 1024, kSw128);
@@ -448,8 +453,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       const uint8_t *rec = a.records + ((size_t)bh * a.N + (size_t)seg * a.seg_chunks) * kRecBytes;
       int sent = 0;
       for (int c = 0; c < n; ++c) {
-        const int st = c & 1, row = t_begin + kC * c;
-        if (c >= 2 && !mbar_wait(&bars[kFree + st], ((c >> 1) - 1) & 1, abort_flag)) break;
+        const int st = c % NS, row = t_begin + kC * c;
+        if (c >= NS && !mbar_wait(&bars[kFree + st], (c / NS - 1) & 1, abort_flag)) break;
         uint8_t *kq = smem + L::kOffKq + st * L::kKq;
         mbar_arrive_expect_tx(&bars[kKqFull + st], L::kKq + kRecGates + L::kTiles);
 #pragma unroll
@@ -463,15 +468,15 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                   &bars[kKqFull + st]);
         sent = c + 1;
         if (values) {
-          if (OUT && c >= 2 && !mbar_wait(&bars[kStored + st], ((c >> 1) - 1) & 1, abort_flag)) break;
+          if (OUT && c >= NS && !mbar_wait(&bars[kStored + st], (c / NS - 1) & 1, abort_flag)) break;
           mbar_arrive_expect_tx(&bars[kVFull + st], L::kV);
           tma_load_3d(smem + L::kOffV + st * L::kV, &tmv, &bars[kVFull + st], 0, row, bh);
         }
       }
       if (*abort_flag)                                     // copies in flight land before the exit
-        for (int c = sent > 2 ? sent - 2 : 0; c < sent; ++c) {
-          drain(&bars[kKqFull + (c & 1)], (c >> 1) & 1);
-          if (values) drain(&bars[kVFull + (c & 1)], (c >> 1) & 1);
+        for (int c = sent > NS ? sent - NS : 0; c < sent; ++c) {
+          drain(&bars[kKqFull + c % NS], (c / NS) & 1);
+          if (values) drain(&bars[kVFull + c % NS], (c / NS) & 1);
         }
     }
   } else if (OUT && warp == 10) {
@@ -479,11 +484,11 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       // ---------------------------------------------------------- output stores
       tma_prefetch_desc(&tmo);
       for (int c = 0; c < n; ++c) {
-        if (!mbar_wait(&bars[kFree + (c & 1)], (c >> 1) & 1, abort_flag)) break;
-        tma_store_3d(&tmo, smem + L::kOffV + (c & 1) * L::kV, 0, t_begin + kC * c, bh);
+        if (!mbar_wait(&bars[kFree + c % NS], (c / NS) & 1, abort_flag)) break;
+        tma_store_3d(&tmo, smem + L::kOffV + c % NS * L::kV, 0, t_begin + kC * c, bh);
         bulk_commit_group();
         bulk_wait_read_all();
-        mbar_arrive(&bars[kStored + (c & 1)]);
+        mbar_arrive(&bars[kStored + c % NS]);
       }
       bulk_wait_all();
     }
