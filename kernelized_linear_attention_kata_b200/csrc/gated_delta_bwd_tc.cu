@@ -17,9 +17,6 @@
 // and dR are saved as bf16 halves for the second kernel. Where the sequence is
 // cut into segments, a segment passes F^T dS' + B' on: F is the forward's, B' what
 // the same chain leaves from dO and dS' = 0.
-//
-// Warps (384 threads): 0-7 the value columns (two warpgroups, each half of the
-// keys or tokens), 8 the MMA issuer, 9 the loads, 10 the saves, 11 dV's stores.
 #include "common.cuh"
 #include "gated_delta_tc.cuh"
 #include "profile.h"
@@ -30,8 +27,7 @@ namespace {
 
 using namespace gdtc;
 
-constexpr int kThreads = 384;
-constexpr int kStateWarps = 8;
+constexpr int kThreads = kChainThreads + 32;            // warp 19 stores dV
 constexpr uint32_t kTmemCols = 512;
 // Columns: dS' operand and update accumulator; K dS', then dD; P^T dO in two
 // accumulators; M^T dD in two, the first then -(e^G dV); e^G dO.
@@ -109,7 +105,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == 8) {
+  if (warp == kIssuer) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -124,7 +120,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     const int r = 32 * (warp % 4) + lane;
     const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
     const bool active = r < DV;
-    constexpr int HK = DK / 2;
+    constexpr int HK = DK / 4;
     float2 S[HK / 2];                                      // dS'
     {
       const bool given = seg == a.G - 1;                   // by the caller, in its own head sizes
@@ -139,7 +135,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       for (int i = 0; i < HK / 2; ++i) S[i] = make_float2(entry(HK * h + 2 * i), entry(HK * h + 2 * i + 1));
     }
     const uint32_t col_s = tbase + lane_off + kColS + HK * h;
-    const uint32_t col_half = tbase + lane_off + 32 * h;
+    const uint32_t col_part = tbase + lane_off + 16 * h;
     uint8_t *stage = smem + L::kOffStage;
     auto stage_free = [&](int use) -> bool {
       return use == 0 || warp_wait(&bars[kSaved], (use - 1) & 1, abort_flag);
@@ -155,7 +151,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       ok &= warp_wait(&bars[kLoaded + st], (i / NS) & 1, abort_flag);
       if (active) {
 #pragma unroll
-        for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
+        for (int b = 0; b < HK / 16; ++b) put16(col_s + 16 * b, S + 8 * b);
         tmem_wait_st();
       }
       tc_fence_before();
@@ -172,16 +168,16 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       const int chunk = r % 64 / 8;
       auto at = [&](int t) { return reinterpret_cast<uint16_t *>(col + sw128(t, chunk)); };
       if (active) {
-        float2 y[16];
+        float2 y[8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float4 f = gate4(from_start, 32 * h + 2 * j);
-          const int t = 32 * h + 2 * j;
+        for (int j = 0; j < 8; j += 2) {
+          const float4 f = gate4(from_start, 16 * h + 2 * j);
+          const int t = 16 * h + 2 * j;
           y[j] = __fmul2_rn(make_float2(f.x, f.y), as_float2((uint32_t)*at(t) << 16, (uint32_t)*at(t + 1) << 16));
           y[j + 1] = __fmul2_rn(make_float2(f.z, f.w),
                                 as_float2((uint32_t)*at(t + 2) << 16, (uint32_t)*at(t + 3) << 16));
         }
-        put32(col_half + kColG, y);
+        put16(col_part + kColG, y);
       }
 
       // dD = P^T dO + e^{G_C - G} (K dS')
@@ -189,23 +185,23 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       ok &= warp_wait(&bars[kUDone], i & 1, abort_flag);
       tc_fence_after();
       if (active) {
-        uint32_t x[32], y[32];
-        float2 z[16];
-        tmem_ld32(col_half + kColX, x);
-        tmem_ld32(col_half + kColX + 64, y);
+        uint32_t x[16], y[16];
+        float2 z[8];
+        tmem_ld16(col_part + kColX, x);
+        tmem_ld16(col_part + kColX + 64, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 8; ++j)
           z[j] = __fadd2_rn(as_float2(x[2 * j], x[2 * j + 1]), as_float2(y[2 * j], y[2 * j + 1]));
-        tmem_ld32(col_half + kColU, x);
+        tmem_ld16(col_part + kColU, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float4 f = gate4(to_end, 32 * h + 2 * j);
+        for (int j = 0; j < 8; j += 2) {
+          const float4 f = gate4(to_end, 16 * h + 2 * j);
           z[j] = __ffma2_rn(make_float2(f.x, f.y), as_float2(x[2 * j], x[2 * j + 1]), z[j]);
           z[j + 1] = __ffma2_rn(make_float2(f.z, f.w), as_float2(x[2 * j + 2], x[2 * j + 3]), z[j + 1]);
         }
-        put32(col_half + kColU, z);
+        put16(col_part + kColU, z);
         tmem_wait_st();
       }
       tc_fence_before();
@@ -219,22 +215,22 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       // dR = M^T dD, dV = beta dR
       ok &= warp_wait(&bars[kRDone], i & 1, abort_flag);
       tc_fence_after();
-      float2 d[16];
+      float2 d[8];
       if (active) {
-        uint32_t x[32], y[32];
-        float2 z[16];
-        tmem_ld32(col_half + kColD, x);
-        tmem_ld32(col_half + kColD + 64, y);
+        uint32_t x[16], y[16];
+        float2 z[8];
+        tmem_ld16(col_part + kColD, x);
+        tmem_ld16(col_part + kColD + 64, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float4 f = gate4(from_start, 32 * h + 2 * j), b = gate4(beta, 32 * h + 2 * j);
+        for (int j = 0; j < 8; j += 2) {
+          const float4 f = gate4(from_start, 16 * h + 2 * j), b = gate4(beta, 16 * h + 2 * j);
           d[j] = __fadd2_rn(as_float2(x[2 * j], x[2 * j + 1]), as_float2(y[2 * j], y[2 * j + 1]));
           d[j + 1] = __fadd2_rn(as_float2(x[2 * j + 2], x[2 * j + 3]), as_float2(y[2 * j + 2], y[2 * j + 3]));
           z[j] = __fmul2_rn(make_float2(-f.x * b.x, -f.y * b.y), d[j]);
           z[j + 1] = __fmul2_rn(make_float2(-f.z * b.z, -f.w * b.w), d[j + 1]);
         }
-        put32(col_half + kColD, z);
+        put16(col_part + kColD, z);
         tmem_wait_st();
       }
       tc_fence_before();
@@ -243,11 +239,11 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       if (!EFFECT) {
         ok &= stage_free(3 * i + 2);
         if (active) {
-          stage_row<4>(stage, DV, r, 32 * h, d, false);
-          stage_row<4>(stage + (size_t)DV * 128, DV, r, 32 * h, d, true);
+          stage_row<2>(stage, DV, r, 16 * h, d, false);
+          stage_row<2>(stage + (size_t)DV * 128, DV, r, 16 * h, d, true);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int t = 32 * h + 2 * j;
+          for (int j = 0; j < 8; ++j) {
+            const int t = 16 * h + 2 * j;
             *reinterpret_cast<__nv_bfloat16 *>(at(t)) = __float2bfloat16_rn(beta[t] * d[j].x);
             *reinterpret_cast<__nv_bfloat16 *>(at(t + 1)) = __float2bfloat16_rn(beta[t + 1] * d[j].y);
           }
@@ -262,13 +258,13 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       if (active) {
         const float2 w2 = make_float2(whole, whole);
 #pragma unroll
-        for (int b = 0; b < HK / 32; ++b) {
-          uint32_t x[32];
-          tmem_ld32(col_s + 32 * b, x);
+        for (int b = 0; b < HK / 16; ++b) {
+          uint32_t x[16];
+          tmem_ld16(col_s + 16 * b, x);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            S[16 * b + j] = __ffma2_rn(w2, S[16 * b + j], as_float2(x[2 * j], x[2 * j + 1]));
+          for (int j = 0; j < 8; ++j)
+            S[8 * b + j] = __ffma2_rn(w2, S[8 * b + j], as_float2(x[2 * j], x[2 * j + 1]));
         }
       }
       warp_arrive(&bars[kFree + st]);
@@ -287,7 +283,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
           dst[(size_t)(HK * h + 2 * i + 1) * ld + r] = S[i].y;
         }
     }
-  } else if (warp == 8) {
+  } else if (warp == kIssuer) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t id_u = idesc_bf16(128, 64, false, false);       // K-major right operand
     constexpr uint32_t id_x = idesc_bf16(128, 128, true, true);        // both MN-major
@@ -364,7 +360,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       mma_commit(&bars[kEnd]);
       drain(&bars[kEnd], 0);
     }
-  } else if (warp == 9) {
+  } else if (warp == kLoader) {
     if (lane == 0) {
       // ---------------------------------------------------------- loads, last chunk first
       tma_prefetch_desc(&tmk);
@@ -393,7 +389,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       if (*abort_flag)
         for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) drain(&bars[kLoaded + i % NS], (i / NS) & 1);
     }
-  } else if (!EFFECT && warp == 10) {
+  } else if (!EFFECT && warp == kSaver) {
     if (lane == 0) {
       // ---------------------------------------------------------- saves: dS' hi, lo, dR
       for (int use = 0; use < 3 * n; ++use) {
@@ -430,7 +426,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tbase, kTmemCols);
+  if (warp == kIssuer) tmem_dealloc(tbase, kTmemCols);
   if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
 }
 

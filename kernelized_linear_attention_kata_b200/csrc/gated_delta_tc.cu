@@ -25,22 +25,17 @@
 // What bounds it: the chain S -> K S -> R -> D -> S' of one chunk, three MMA
 // rounds and three passes of the value threads over the columns. What does
 // not depend on S is kept off it: M, P and the decays come ready from the
-// solve (gated_delta_solve.cu), and the outputs of a chunk leave while the next
-// chunk's K S runs. With fewer heads than SMs the sequence is cut into G
+// solve (gated_delta_solve.cu), a chunk's P D runs in the two gaps that the next
+// one leaves the tensor core, and its outputs leave during the next one's update. With fewer heads than SMs the sequence is cut into G
 // segments: each but the last is first walked for its effect on a state, S_end =
 // F S_start + B (the same kernel without outputs, once on V from S = 0 and once
 // with V = 0 from S = I), a small kernel joins them, and the segments then run
 // side by side. For the gradient the same kernel without outputs saves every
 // chunk's S and D (gated_delta_bwd_tc.cu).
 //
-// An issuing thread gets an MMA out every 75-95 cycles whatever its N, so N is
-// 128 wherever two tiles lie side by side: K and Q rows, the two 64-key panels
-// of the update, the hi and lo tiles of M.
-//
-// Warps (384 threads): 0-7 the state warps (two warpgroups, each half of the
-// columns), 8 the MMA issuer, 9 the loads, 10 the output stores. Twelve warps
-// leave 168 registers a thread, which the state warps need: up to 64 entries
-// of S and as many in flight.
+// An MMA takes 70-85 cycles here whatever its N (from one issuing thread or from
+// two), so N is 128 wherever two tiles lie side by side: K and Q rows, the two
+// 64-key panels of the update, the hi and lo tiles of M.
 #include "common.cuh"
 #include "gated_delta_tc.cuh"
 #include "profile.h"
@@ -51,13 +46,17 @@ namespace {
 
 using namespace gdtc;
 
-constexpr int kThreads = 384;
-constexpr int kStateWarps = 8;
+constexpr int kThreads = kChainThreads;
 constexpr uint32_t kTmemCols = 512;
-// Tensor memory columns. The state's operand halves share their columns with
-// the update's accumulator, R's with K S, D~'s and D's with M R: each thread
-// rewrites only the columns it has read.
-constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColD = 256, kColDl = 320, kColO = 384;
+// Tensor memory columns. Operands and accumulators share them, each thread
+// rewriting only what it has read:
+//   kColS     S operand; M R with M hi, with M lo; the update
+//   col_ks(c) [K; Q] S, in two places by turns; R operand in K S's, then P D, which
+//             with Q S stays until the next chunk's update
+//   kColD     D~ operand;  kColDl  D operand
+constexpr uint32_t kColS = 0, kColKS = 128, kColD = 384, kColDl = 448;
+__device__ __forceinline__ uint32_t col_ks(int c) { return kColKS + 128 * (c & 1); }
+__device__ __forceinline__ uint32_t col_qs(int c) { return col_ks(c) + 64; }
 
 // kOut: outputs of segments 0 .. G - 1. kEffect: the effect of segments on a
 // state, of two kinds: first the blocks for B of segments 0 .. G - 2, from V and S = 0
@@ -70,34 +69,36 @@ template <int DK, int DV, int MODE> struct Layout {
   static constexpr int NP = DK / 64;                       // panels of a K or Q tile
   static constexpr int kStride = (MODE == kOut ? 2 : 1) * kPanel;   // [K p0][Q p0][K p1][Q p1] or K alone
   static constexpr int kKq = NP * kStride;
-  static constexpr int kTiles = (MODE == kOut ? 4 : 2) * kPanel;    // M hi, lo, P hi, lo
+  static constexpr int kM = 2 * kPanel, kP = MODE == kOut ? 2 * kPanel : 0;   // tiles hi, lo
   static constexpr int kV = kC * DV * 2;                   // V, then the outputs in its place
   static constexpr int kStateHalf = (int)state_image(DK, DV) / 2, kWrites = (int)write_image(DV);
   static constexpr int kSaves = MODE != kSave ? 0 : kStateHalf > kWrites ? kStateHalf : kWrites;
-  // stages of all: as many as fit, up to 4 (a stage is free only in the middle of
-  // the next chunk, and of two the second is then needed again after 1.5 us)
-  static constexpr int kOne = kKq + kTiles + kV + kRecGates, kRoom = 232448 - 512 - 1024 - kSaves;
-  static constexpr int NS = kRoom / kOne < 4 ? kRoom / kOne : 4;
+  // Stages of loads, as many as fit: NS of K, Q and M, which a chunk's update
+  // frees, and NV of V, P and the gates, which its outputs free in the next chunk.
+  static constexpr int kEarly = kKq + kM, kLate = kV + kP + kRecGates, kRoom = 232448 - 512 - 1024 - kSaves;
+  static constexpr int kExtra = MODE == kOut ? 1 : 0;
+  static constexpr int kFit = (kRoom - kExtra * kLate) / (kEarly + kLate);
+  static constexpr int NS = kFit < 4 - kExtra ? kFit : 4 - kExtra, NV = NS + kExtra;
   static constexpr int kOffKq = 0;
-  static constexpr int kOffTiles = NS * kKq;
-  static constexpr int kOffV = kOffTiles + NS * kTiles;
-  static constexpr int kOffStage = kOffV + NS * kV;        // what is being saved: half an image
+  static constexpr int kOffM = NS * kKq;
+  static constexpr int kOffP = kOffM + NS * kM;
+  static constexpr int kOffV = kOffP + NV * kP;
+  static constexpr int kOffStage = kOffV + NV * kV;        // what is being saved: half an image
   static constexpr int kOffGates = kOffStage + kSaves;
-  static constexpr int kOffBars = kOffGates + NS * kRecGates;
+  static constexpr int kOffBars = kOffGates + NV * kRecGates;
   static constexpr int kBytes = kOffBars + 512 + 1024;     // barriers, alignment slack
-  static_assert(kBytes <= 232448, "shared memory budget");
+  static_assert(NS >= 2 && kBytes <= 232448, "shared memory budget");
 };
-// Loaded: K, Q and the record; V. Free: the chunk's MMAs are done and its
-// outputs are in V's place (OUT), V is read (!OUT). Stored: they have left it.
-// The issuer waits for the state warps alone: they wait for the loads and fold
-// them into their own arrivals.
+// Loaded: K, Q and M; V, P and the gates. Free: K, Q and M (!OUT: V and the gates
+// too); V's place, which holds the chunk's outputs. The issuer waits for the
+// state warps alone: they wait for the loads and fold them into their own arrivals.
 enum {
-  kKqFull = 0, kVFull = 4, kFree = 8, kStored = 12, kKsDone = 16, kDDone, kUDone, kODone, kStaged, kSaved, kEnd,
+  kKqFull = 0, kVFull = 4, kFree = 8, kOutputs = 12, kKsDone = 16, kDDone, kUDone, kODone, kStaged, kSaved, kEnd,
   kNumBars
 };
-// hardware barriers, state warps to issuer (0 is the block's)
-enum { kSReady = 1, kRReady, kDtReady, kDlReady };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
+// hardware barriers, state warps to issuers (0 is the block's)
+enum { kSReady = 1, kRReady, kDtReady, kDlReady };
 
 struct Args {
   const float *g, *beta, *S0;
@@ -118,7 +119,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
              const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
              const Args a) {
   using L = Layout<DK, DV, MODE>;
-  constexpr int NP = L::NP, NS = L::NS;
+  constexpr int NP = L::NP, NS = L::NS, NV = L::NV;
   constexpr bool OUT = MODE == kOut, SAVE = MODE == kSave;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -144,13 +145,13 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if ((i >= kFree && i < kFree + 4) || i == kStaged) count = kStateWarps;
+      if ((i >= kFree && i < kOutputs + 4) || i == kStaged) count = kStateWarps;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == 8) {
+  if (warp == kIssuer) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -161,12 +162,12 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
 
   if (warp < kStateWarps) {
     // ------------------------------------------------------------ state warps
-    const int h = warp / 4;                                // half of the columns
+    const int h = warp / 4;                                // quarter of the columns
     const int r = 32 * (warp % 4) + lane;                  // value column
     const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
     const int width = values ? DV : DK;                    // value columns (kind 1: those of I)
     const bool active = r < width;                         // the same in the whole warp
-    constexpr int HK = DK / 2;                             // state entries a thread
+    constexpr int HK = DK / 4;                             // state entries a thread
     float2 S[HK / 2];
     {
       const float *src = nullptr;
@@ -183,7 +184,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       for (int i = 0; i < HK / 2; ++i) S[i] = make_float2(entry(HK * h + 2 * i), entry(HK * h + 2 * i + 1));
     }
     const uint32_t col_s = tbase + lane_off + kColS + HK * h;
-    const uint32_t col_half = tbase + lane_off + 32 * h;           // + a 64-token region
+    const uint32_t col_part = tbase + lane_off + 16 * h;           // + a 64-token region
     bool ok = true;
 
     // the staging buffer takes three parts a chunk: S hi, S lo, D
@@ -195,66 +196,70 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       fence_async_smem();
       warp_arrive(&bars[kStaged]);
     };
-    // outputs of chunk c, o_t = e^{G_t} (Q S)_t + (P D)_t, 32 tokens a thread,
+    // outputs of chunk c, o_t = e^{G_t} (Q S)_t + (P D)_t, 16 tokens a thread,
     // into the places its values of V were read from
     auto outputs = [&](int c) {
-      ok &= warp_wait(&bars[kODone], c & 1, abort_flag);
-      tc_fence_after();
       if (active) {
-        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffV + c % NS * L::kV) +
-                             32 * h * DV + r;
-        uint32_t x[32];
-        tmem_ld32(col_half + kColO, x);
+        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffV + c % NV * L::kV) +
+                             16 * h * DV + r;
+        const float *from_start = gates + c % NV * (kRecGates / 4);
+        uint32_t x[16], y[16];
+        tmem_ld16(col_part + col_ks(c), x);
+        tmem_ld16(col_part + col_qs(c), y);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) dst[i * DV] = __float2bfloat16_rn(__uint_as_float(x[i]));
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = gate4(from_start, 16 * h + i);
+          const float2 o0 = __ffma2_rn(make_float2(f.x, f.y), as_float2(y[i], y[i + 1]), as_float2(x[i], x[i + 1]));
+          const float2 o1 =
+              __ffma2_rn(make_float2(f.z, f.w), as_float2(y[i + 2], y[i + 3]), as_float2(x[i + 2], x[i + 3]));
+          dst[i * DV] = __float2bfloat16_rn(o0.x);
+          dst[(i + 1) * DV] = __float2bfloat16_rn(o0.y);
+          dst[(i + 2) * DV] = __float2bfloat16_rn(o1.x);
+          dst[(i + 3) * DV] = __float2bfloat16_rn(o1.y);
+        }
       }
       fence_async_smem();
-      warp_arrive(&bars[kFree + c % NS]);
+      tc_fence_before();
+      warp_arrive(&bars[kOutputs + c % NV]);
     };
 
-    // The outputs of a chunk leave while the next one's K S runs (d_k = 128), or,
-    // where that is as short as P D before it, after its R (d_k = 64).
-    for (int c = 0; c <= n; ++c) {
-      const int st = c % NS;
-      if (c < n) {
-        ok &= warp_wait(&bars[kKqFull + st], (c / NS) & 1, abort_flag);
-        if (active) {
+    for (int c = 0; c < n; ++c) {
+      const int st = c % NS, sv = c % NV;
+      ok &= warp_wait(&bars[kKqFull + st], (c / NS) & 1, abort_flag);
+      if (active) {
 #pragma unroll
-          for (int b = 0; b < HK / 32; ++b) put32(col_s + 32 * b, S + 16 * b);
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        hand_over(kSReady);
+        for (int b = 0; b < HK / 16; ++b) put16(col_s + 16 * b, S + 8 * b);
+        tmem_wait_st();
       }
+      tc_fence_before();
+      hand_over(kSReady);
       if (SAVE) {
         ok &= stage_free(3 * c);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
         staged();
       }
-      if (OUT && c > 0 && (DK == 128 || c == n)) outputs(c - 1);
-      if (c == n) break;
 
       // R = beta (V - e^G (K S))
-      if (values) ok &= warp_wait(&bars[kVFull + st], (c / NS) & 1, abort_flag);
-      const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC, *beta = to_end + kC;
-      uint32_t V[16];                                      // two tokens a register
+      ok &= warp_wait(&bars[kVFull + sv], (c / NV) & 1, abort_flag);
+      const float *from_start = gates + sv * (kRecGates / 4), *to_end = from_start + kC, *beta = to_end + kC;
+      uint32_t V[8];                                       // two tokens a register
       {
-        const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + st * L::kV) + 32 * h * DV + r;
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + sv * L::kV) + 16 * h * DV + r;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 8; ++i)
           V[i] = active && values ? (uint32_t)v[2 * i * DV] | (uint32_t)v[(2 * i + 1) * DV] << 16 : 0u;
       }
       ok &= warp_wait(&bars[kKsDone], c & 1, abort_flag);
       tc_fence_after();
       if (active) {
-        uint32_t x[32];
-        float2 y[16];
-        tmem_ld32(col_half + kColKS, x);
+        uint32_t x[16];
+        float2 y[8];
+        tmem_ld16(col_part + col_ks(c), x);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float4 f = gate4(from_start, 32 * h + 2 * i), b = gate4(beta, 32 * h + 2 * i);
+        for (int i = 0; i < 8; i += 2) {
+          const float4 f = gate4(from_start, 16 * h + 2 * i), b = gate4(beta, 16 * h + 2 * i);
           y[i] = __ffma2_rn(make_float2(-f.x, -f.y), as_float2(x[2 * i], x[2 * i + 1]),
                             as_float2(V[i] << 16, V[i] & 0xffff0000u));
           y[i + 1] = __ffma2_rn(make_float2(-f.z, -f.w), as_float2(x[2 * i + 2], x[2 * i + 3]),
@@ -262,30 +267,11 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           y[i] = __fmul2_rn(make_float2(b.x, b.y), y[i]);
           y[i + 1] = __fmul2_rn(make_float2(b.z, b.w), y[i + 1]);
         }
-        put32(col_half + kColKS, y);
+        put16(col_part + col_ks(c), y);
         tmem_wait_st();
       }
       tc_fence_before();
       hand_over(kRReady);
-      if (OUT && DK == 64 && c > 0) outputs(c - 1);
-      // e^G (Q S) to where P D is added to it, so that the next chunk's Q S
-      // need not wait for this chunk's outputs
-      if (OUT && active) {
-        uint32_t x[32];
-        tmem_ld32(col_half + kColQS, x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 f = gate4(from_start, 32 * h + i);
-          x[i] = __float_as_uint(f.x * __uint_as_float(x[i]));
-          x[i + 1] = __float_as_uint(f.y * __uint_as_float(x[i + 1]));
-          x[i + 2] = __float_as_uint(f.z * __uint_as_float(x[i + 2]));
-          x[i + 3] = __float_as_uint(f.w * __uint_as_float(x[i + 3]));
-        }
-        tmem_st32(col_half + kColO, x);
-        tmem_wait_st();
-      }
-
       if (SAVE) {
         ok &= stage_free(3 * c + 1);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
@@ -296,41 +282,46 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       // for the outputs after
       ok &= warp_wait(&bars[kDDone], c & 1, abort_flag);
       tc_fence_after();
-      float2 d[16];
+      float2 d[8];
       if (active) {
-        uint32_t x[32], y[32];
-        float2 z[16];
-        tmem_ld32(col_half + kColD, x);
-        tmem_ld32(col_half + kColDl, y);
+        uint32_t x[16], y[16];
+        float2 z[8];
+        tmem_ld16(col_part + kColS, x);
+        tmem_ld16(col_part + kColS + 64, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float4 f = gate4(to_end, 32 * h + 2 * i);
+        for (int i = 0; i < 8; i += 2) {
+          const float4 f = gate4(to_end, 16 * h + 2 * i);
           d[i] = __fadd2_rn(as_float2(x[2 * i], x[2 * i + 1]), as_float2(y[2 * i], y[2 * i + 1]));
           d[i + 1] = __fadd2_rn(as_float2(x[2 * i + 2], x[2 * i + 3]), as_float2(y[2 * i + 2], y[2 * i + 3]));
           z[i] = __fmul2_rn(make_float2(f.x, f.y), d[i]);
           z[i + 1] = __fmul2_rn(make_float2(f.z, f.w), d[i + 1]);
         }
-        put32(col_half + kColD, z);
+        put16(col_part + kColD, z);
         tmem_wait_st();
       }
       tc_fence_before();
       hand_over(kDtReady);
       const float whole = from_start[kC - 1];
       if (OUT) {
+        if (c > 0) {                                       // P D of the chunk before has read its D
+          ok &= warp_wait(&bars[kODone], (c - 1) & 1, abort_flag);
+          tc_fence_after();
+        }
         if (active) {
-          put32(col_half + kColDl, d);
+          put16(col_part + kColDl, d);
           tmem_wait_st();
         }
         tc_fence_before();
         hand_over(kDlReady);
+        if (c > 0) outputs(c - 1);
       }
 
       if (SAVE) {
         ok &= stage_free(3 * c + 2);
         if (active) {
-          stage_row<4>(stage, DV, r, 32 * h, d, false);
-          stage_row<4>(stage + (size_t)DV * 128, DV, r, 32 * h, d, true);
+          stage_row<2>(stage, DV, r, 16 * h, d, false);
+          stage_row<2>(stage + (size_t)DV * 128, DV, r, 16 * h, d, true);
         }
         staged();
       }
@@ -340,15 +331,22 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       tc_fence_after();
       if (active) {
         const float2 w2 = make_float2(whole, whole);
-        uint32_t x[HK];
 #pragma unroll
-        for (int b = 0; b < HK / 32; ++b)
-          tmem_ld32(col_s + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * b));
-        tmem_wait_ld();
+        for (int b = 0; b < HK / 16; ++b) {
+          uint32_t x[16];
+          tmem_ld16(col_s + 16 * b, x);
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < HK / 2; ++i) S[i] = __ffma2_rn(w2, S[i], as_float2(x[2 * i], x[2 * i + 1]));
+          for (int i = 0; i < 8; ++i)
+            S[8 * b + i] = __ffma2_rn(w2, S[8 * b + i], as_float2(x[2 * i], x[2 * i + 1]));
+        }
       }
-      if (!OUT) warp_arrive(&bars[kFree + st]);
+      warp_arrive(&bars[kFree + st]);
+    }
+    if (OUT) {
+      ok &= warp_wait(&bars[kODone], (n - 1) & 1, abort_flag);
+      tc_fence_after();
+      outputs(n - 1);
     }
     if (active && ok) {
       float *dst = nullptr;
@@ -372,24 +370,32 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kIssuer) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks the loop and one lane issues: descriptors and
-    // column addresses are then uniform values (computed by a lane on its own
-    // they cost an MMA 100 cycles instead of 50-60). Descriptors of a stage
-    // differ only in their address field (bytes / 16).
+    // The whole warp walks the loop and one lane issues: descriptors and column
+    // addresses are then uniform values (computed by a lane on its own they cost
+    // an MMA 100 cycles). Descriptors of a stage differ only in their address
+    // field (bytes / 16).
     constexpr uint32_t id_64 = idesc_bf16(128, 64, false, false);      // K-major right operand
     constexpr uint32_t id_128 = idesc_bf16(128, 128, false, false);
     constexpr uint32_t id_up = idesc_bf16(128, DK, false, true);       // MN-major
     const bool leader = lane == 0;
     const uint32_t base = smem_u32(smem);
     auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
+    // D P of chunk c, MMAs from .. to of 12: hi hi, hi lo, lo hi
+    auto issue_pd = [&](int c, int from, int to) {
+      const uint64_t d_p = smem_desc(base + L::kOffP + c % NV * L::kP, 16, 1024, kSw128);
+#pragma unroll
+      for (int m = from; m < to; ++m)
+        mma_ts(tbase + col_ks(c), tbase + kColDl + 16 * (m % 4) + 8 * (m / 8),
+               adv(d_p, (m / 4 == 1 ? kPanel : 0) + 32 * (m % 4)), id_64, m > 0);
+    };
     for (int c = 0; c < n; ++c) {
       const int st = c % NS;
       const uint64_t d_kq = smem_desc(base + L::kOffKq + st * L::kKq, 16, 1024, kSw128);
       const uint64_t d_k_mn = smem_desc(base + L::kOffKq + st * L::kKq, L::kStride, 1024, kSw128);
-      const uint64_t d_m = smem_desc(base + L::kOffTiles + st * L::kTiles, 16, 1024, kSw128);
-      const uint64_t d_p = adv(d_m, 2 * kPanel);
+      const uint64_t d_m = smem_desc(base + L::kOffM + st * L::kM, 16, 1024, kSw128);
+      const uint32_t ks = tbase + col_ks(c);
       take_over(kSReady);
       tc_fence_after();
       if (leader) {
@@ -399,9 +405,14 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k)
-            mma_ts(tbase + kColKS, tbase + kColS + 16 * k + 8 * lo, adv(d_kq, (k / 4) * L::kStride + (k % 4) * 32),
+            mma_ts(ks, tbase + kColS + 16 * k + 8 * lo, adv(d_kq, (k / 4) * L::kStride + (k % 4) * 32),
                    OUT ? id_128 : id_64, lo > 0 || k > 0);
         mma_commit(&bars[kKsDone]);
+      }
+      if (OUT && c > 0) {                                  // while R is made, and then D~
+        take_over(kDlReady);
+        tc_fence_after();
+        if (leader) issue_pd(c - 1, 0, 6);
       }
       take_over(kRReady);
       tc_fence_after();
@@ -411,9 +422,12 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tbase + kColD, tbase + kColKS + 16 * k + 8 * lo, adv(d_m, 32 * k), lo ? id_64 : id_128,
-                   lo > 0 || k > 0);
+            mma_ts(tbase + kColS, ks + 16 * k + 8 * lo, adv(d_m, 32 * k), lo ? id_64 : id_128, lo > 0 || k > 0);
         mma_commit(&bars[kDDone]);
+        if (OUT && c > 0) {
+          issue_pd(c - 1, 6, 12);
+          mma_commit(&bars[kODone]);
+        }
       }
       take_over(kDtReady);
       tc_fence_after();
@@ -425,74 +439,78 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             mma_ts(tbase + kColS, tbase + kColD + 16 * k + 8 * lo, adv(d_k_mn, k * 2048), id_up, lo > 0 || k > 0);
         mma_commit(&bars[kUDone]);
       }
-      if (OUT) {
-        take_over(kDlReady);
-        tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int pass = 0; pass < 3; ++pass)             // += D P: hi hi, hi lo, lo hi
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tbase + kColO, tbase + kColDl + 16 * k + 8 * (pass == 2),
-                     adv(d_p, (pass == 1 ? kPanel : 0) + 32 * k), id_64, 1);
-          mma_commit(&bars[kODone]);
-        }
+    }
+    if (OUT) {
+      take_over(kDlReady);
+      tc_fence_after();
+      if (leader) {
+        issue_pd(n - 1, 0, 12);
+        mma_commit(&bars[kODone]);
       }
-      __syncwarp();
     }
     if (leader) {                                          // nothing in flight when tensor memory is given back
       mma_commit(&bars[kEnd]);
       drain(&bars[kEnd], 0);
     }
-  } else if (warp == 9) {
+  } else if (warp == kLoader) {
     if (lane == 0) {
-      // ---------------------------------------------------------- loads
+      // ---------------------------------------------------------- loads, output stores
       tma_prefetch_desc(&tmk);
       if (OUT) tma_prefetch_desc(&tmq);
+      if (OUT) tma_prefetch_desc(&tmo);
       if (values) tma_prefetch_desc(&tmv);
       const uint8_t *rec = a.records + ((size_t)bh * a.N + (size_t)seg * a.seg_chunks) * kRecBytes;
-      int sent = 0;
-      for (int c = 0; c < n; ++c) {
-        const int st = c % NS, row = t_begin + kC * c;
-        if (c >= NS && !mbar_wait(&bars[kFree + st], (c / NS - 1) & 1, abort_flag)) break;
+      auto load_early = [&](int c) {
+        const int st = c % NS;
         uint8_t *kq = smem + L::kOffKq + st * L::kKq;
-        mbar_arrive_expect_tx(&bars[kKqFull + st], L::kKq + kRecGates + L::kTiles);
+        mbar_arrive_expect_tx(&bars[kKqFull + st], L::kEarly);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          tma_load_3d(kq + p * L::kStride, &tmk, &bars[kKqFull + st], 64 * p, row, kh);
-          if (OUT) tma_load_3d(kq + p * L::kStride + kPanel, &tmq, &bars[kKqFull + st], 64 * p, row, kh);
+          tma_load_3d(kq + p * L::kStride, &tmk, &bars[kKqFull + st], 64 * p, t_begin + kC * c, kh);
+          if (OUT) tma_load_3d(kq + p * L::kStride + kPanel, &tmq, &bars[kKqFull + st], 64 * p, t_begin + kC * c, kh);
         }
-        bulk_load(smem + L::kOffGates + st * kRecGates, rec + (size_t)c * kRecBytes, kRecGates,
-                  &bars[kKqFull + st]);
-        bulk_load(smem + L::kOffTiles + st * L::kTiles, rec + (size_t)c * kRecBytes + kRecM, L::kTiles,
-                  &bars[kKqFull + st]);
-        sent = c + 1;
-        if (values) {
-          if (OUT && c >= NS && !mbar_wait(&bars[kStored + st], (c / NS - 1) & 1, abort_flag)) break;
-          mbar_arrive_expect_tx(&bars[kVFull + st], L::kV);
-          tma_load_3d(smem + L::kOffV + st * L::kV, &tmv, &bars[kVFull + st], 0, row, bh);
-        }
+        bulk_load(smem + L::kOffM + st * L::kM, rec + (size_t)c * kRecBytes + kRecM, L::kM, &bars[kKqFull + st]);
+      };
+      auto load_late = [&](int c) {
+        const int sv = c % NV;
+        mbar_arrive_expect_tx(&bars[kVFull + sv], values ? L::kLate : kRecGates);
+        bulk_load(smem + L::kOffGates + sv * kRecGates, rec + (size_t)c * kRecBytes, kRecGates, &bars[kVFull + sv]);
+        if (values) tma_load_3d(smem + L::kOffV + sv * L::kV, &tmv, &bars[kVFull + sv], 0, t_begin + kC * c, bh);
+        if (OUT)
+          bulk_load(smem + L::kOffP + sv * L::kP, rec + (size_t)c * kRecBytes + kRecP, L::kP, &bars[kVFull + sv]);
+      };
+      int early = 0, late = 0;                             // sent
+      for (; early < n && early < NS; ++early) {
+        load_early(early);
+        load_late(late++);
       }
-      if (*abort_flag)                                     // copies in flight land before the exit
-        for (int c = sent > NS ? sent - NS : 0; c < sent; ++c) {
-          drain(&bars[kKqFull + c % NS], (c / NS) & 1);
-          if (values) drain(&bars[kVFull + c % NS], (c / NS) & 1);
+      if (OUT && late < n) load_late(late++);
+      for (int c = 0; c <= n; ++c) {
+        if (OUT && c > 0) {
+          const int sv = (c - 1) % NV;
+          if (!mbar_wait(&bars[kOutputs + sv], ((c - 1) / NV) & 1, abort_flag)) break;
+          tma_store_3d(&tmo, smem + L::kOffV + sv * L::kV, 0, t_begin + kC * (c - 1), bh);
+          bulk_commit_group();
+          if (late < n) {
+            bulk_wait_read_all();                          // the outputs have left V's place
+            load_late(late++);
+          }
         }
-    }
-  } else if (OUT && warp == 10) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- output stores
-      tma_prefetch_desc(&tmo);
-      for (int c = 0; c < n; ++c) {
-        if (!mbar_wait(&bars[kFree + c % NS], (c / NS) & 1, abort_flag)) break;
-        tma_store_3d(&tmo, smem + L::kOffV + c % NS * L::kV, 0, t_begin + kC * c, bh);
-        bulk_commit_group();
-        bulk_wait_read_all();
-        mbar_arrive(&bars[kStored + c % NS]);
+        if (early < n) {
+          if (!mbar_wait(&bars[kFree + c % NS], (c / NS) & 1, abort_flag)) break;
+          load_early(early++);
+          if (!OUT) load_late(late++);
+        } else if (!OUT) {
+          break;
+        }
       }
       bulk_wait_all();
+      if (*abort_flag) {                                   // copies in flight land before the exit
+        for (int c = early > NS ? early - NS : 0; c < early; ++c) drain(&bars[kKqFull + c % NS], (c / NS) & 1);
+        for (int c = late > NV ? late - NV : 0; c < late; ++c) drain(&bars[kVFull + c % NV], (c / NV) & 1);
+      }
     }
-  } else if (SAVE && warp == 10) {
+  } else if (SAVE && warp == kSaver) {
     if (lane == 0) {
       // ---------------------------------------------------------- saves
       const size_t first = (size_t)bh * a.N + (size_t)seg * a.seg_chunks;
@@ -515,7 +533,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tbase, kTmemCols);
+  if (warp == kIssuer) tmem_dealloc(tbase, kTmemCols);
   if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
 }
 

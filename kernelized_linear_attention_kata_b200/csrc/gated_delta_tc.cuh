@@ -41,16 +41,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(bar, parity, abort_flag));
 }
-// Hardware barrier `id` of the eight state warps and the issuer (288 threads):
-// the state warps pass, the issuer waits for them. Through an mbarrier the same
-// takes 300 cycles instead of 40, three or four times a chunk.
+// The chains' warps: 0-15 the state warps (four warpgroups, each a quarter of the
+// columns of keys or tokens), 16 the MMA issuer, 17 the loads and the output
+// stores, 18 the saves. A pass of the state warps waits for its own tensor memory,
+// shared memory and conversions more than it computes: with 8 warps of twice the
+// columns a pass took 1.5 times as long (1 or 2 warps a scheduler).
+constexpr int kStateWarps = 16, kIssuer = 16, kLoader = 17, kSaver = 18, kChainThreads = 19 * 32;
+
+// Hardware barrier `id` of the state warps and the issuer: the state warps pass,
+// the issuer waits for them. Through an mbarrier the same takes 300 cycles
+// instead of 40, three or four times a chunk.
 __device__ __forceinline__ void hand_over(int id) {
   __syncwarp();
-  asm volatile("bar.arrive %0, 288;" ::"r"(id) : "memory");
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(32 * (kStateWarps + 1)) : "memory");
 }
 __device__ __forceinline__ void take_over(int id) {
   __syncwarp();
-  asm volatile("bar.sync %0, 288;" ::"r"(id) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(32 * (kStateWarps + 1)) : "memory");
 }
 // One arrival for a warp, after all its lanes got here.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -323,13 +330,13 @@ __device__ __forceinline__ void store_inverse(const float *Lm, uint8_t *hi_tile,
   }
 }
 
-// 32 values of a thread's row (one TMEM lane) as an operand, in 16-deep steps
-// of hi, then lo.
-__device__ __forceinline__ void put32(uint32_t col, const float2 *x) {
-  uint32_t y[32];
+// 16 values of a thread's row (one TMEM lane) as an operand: a 16-deep step of
+// hi, then of lo.
+__device__ __forceinline__ void put16(uint32_t col, const float2 *x) {
+  uint32_t y[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) split2(x[i], y[16 * (i / 8) + i % 8], y[16 * (i / 8) + 8 + i % 8]);
-  tmem_st32(col, y);
+  for (int i = 0; i < 8; ++i) split2(x[i], y[i], y[8 + i]);
+  tmem_st16(col, y);
 }
 // 8 x COUNT values of row `row` of a saved image (128-byte rows, 64 values a
 // panel of `rows` rows), from value `first`; the hi or the lo halves.
