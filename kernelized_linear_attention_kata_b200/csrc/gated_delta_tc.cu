@@ -25,8 +25,8 @@
 // What bounds it: the chain S -> K S -> R -> D -> S' of one chunk, three MMA
 // rounds and three passes of the value threads over the columns. What does
 // not depend on S is kept off it: M, P and the decays come ready from the
-// solve (gated_delta_solve.cu), a chunk's P D runs in the two gaps that the next
-// one leaves the tensor core, and its outputs leave during the next one's update. With fewer heads than SMs the sequence is cut into G
+// solve (gated_delta_solve.cu), and a chunk's P D runs while the state warps make
+// S' and its operand, its outputs leave during the next one's K S. With fewer heads than SMs the sequence is cut into G
 // segments: each but the last is first walked for its effect on a state, S_end =
 // F S_start + B (the same kernel without outputs, once on V from S = 0 and once
 // with V = 0 from S = I), a small kernel joins them, and the segments then run
@@ -52,7 +52,7 @@ constexpr uint32_t kTmemCols = 512;
 // rewriting only what it has read:
 //   kColS     S operand; M R with M hi, with M lo; the update
 //   col_ks(c) [K; Q] S, in two places by turns; R operand in K S's, then P D, which
-//             with Q S stays until the next chunk's update
+//             with Q S stays into the next chunk
 //   kColD     D~ operand;  kColDl  D operand
 constexpr uint32_t kColS = 0, kColKS = 128, kColD = 384, kColDl = 448;
 __device__ __forceinline__ uint32_t col_ks(int c) { return kColKS + 128 * (c & 1); }
@@ -199,6 +199,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     // outputs of chunk c, o_t = e^{G_t} (Q S)_t + (P D)_t, 16 tokens a thread,
     // into the places its values of V were read from
     auto outputs = [&](int c) {
+      ok &= warp_wait(&bars[kODone], c & 1, abort_flag);
+      tc_fence_after();
       if (active) {
         __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffV + c % NV * L::kV) +
                              16 * h * DV + r;
@@ -234,6 +236,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       tc_fence_before();
       hand_over(kSReady);
+      if (OUT && c > 0) outputs(c - 1);
       if (SAVE) {
         ok &= stage_free(3 * c);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
@@ -304,17 +307,12 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       hand_over(kDtReady);
       const float whole = from_start[kC - 1];
       if (OUT) {
-        if (c > 0) {                                       // P D of the chunk before has read its D
-          ok &= warp_wait(&bars[kODone], (c - 1) & 1, abort_flag);
-          tc_fence_after();
-        }
         if (active) {
           put16(col_part + kColDl, d);
           tmem_wait_st();
         }
         tc_fence_before();
         hand_over(kDlReady);
-        if (c > 0) outputs(c - 1);
       }
 
       if (SAVE) {
@@ -344,8 +342,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       warp_arrive(&bars[kFree + st]);
     }
     if (OUT) {
-      ok &= warp_wait(&bars[kODone], (n - 1) & 1, abort_flag);
-      tc_fence_after();
       outputs(n - 1);
     }
     if (active && ok) {
@@ -382,14 +378,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     const bool leader = lane == 0;
     const uint32_t base = smem_u32(smem);
     auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
-    // D P of chunk c, MMAs from .. to of 12: hi hi, hi lo, lo hi
-    auto issue_pd = [&](int c, int from, int to) {
-      const uint64_t d_p = smem_desc(base + L::kOffP + c % NV * L::kP, 16, 1024, kSw128);
-#pragma unroll
-      for (int m = from; m < to; ++m)
-        mma_ts(tbase + col_ks(c), tbase + kColDl + 16 * (m % 4) + 8 * (m / 8),
-               adv(d_p, (m / 4 == 1 ? kPanel : 0) + 32 * (m % 4)), id_64, m > 0);
-    };
     for (int c = 0; c < n; ++c) {
       const int st = c % NS;
       const uint64_t d_kq = smem_desc(base + L::kOffKq + st * L::kKq, 16, 1024, kSw128);
@@ -409,11 +397,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                    OUT ? id_128 : id_64, lo > 0 || k > 0);
         mma_commit(&bars[kKsDone]);
       }
-      if (OUT && c > 0) {                                  // while R is made, and then D~
-        take_over(kDlReady);
-        tc_fence_after();
-        if (leader) issue_pd(c - 1, 0, 6);
-      }
       take_over(kRReady);
       tc_fence_after();
       if (leader) {
@@ -424,10 +407,6 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           for (int k = 0; k < 4; ++k)
             mma_ts(tbase + kColS, ks + 16 * k + 8 * lo, adv(d_m, 32 * k), lo ? id_64 : id_128, lo > 0 || k > 0);
         mma_commit(&bars[kDDone]);
-        if (OUT && c > 0) {
-          issue_pd(c - 1, 6, 12);
-          mma_commit(&bars[kODone]);
-        }
       }
       take_over(kDtReady);
       tc_fence_after();
@@ -439,13 +418,19 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             mma_ts(tbase + kColS, tbase + kColD + 16 * k + 8 * lo, adv(d_k_mn, k * 2048), id_up, lo > 0 || k > 0);
         mma_commit(&bars[kUDone]);
       }
-    }
-    if (OUT) {
-      take_over(kDlReady);
-      tc_fence_after();
-      if (leader) {
-        issue_pd(n - 1, 0, 12);
-        mma_commit(&bars[kODone]);
+      if (OUT) {
+        const uint64_t d_p = smem_desc(base + L::kOffP + c % NV * L::kP, 16, 1024, kSw128);
+        take_over(kDlReady);
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int pass = 0; pass < 3; ++pass)             // D P: hi hi, hi lo, lo hi
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(ks, tbase + kColDl + 16 * k + 8 * (pass == 2), adv(d_p, (pass == 1 ? kPanel : 0) + 32 * k),
+                     id_64, pass > 0 || k > 0);
+          mma_commit(&bars[kODone]);
+        }
       }
     }
     if (leader) {                                          // nothing in flight when tensor memory is given back
