@@ -26,7 +26,7 @@
 // rounds and three passes of the value threads over the columns. What does
 // not depend on S is kept off it: M, P and the decays come ready from the
 // solve (gated_delta_solve.cu), and a chunk's P D runs while the state warps make
-// S' and its operand, its outputs leave during the next one's K S. With fewer heads than SMs the sequence is cut into G
+// S' and its operand, its outputs leave during the next one's K S (d_k = 64: M R). With fewer heads than SMs the sequence is cut into G
 // segments: each but the last is first walked for its effect on a state, S_end =
 // F S_start + B (the same kernel without outputs, once on V from S = 0 and once
 // with V = 0 from S = I), a small kernel joins them, and the segments then run
@@ -94,7 +94,7 @@ template <int DK, int DV, int MODE> struct Layout {
 // state warps alone: they wait for the loads and fold them into their own arrivals.
 enum {
   kKqFull = 0, kVFull = 4, kFree = 8, kOutputs = 12, kKsDone = 16, kDDone, kUDone, kODone, kStaged, kSaved, kEnd,
-  kNumBars
+  kNumBars = kEnd + 2
 };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
 // hardware barriers, state warps to issuers (0 is the block's)
@@ -159,6 +159,29 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+
+  // P D of chunk c, by a whole warp. For d_k = 64 a warp of its own issues it
+  // while the issuer goes on: P D takes as long as K S, which the state warps then
+  // wait for (94 us instead of 103 at 128 heads of 2048 tokens). For d_k = 128 it
+  // comes after the update, which it would only slow down (792 us instead of 817 at
+  // 16 heads of 131072).
+  constexpr bool kOwnPd = DK == 64;
+  auto issue_pd = [&](int c) {
+    constexpr uint32_t id_64 = idesc_bf16(128, 64, false, false);
+    const uint32_t acc = tbase + col_ks(c);
+    const uint64_t d_p = smem_desc(smem_u32(smem) + L::kOffP + c % NV * L::kP, 16, 1024, kSw128);
+    take_over(kDlReady);
+    tc_fence_after();
+    if (lane == 0) {
+#pragma unroll
+      for (int pass = 0; pass < 3; ++pass)                 // hi hi, hi lo, lo hi
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ts(acc, tbase + kColDl + 16 * k + 8 * (pass == 2),
+                 d_p + (uint64_t)(((pass == 1 ? kPanel : 0) + 32 * k) >> 4), id_64, pass > 0 || k > 0);
+      mma_commit(&bars[kODone]);
+    }
+  };
 
   if (warp < kStateWarps) {
     // ------------------------------------------------------------ state warps
@@ -236,7 +259,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       tc_fence_before();
       hand_over(kSReady);
-      if (OUT && c > 0) outputs(c - 1);
+      if (OUT && !kOwnPd && c > 0) outputs(c - 1);
       if (SAVE) {
         ok &= stage_free(3 * c);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
@@ -275,6 +298,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       }
       tc_fence_before();
       hand_over(kRReady);
+      if (OUT && kOwnPd && c > 0) outputs(c - 1);
       if (SAVE) {
         ok &= stage_free(3 * c + 1);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
@@ -418,24 +442,17 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             mma_ts(tbase + kColS, tbase + kColD + 16 * k + 8 * lo, adv(d_k_mn, k * 2048), id_up, lo > 0 || k > 0);
         mma_commit(&bars[kUDone]);
       }
-      if (OUT) {
-        const uint64_t d_p = smem_desc(base + L::kOffP + c % NV * L::kP, 16, 1024, kSw128);
-        take_over(kDlReady);
-        tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int pass = 0; pass < 3; ++pass)             // D P: hi hi, hi lo, lo hi
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(ks, tbase + kColDl + 16 * k + 8 * (pass == 2), adv(d_p, (pass == 1 ? kPanel : 0) + 32 * k),
-                     id_64, pass > 0 || k > 0);
-          mma_commit(&bars[kODone]);
-        }
-      }
+      if (OUT && !kOwnPd) issue_pd(c);
     }
     if (leader) {                                          // nothing in flight when tensor memory is given back
       mma_commit(&bars[kEnd]);
       drain(&bars[kEnd], 0);
+    }
+  } else if (OUT && kOwnPd && warp == kSaver) {
+    for (int c = 0; c < n; ++c) issue_pd(c);
+    if (lane == 0) {
+      mma_commit(&bars[kEnd + 1]);
+      drain(&bars[kEnd + 1], 0);
     }
   } else if (warp == kLoader) {
     if (lane == 0) {
