@@ -28,9 +28,8 @@
 // solve (gated_delta_solve.cu), and a chunk's P D runs while the state warps make
 // S' and its operand, its outputs leave during the next one's K S (d_k = 64: M R). With fewer heads than SMs the sequence is cut into G
 // segments: each but the last is first walked for its effect on a state, S_end =
-// F S_start + B (the same kernel without outputs, once on V from S = 0 and once
-// with V = 0 from S = I), a small kernel joins them, and the segments then run
-// side by side. For the gradient the same kernel without outputs saves every
+// F S_start + B (gated_delta_effect.cu), a small kernel joins them, and the segments
+// then run side by side. For the gradient the same kernel without outputs saves every
 // chunk's S and D (gated_delta_bwd_tc.cu).
 //
 // An MMA takes 70-85 cycles here whatever its N (from one issuing thread or from
@@ -58,12 +57,8 @@ constexpr uint32_t kColS = 0, kColKS = 128, kColD = 384, kColDl = 448;
 __device__ __forceinline__ uint32_t col_ks(int c) { return kColKS + 128 * (c & 1); }
 __device__ __forceinline__ uint32_t col_qs(int c) { return col_ks(c) + 64; }
 
-// kOut: outputs of segments 0 .. G - 1. kEffect: the effect of segments on a
-// state, of two kinds: first the blocks for B of segments 0 .. G - 2, from V and S = 0
-// (segment 0: from S0, which makes its B the next one's starting state), then
-// those for F of segments 1 .. G - 2, from S = I without V.
-// kSave: each chunk's starting state and writes for the gradient.
-enum Mode { kOut, kEffect, kSave };
+// kOut: outputs. kSave: each chunk's starting state and writes for the gradient.
+enum Mode { kOut, kSave };
 
 template <int DK, int DV, int MODE> struct Layout {
   static constexpr int NP = DK / 64;                       // panels of a K or Q tile
@@ -104,13 +99,11 @@ struct Args {
   const float *g, *beta, *S0;
   float *S_out;
   uint8_t *img_S, *img_D;          // kSave
-  float *F;                        // segments' effects, kind 1; kind 0 goes to starts
   const uint8_t *records;          // [BH][N]
-  float *starts;                   // segments' starting states [BH][G][DK][DV], 1 .. G - 1 used
+  const float *starts;             // segments' starting states [BH][G][DK][DV], 1 .. G - 1 used
   unsigned *status;
   int H, Hk, T, N, G, seg_chunks;
   int dk, dv;                      // the tensors' head sizes, <= DK, DV
-  int kind0;                       // kEffect: blocks of the first kind
 };
 
 template <int DK, int DV, int MODE>
@@ -130,17 +123,12 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
   const float *gates = reinterpret_cast<const float *>(smem + L::kOffGates);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int kind = MODE == kEffect && (int)blockIdx.x >= a.kind0 ? 1 : 0;
-  const int segs = MODE == kEffect ? a.G - 1 - kind : a.G;
-  const int job = (int)blockIdx.x - (kind ? a.kind0 : 0);
-  const int seg = job % segs + kind;
-  const int bh = job / segs;
+  const int seg = blockIdx.x % a.G, bh = blockIdx.x / a.G;
   const int kh = bh / a.H * a.Hk + bh % a.H / (a.H / a.Hk);
   const int t_begin = seg * a.seg_chunks * kC;
   const int t_left = a.T - t_begin;
   const int nall = t_left <= 0 ? 0 : (t_left - 1) / kC + 1;
   const int n = nall < a.seg_chunks ? nall : a.seg_chunks;
-  const bool values = MODE != kEffect || kind == 0;                    // V is read
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
@@ -188,8 +176,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     const int h = warp / 4;                                // quarter of the columns
     const int r = 32 * (warp % 4) + lane;                  // value column
     const uint32_t lane_off = (uint32_t)(32 * (warp % 4)) << 16;
-    const int width = values ? DV : DK;                    // value columns (kind 1: those of I)
-    const bool active = r < width;                         // the same in the whole warp
+    const bool active = r < DV;                            // the same in the whole warp
     constexpr int HK = DK / 4;                             // state entries a thread
     float2 S[HK / 2];
     {
@@ -198,11 +185,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       const int rows = given ? a.dk : DK, ld = given ? a.dv : DV;
       if (given)
         src = a.S0 ? a.S0 + (size_t)bh * rows * ld : nullptr;
-      else if (MODE != kEffect)
+      else
         src = a.starts + ((size_t)bh * a.G + seg) * DK * DV;
-      auto entry = [&](int k) {
-        return src ? (r < ld && k < rows ? src[(size_t)k * ld + r] : 0.f) : (kind == 1 && k == r ? 1.f : 0.f);
-      };
+      auto entry = [&](int k) { return src && r < ld && k < rows ? src[(size_t)k * ld + r] : 0.f; };
 #pragma unroll
       for (int i = 0; i < HK / 2; ++i) S[i] = make_float2(entry(HK * h + 2 * i), entry(HK * h + 2 * i + 1));
     }
@@ -274,7 +259,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + sv * L::kV) + 16 * h * DV + r;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          V[i] = active && values ? (uint32_t)v[2 * i * DV] | (uint32_t)v[(2 * i + 1) * DV] << 16 : 0u;
+          V[i] = active ? (uint32_t)v[2 * i * DV] | (uint32_t)v[(2 * i + 1) * DV] << 16 : 0u;
       }
       ok &= warp_wait(&bars[kKsDone], c & 1, abort_flag);
       tc_fence_after();
@@ -368,26 +353,15 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     if (OUT) {
       outputs(n - 1);
     }
-    if (active && ok) {
-      float *dst = nullptr;
-      int ld = DV, rows = DK;
-      if (MODE != kEffect) {
-        ld = a.dv;
-        rows = a.dk;
-        if (OUT && seg == a.G - 1 && a.S_out && r < ld) dst = a.S_out + (size_t)bh * rows * ld;
-      } else if (kind == 0) {
-        dst = a.starts + ((size_t)bh * a.G + seg + 1) * DK * DV;
-      } else {
-        dst = a.F + ((size_t)bh * segs + seg - 1) * DK * DK;
-        ld = DK;
-      }
-      if (dst) {
+    if (OUT && ok && seg == a.G - 1 && a.S_out && r < a.dv) {
+      float *dst = a.S_out + (size_t)bh * a.dk * a.dv + r;
 #pragma unroll
-        for (int i = 0; i < HK / 2; ++i)
-          if (HK * h + 2 * i < rows) {                     // even
-            dst[(size_t)(HK * h + 2 * i) * ld + r] = S[i].x;
-            dst[(size_t)(HK * h + 2 * i + 1) * ld + r] = S[i].y;
-          }
+      for (int i = 0; i < HK / 2; ++i) {
+        const int k = HK * h + 2 * i;
+        if (k < a.dk) {                                    // even
+          dst[(size_t)k * a.dv] = S[i].x;
+          dst[(size_t)(k + 1) * a.dv] = S[i].y;
+        }
       }
     }
   } else if (warp == kIssuer) {
@@ -460,7 +434,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       tma_prefetch_desc(&tmk);
       if (OUT) tma_prefetch_desc(&tmq);
       if (OUT) tma_prefetch_desc(&tmo);
-      if (values) tma_prefetch_desc(&tmv);
+      tma_prefetch_desc(&tmv);
       const uint8_t *rec = a.records + ((size_t)bh * a.N + (size_t)seg * a.seg_chunks) * kRecBytes;
       auto load_early = [&](int c) {
         const int st = c % NS;
@@ -475,9 +449,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       };
       auto load_late = [&](int c) {
         const int sv = c % NV;
-        mbar_arrive_expect_tx(&bars[kVFull + sv], values ? L::kLate : kRecGates);
+        mbar_arrive_expect_tx(&bars[kVFull + sv], L::kLate);
         bulk_load(smem + L::kOffGates + sv * kRecGates, rec + (size_t)c * kRecBytes, kRecGates, &bars[kVFull + sv]);
-        if (values) tma_load_3d(smem + L::kOffV + sv * L::kV, &tmv, &bars[kVFull + sv], 0, t_begin + kC * c, bh);
+        tma_load_3d(smem + L::kOffV + sv * L::kV, &tmv, &bars[kVFull + sv], 0, t_begin + kC * c, bh);
         if (OUT)
           bulk_load(smem + L::kOffP + sv * L::kP, rec + (size_t)c * kRecBytes + kRecP, L::kP, &bars[kVFull + sv]);
       };
@@ -561,17 +535,16 @@ cudaError_t launch(const char *name, const GatedDeltaLaunch &a, int d_k, int d_v
       !make_tma_3d_bf16_box(&m[2], a.v, d_v, a.T, a.BH, DV, kC, false) ||
       !make_tma_3d_bf16_box(&m[3], o, d_v, a.T, a.BH, DV, kC, false))
     return cudaErrorInvalidValue;
-  const int kind0 = (int)(a.BH * (a.G - 1));
-  const Args x{a.g, a.beta, a.S0, a.S_out, a.img_S, a.img_D, a.F, a.records, a.starts_seg,
-               a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks, d_k, d_v, kind0};
-  return run_chain<DK, DV, MODE>(name, a, m, x, MODE == kEffect ? kind0 + a.BH * (a.G - 2) : a.BH * a.G);
+  const Args x{a.g, a.beta, a.S0, a.S_out, a.img_S, a.img_D, a.records, a.starts_seg,
+               a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks, d_k, d_v};
+  return run_chain<DK, DV, MODE>(name, a, m, x, a.BH * a.G);
 }
 
 }  // namespace
 
 // Segments a head, by the time they should take in chunks of the output pass
-// (3.6 us): a wave runs one block an SM; an effect chunk costs 0.9; the gradient's
-// save, reverse and reverse effect chunks 1.3, 1.5 and 1.2; a join step 0.8, and a
+// (3.4 us): a wave runs one block an SM; an effect chunk costs 0.75; the gradient's
+// save, reverse and reverse effect chunks 1.2, 1.5 and 1; a join step 0.8, and a
 // further launch 2.
 void gd_tc_split(long long BH, int N, bool gradient, int *G, int *seg_chunks) {
   int best = 1;
@@ -580,9 +553,9 @@ void gd_tc_split(long long BH, int N, bool gradient, int *G, int *seg_chunks) {
   for (int g = 1; g <= 64 && (g == 1 || (long long)g * BH <= kGdSms); ++g) {
     const int per = (N + g - 1) / g, used = per > 0 ? (N + per - 1) / per : 1;
     if (used != g) continue;
-    double time = (gradient ? 1.3 + 1.5 : 1.0) * waves(BH * g) * per;
+    double time = (gradient ? 1.2 + 1.5 : 1.0) * waves(BH * g) * per;
     if (g > 1)
-      time += (0.9 * waves(BH * (2 * g - 3)) + (gradient ? 1.2 * waves(BH * (g - 1)) : 0.0)) * per +
+      time += (0.75 + (gradient ? 1.0 : 0.0)) * waves(BH * (g - 1)) * per +
               (g > 2 ? 2.0 + 0.8 * (g - 2) : 0.0) + (gradient ? 4.0 : 2.0);
     if (time < least) {
       least = time;
@@ -593,12 +566,6 @@ void gd_tc_split(long long BH, int N, bool gradient, int *G, int *seg_chunks) {
   *seg_chunks = (N + best - 1) / best;
 }
 
-cudaError_t gd_tc_effect(const GatedDeltaLaunch &a, int d_k, int d_v) {
-  if (a.G == 1) return cudaSuccess;
-#define GD_RUN(DK, DV) launch<DK, DV, kEffect>("gd_tc_segment", a, d_k, d_v)
-  return GD_TC_DISPATCH(GD_RUN);
-#undef GD_RUN
-}
 cudaError_t gd_tc_save(const GatedDeltaLaunch &a, int d_k, int d_v) {
 #define GD_RUN(DK, DV) launch<DK, DV, kSave>("gd_tc_save", a, d_k, d_v)
   return GD_TC_DISPATCH(GD_RUN);
