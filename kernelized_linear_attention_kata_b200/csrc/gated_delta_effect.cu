@@ -28,13 +28,15 @@ constexpr uint32_t kTmemCols = 512, kChain = 256, kColKS = 128, kColD = 192;
 template <int DK, int DV> struct Layout {
   static constexpr int NP = DK / 64;
   static constexpr int kK = NP * kPanel, kM = 2 * kPanel, kV = kC * DV * 2;
-  static constexpr int kOne = kK + kM + kV + kRecGates, kRoom = 232448 - 512 - 1024;
+  static constexpr int kState = DK == 128 ? DK * DK * 4 : 0;   // F's state (see below)
+  static constexpr int kOne = kK + kM + kV + kRecGates, kRoom = 232448 - 512 - 1024 - kState;
   static constexpr int NS = kRoom / kOne < 4 ? kRoom / kOne : 4;   // stages of loads
   static constexpr int kOffK = 0;
   static constexpr int kOffM = NS * kK;
   static constexpr int kOffV = kOffM + NS * kM;
   static constexpr int kOffGates = kOffV + NS * kV;
-  static constexpr int kOffBars = kOffGates + NS * kRecGates;
+  static constexpr int kOffState = kOffGates + NS * kRecGates;
+  static constexpr int kOffBars = kOffState + kState;
   static constexpr int kBytes = kOffBars + 512 + 1024;
   static_assert(NS >= 2 && kBytes <= 232448, "shared memory budget");
 };
@@ -91,7 +93,12 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     const int r = 32 * (warp % 4) + lane;                  // value column
     const uint32_t col = tbase + ((uint32_t)(32 * (warp % 4)) << 16);
     constexpr int HK = DK / 4;
+    // The states, in registers; F's of d_k = 128 in shared memory [k][column]: both
+    // are 64 registers, which leaves too few for the rest (spilled, the loads went
+    // to the L2, and a chunk took 10.8K cycles).
+    constexpr bool kInSmem = L::kState > 0;
     float2 S[2][HK / 2];
+    float *Fs = reinterpret_cast<float *>(smem + L::kOffState) + HK * h * DK + r;
     {
       const float *src = seg == 0 && a.S0 ? a.S0 + (size_t)bh * a.dk * a.dv : nullptr;
       auto given = [&](int k) { return src && r < a.dv && k < a.dk ? src[(size_t)k * a.dv + r] : 0.f; };
@@ -99,16 +106,32 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
       for (int i = 0; i < HK / 2; ++i) {
         const int k = HK * h + 2 * i;
         S[0][i] = make_float2(given(k), given(k + 1));
-        S[1][i] = make_float2(k == r ? 1.f : 0.f, k + 1 == r ? 1.f : 0.f);
+        const float2 one = make_float2(k == r ? 1.f : 0.f, k + 1 == r ? 1.f : 0.f);
+        if (kInSmem) {
+          Fs[2 * i * DK] = one.x;
+          Fs[(2 * i + 1) * DK] = one.y;
+        } else {
+          S[1][i] = one;
+        }
       }
     }
     bool ok = true;
     auto runs = [&](int x) { return x == 0 || dual; };
     auto active = [&](int x) { return r < (x == 0 ? DV : DK); };       // the same in the whole warp
+    auto state16 = [&](int x, int b, float2 (&y)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        y[i] = kInSmem && x == 1 ? make_float2(Fs[(16 * b + 2 * i) * DK], Fs[(16 * b + 2 * i + 1) * DK])
+                                 : S[x][8 * b + i];
+    };
     auto put_state = [&](int x) {
       if (active(x)) {
 #pragma unroll
-        for (int b = 0; b < HK / 16; ++b) put16(col + kChain * x + HK * h + 16 * b, S[x] + 8 * b);
+        for (int b = 0; b < HK / 16; ++b) {
+          float2 y[8];
+          state16(x, b, y);
+          put16(col + kChain * x + HK * h + 16 * b, y);
+        }
         tmem_wait_st();
       }
       tc_fence_before();
@@ -122,13 +145,8 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     for (int c = 0; c < n; ++c) {
       const int st = c % NS;
       const float *from_start = gates + st * (kRecGates / 4), *to_end = from_start + kC, *beta = to_end + kC;
-      uint32_t V[8];                                       // two tokens a register
-      {
-        const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + st * L::kV) + 16 * h * DV + r;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          V[i] = active(0) ? (uint32_t)v[2 * i * DV] | (uint32_t)v[(2 * i + 1) * DV] << 16 : 0u;
-      }
+      const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + L::kOffV + st * L::kV) + 16 * h * DV + r;
+      auto value = [&](int i) { return __uint_as_float((uint32_t)v[i * DV] << 16); };
       // R = beta (V - e^G (K S)); beta (- e^G (K S))
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -142,14 +160,11 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
           tmem_ld16(at, y);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float4 f = gate4(from_start, 16 * h + 2 * i), b = gate4(beta, 16 * h + 2 * i);
-            const float2 v0 = x == 0 ? as_float2(V[i] << 16, V[i] & 0xffff0000u) : make_float2(0.f, 0.f);
-            const float2 v1 = x == 0 ? as_float2(V[i + 1] << 16, V[i + 1] & 0xffff0000u) : make_float2(0.f, 0.f);
-            z[i] = __ffma2_rn(make_float2(-f.x, -f.y), as_float2(y[2 * i], y[2 * i + 1]), v0);
-            z[i + 1] = __ffma2_rn(make_float2(-f.z, -f.w), as_float2(y[2 * i + 2], y[2 * i + 3]), v1);
-            z[i] = __fmul2_rn(make_float2(b.x, b.y), z[i]);
-            z[i + 1] = __fmul2_rn(make_float2(b.z, b.w), z[i + 1]);
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = *reinterpret_cast<const float2 *>(from_start + 16 * h + 2 * i);
+            const float2 b = *reinterpret_cast<const float2 *>(beta + 16 * h + 2 * i);
+            const float2 v2 = x == 0 ? make_float2(value(2 * i), value(2 * i + 1)) : make_float2(0.f, 0.f);
+            z[i] = __fmul2_rn(b, __ffma2_rn(make_float2(-f.x, -f.y), as_float2(y[2 * i], y[2 * i + 1]), v2));
           }
           put16(at, z);
           tmem_wait_st();
@@ -170,12 +185,9 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
           tmem_ld16(col + kChain * x + 64 + 16 * h, w);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float4 f = gate4(to_end, 16 * h + 2 * i);
-            z[i] = __fmul2_rn(make_float2(f.x, f.y), __fadd2_rn(as_float2(y[2 * i], y[2 * i + 1]),
-                                                                as_float2(w[2 * i], w[2 * i + 1])));
-            z[i + 1] = __fmul2_rn(make_float2(f.z, f.w), __fadd2_rn(as_float2(y[2 * i + 2], y[2 * i + 3]),
-                                                                    as_float2(w[2 * i + 2], w[2 * i + 3])));
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = *reinterpret_cast<const float2 *>(to_end + 16 * h + 2 * i);
+            z[i] = __fmul2_rn(f, __fadd2_rn(as_float2(y[2 * i], y[2 * i + 1]), as_float2(w[2 * i], w[2 * i + 1])));
           }
           put16(col + kChain * x + kColD + 16 * h, z);
           tmem_wait_st();
@@ -198,8 +210,15 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
               tmem_ld16(col + kChain * x + HK * h + 16 * b, y);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                S[x][8 * b + i] = __ffma2_rn(w2, S[x][8 * b + i], as_float2(y[2 * i], y[2 * i + 1]));
+              for (int i = 0; i < 8; ++i) {
+                const int k = 16 * b + 2 * i;
+                if (kInSmem && x == 1) {
+                  Fs[k * DK] = fmaf(whole, Fs[k * DK], __uint_as_float(y[2 * i]));
+                  Fs[(k + 1) * DK] = fmaf(whole, Fs[(k + 1) * DK], __uint_as_float(y[2 * i + 1]));
+                } else {
+                  S[x][8 * b + i] = __ffma2_rn(w2, S[x][8 * b + i], as_float2(y[2 * i], y[2 * i + 1]));
+                }
+              }
             }
           }
         }
@@ -219,8 +238,8 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
           B[(k + 1) * DV + r] = S[0][i].y;
         }
         if (dual && active(1)) {
-          F[k * DK + r] = S[1][i].x;
-          F[(k + 1) * DK + r] = S[1][i].y;
+          F[k * DK + r] = kInSmem ? Fs[2 * i * DK] : S[1][i].x;
+          F[(k + 1) * DK + r] = kInSmem ? Fs[(2 * i + 1) * DK] : S[1][i].y;
         }
       }
     }
