@@ -10,6 +10,7 @@ only provides device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -313,10 +314,12 @@ class _On:
             guard.__exit__(*exc)
 
 
+@functools.lru_cache(maxsize=1024)
 def fwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, dtype=torch.bfloat16) -> int:
     return int(lib().kata_fwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, _DTYPES[dtype]))
 
 
+@functools.lru_cache(maxsize=1024)
 def bwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, dtype=torch.bfloat16) -> int:
     return int(lib().kata_bwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, _DTYPES[dtype]))
 

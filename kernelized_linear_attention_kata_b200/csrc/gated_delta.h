@@ -82,6 +82,14 @@ cudaError_t gd_sum_groups(const GatedDeltaLaunch &a, int d_k, bool bf16);
 size_t gd_tc_state_image(int d_k, int d_v);
 size_t gd_tc_write_image(int d_v);
 cudaError_t gd_tc_forward(const GatedDeltaLaunch &a, int d_k, int d_v);
+// Lets `kern` use `bytes` of dynamic shared memory on the current device; on every
+// call, since a device reset forgets it.
+#define GD_ALLOW_SMEM(kern, bytes)                                                                          \
+  do {                                                                                                      \
+    const cudaError_t e_ = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(bytes)); \
+    if (e_ != cudaSuccess) return e_;                                                                       \
+  } while (0)
+
 template <typename Tin> cudaError_t gated_delta_step(const GatedDeltaStep &a, int d_k, int d_v);
 
 }  // namespace kata

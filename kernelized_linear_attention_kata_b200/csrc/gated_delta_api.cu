@@ -165,8 +165,9 @@ kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const void *v, 
   if (a.BH > 0 && T > 0 &&
       (!q || !k || !v || !g || !beta || !o || (tc && !aligned16({q, k, v, o}))))
     return KATA_ERR_INVALID_ARGUMENT;
-  if (cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
-  if (a.BH == 0 || T == 0) return pass_state(S0, S_out, state, a.stream);
+  const bool empty = a.BH == 0 || T == 0;                  // the fp32 kernels write the status themselves
+  if ((tc || empty) && cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
+  if (empty) return pass_state(S0, S_out, state, a.stream);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.o = o; a.S0 = S0; a.S_out = S_out;
   a.status = static_cast<unsigned *>(workspace);
   const cudaError_t e = tc ? gd_tc_forward(a, d_k, d_v) : gd_f32(a, d_k, d_v);
@@ -200,8 +201,9 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
       (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta ||
        (tc && !aligned16({q, k, v, dout, dq, dk, dv}))))
     return KATA_ERR_INVALID_ARGUMENT;
-  if (cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
-  if (a.BH == 0 || T == 0) return pass_state(dS, dS0, state, a.stream);
+  const bool empty = a.BH == 0 || T == 0;                  // the fp32 kernels write the status themselves
+  if ((tc || empty) && cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
+  if (empty) return pass_state(dS, dS0, state, a.stream);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
   a.dout = dout; a.dS = dS; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
   a.status = static_cast<unsigned *>(workspace);

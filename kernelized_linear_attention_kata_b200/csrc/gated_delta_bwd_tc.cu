@@ -170,12 +170,9 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       if (active) {
         float2 y[8];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float4 f = gate4(from_start, 16 * h + 2 * j);
+        for (int j = 0; j < 8; ++j) {
           const int t = 16 * h + 2 * j;
-          y[j] = __fmul2_rn(make_float2(f.x, f.y), as_float2((uint32_t)*at(t) << 16, (uint32_t)*at(t + 1) << 16));
-          y[j + 1] = __fmul2_rn(make_float2(f.z, f.w),
-                                as_float2((uint32_t)*at(t + 2) << 16, (uint32_t)*at(t + 3) << 16));
+          y[j] = __fmul2_rn(gate2(from_start, t), as_float2((uint32_t)*at(t) << 16, (uint32_t)*at(t + 1) << 16));
         }
         put16(col_part + kColG, y);
       }
@@ -196,11 +193,8 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         tmem_ld16(col_part + kColU, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float4 f = gate4(to_end, 16 * h + 2 * j);
-          z[j] = __ffma2_rn(make_float2(f.x, f.y), as_float2(x[2 * j], x[2 * j + 1]), z[j]);
-          z[j + 1] = __ffma2_rn(make_float2(f.z, f.w), as_float2(x[2 * j + 2], x[2 * j + 3]), z[j + 1]);
-        }
+        for (int j = 0; j < 8; ++j)
+          z[j] = __ffma2_rn(gate2(to_end, 16 * h + 2 * j), as_float2(x[2 * j], x[2 * j + 1]), z[j]);
         put16(col_part + kColU, z);
         tmem_wait_st();
       }
@@ -223,12 +217,10 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         tmem_ld16(col_part + kColD + 64, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float4 f = gate4(from_start, 16 * h + 2 * j), b = gate4(beta, 16 * h + 2 * j);
+        for (int j = 0; j < 8; ++j) {
+          const float2 f = gate2(from_start, 16 * h + 2 * j), b = gate2(beta, 16 * h + 2 * j);
           d[j] = __fadd2_rn(as_float2(x[2 * j], x[2 * j + 1]), as_float2(y[2 * j], y[2 * j + 1]));
-          d[j + 1] = __fadd2_rn(as_float2(x[2 * j + 2], x[2 * j + 3]), as_float2(y[2 * j + 2], y[2 * j + 3]));
           z[j] = __fmul2_rn(make_float2(-f.x * b.x, -f.y * b.y), d[j]);
-          z[j + 1] = __fmul2_rn(make_float2(-f.z * b.z, -f.w * b.w), d[j + 1]);
         }
         put16(col_part + kColD, z);
         tmem_wait_st();
@@ -440,8 +432,7 @@ template <int DK, int DV, bool EFFECT> cudaError_t launch(const GatedDeltaLaunch
     return cudaErrorInvalidValue;
   constexpr int bytes = Layout<DK, DV>::kBytes;
   auto kern = gd_reverse_kernel<DK, DV, EFFECT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
+  GD_ALLOW_SMEM(kern, bytes);
   const Args x{a.dS, a.dS0, a.records, a.img_dS, a.img_dR, a.ends_seg, a.status, a.H, a.Hk, a.T, a.N, a.G,
                a.seg_chunks, d_k, d_v};
   ProfileScope prof(EFFECT ? "gd_tc_reverse_segment" : "gd_tc_reverse", a.stream);

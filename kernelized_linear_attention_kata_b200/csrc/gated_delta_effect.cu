@@ -161,8 +161,7 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 f = *reinterpret_cast<const float2 *>(from_start + 16 * h + 2 * i);
-            const float2 b = *reinterpret_cast<const float2 *>(beta + 16 * h + 2 * i);
+            const float2 f = gate2(from_start, 16 * h + 2 * i), b = gate2(beta, 16 * h + 2 * i);
             const float2 v2 = x == 0 ? make_float2(value(2 * i), value(2 * i + 1)) : make_float2(0.f, 0.f);
             z[i] = __fmul2_rn(b, __ffma2_rn(make_float2(-f.x, -f.y), as_float2(y[2 * i], y[2 * i + 1]), v2));
           }
@@ -186,7 +185,7 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 f = *reinterpret_cast<const float2 *>(to_end + 16 * h + 2 * i);
+            const float2 f = gate2(to_end, 16 * h + 2 * i);
             z[i] = __fmul2_rn(f, __fadd2_rn(as_float2(y[2 * i], y[2 * i + 1]), as_float2(w[2 * i], w[2 * i + 1])));
           }
           put16(col + kChain * x + kColD + 16 * h, z);
@@ -343,8 +342,7 @@ cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v) {
   const Args x{a.S0, a.F, a.starts_seg, a.records, a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks, d_k, d_v};
   constexpr int bytes = Layout<DK, DV>::kBytes;
   auto kern = gd_effect_kernel<DK, DV>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
+  GD_ALLOW_SMEM(kern, bytes);
   ProfileScope prof("gd_tc_segment", a.stream);
   kern<<<(unsigned)(a.BH * (a.G - 1)), kThreads, bytes, a.stream>>>(mk, mv, x);
   return cudaGetLastError();

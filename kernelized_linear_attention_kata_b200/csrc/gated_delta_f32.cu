@@ -5,10 +5,6 @@
 namespace kata {
 namespace gd {
 
-template <typename K> cudaError_t allow_smem(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 #define GD_TRY(expr)                          \
   do {                                        \
     cudaError_t e_ = (expr);                  \
@@ -18,11 +14,11 @@ template <typename K> cudaError_t allow_smem(K kern, size_t bytes) {
 template <int DK>
 cudaError_t solve(const GatedDeltaLaunch &a) {
   auto kern = gd_solve_kernel<DK>;
-  GD_TRY(allow_smem(kern, sizeof(SolveSmem<DK>)));
+  GD_ALLOW_SMEM(kern, sizeof(SolveSmem<DK>));
   ProfileScope prof("gd_f32_solve", a.stream);
   kern<<<(unsigned)(a.BH * a.N), kThreads, sizeof(SolveSmem<DK>), a.stream>>>(
-      static_cast<const float *>(a.q), static_cast<const float *>(a.k), a.g, a.beta, a.M, a.P, a.gates, a.H,
-      a.Hk, a.T, a.N);
+      static_cast<const float *>(a.q), static_cast<const float *>(a.k), a.g, a.beta, a.M, a.P, a.gates, a.status,
+      a.H, a.Hk, a.T, a.N);
   return cudaGetLastError();
 }
 
@@ -30,7 +26,7 @@ template <int DK, int CB>
 cudaError_t chain(const GatedDeltaLaunch &a, int d_v) {
   auto kern = gd_chain_kernel<DK, CB>;
   constexpr size_t smem = sizeof(ChainSmem<DK, CB>);
-  GD_TRY(allow_smem(kern, smem));
+  GD_ALLOW_SMEM(kern, smem);
   ProfileScope prof("gd_f32_chain", a.stream);
   kern<<<(unsigned)(a.BH * (d_v / CB)), kThreads, smem, a.stream>>>(
       static_cast<const float *>(a.q), static_cast<const float *>(a.k), static_cast<const float *>(a.v), a.gates,
@@ -43,7 +39,7 @@ template <int DK, int CB>
 cudaError_t reverse(const GatedDeltaLaunch &a, int d_v) {
   auto kern = gd_chain_reverse_kernel<DK, CB>;
   constexpr size_t smem = sizeof(ChainSmem<DK, CB>);
-  GD_TRY(allow_smem(kern, smem));
+  GD_ALLOW_SMEM(kern, smem);
   ProfileScope prof("gd_f32_chain_reverse", a.stream);
   kern<<<(unsigned)(a.BH * (d_v / CB)), kThreads, smem, a.stream>>>(
       static_cast<const float *>(a.q), static_cast<const float *>(a.k), static_cast<const float *>(a.dout),
@@ -55,7 +51,7 @@ template <int DK, int CB>
 cudaError_t grads(const GatedDeltaLaunch &a, int d_v) {
   auto kern = gd_grads_kernel<DK, CB>;
   constexpr size_t smem = sizeof(GradSmem<DK, CB>);
-  GD_TRY(allow_smem(kern, smem));
+  GD_ALLOW_SMEM(kern, smem);
   ProfileScope prof("gd_f32_grads", a.stream);
   kern<<<(unsigned)(a.BH * a.N), kThreads, smem, a.stream>>>(
       static_cast<const float *>(a.q), static_cast<const float *>(a.k), static_cast<const float *>(a.v),

@@ -230,7 +230,7 @@ template <int DK>
 __global__ void __launch_bounds__(kThreads)
 gd_solve_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ g,
                 const float *__restrict__ beta, float *__restrict__ M, float *__restrict__ P,
-                float *__restrict__ gates, int H, int Hk, int T, int N) {
+                float *__restrict__ gates, unsigned *__restrict__ status, int H, int Hk, int T, int N) {
   extern __shared__ __align__(16) float sm[];
   SolveSmem<DK> &s = *reinterpret_cast<SolveSmem<DK> *>(sm);
   constexpr int LD = DK + 4;
@@ -238,6 +238,7 @@ gd_solve_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
   const long long bh = blockIdx.x / N;
   const int n = blockIdx.x % N, t0 = n * kC, tid = threadIdx.x;
   const Where at(bh, H, Hk, T);
+  if (blockIdx.x == 0 && tid == 0) *status = 0;            // these kernels have no wait that could give up
   fetch_rows<DK, LD>(s.q, q + at.k * DK, t0, T, DK, 0);
   fetch_rows<DK, LD>(s.k, k + at.k * DK, t0, T, DK, 0);
   copies_done();

@@ -526,18 +526,13 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k,
       !make_tma_3d_bf16_box(&tdq, a.dq, d_k, a.T, BHk, 64, kC, true) ||
       !make_tma_3d_bf16_box(&tdk, a.dk, d_k, a.T, BHk, 64, kC, true))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   constexpr int bytes = Layout<DK, DV>::kBytes;
   auto kern = gd_grads_tc_kernel<DK, DV>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
+  GD_ALLOW_SMEM(kern, bytes);
   const Args x{a.g, a.beta, a.img_S, a.img_D, a.img_dS, a.img_dR, a.dg, a.dbeta, a.dq_part, a.dk_part,
                a.status, a.H, a.Hk, a.T, a.N, d_k, a.BH * a.N};
   ProfileScope prof("gd_tc_grads", a.stream);
-  kern<<<(unsigned)(x.jobs < sms ? x.jobs : sms), kThreads, bytes, a.stream>>>(tq, tk, tv, tdo, tdq, tdk, x);
+  kern<<<(unsigned)(x.jobs < kGdSms ? x.jobs : kGdSms), kThreads, bytes, a.stream>>>(tq, tk, tv, tdo, tdq, tdk, x);
   return cudaGetLastError();
 }
 

@@ -105,9 +105,7 @@ gd_join_kernel(const float *__restrict__ F, float *starts, float *ends, int G, i
 
 template <int DK> cudaError_t run(const GatedDeltaLaunch &a, int dv) {
   auto kern = gd_join_kernel<DK>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(JoinSmem<DK>));
-  if (e != cudaSuccess) return e;
+  GD_ALLOW_SMEM(kern, sizeof(JoinSmem<DK>));
   ProfileScope prof("gd_join", a.stream);
   kern<<<dim3((unsigned)(a.BH * (dv / kCols)), a.ends_seg ? 2 : 1), kThreads, sizeof(JoinSmem<DK>), a.stream>>>(
       a.F, a.starts_seg, a.ends_seg, a.G, dv);

@@ -154,8 +154,7 @@ template <int DK> cudaError_t launch(const GatedDeltaLaunch &a, int d_k) {
       !make_tma_3d_bf16_box(&tk, a.k, d_k, a.T, BHk, 64, kC, true))
     return cudaErrorInvalidValue;
   auto kern = gd_solve_tc_kernel<DK>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-  if (e != cudaSuccess) return e;
+  GD_ALLOW_SMEM(kern, L::kBytes);
   ProfileScope prof("gd_tc_solve", a.stream);
   kern<<<(unsigned)(a.BH * a.N), kSolveThreads, L::kBytes, a.stream>>>(tq, tk, a.g, a.beta, a.records,
                                                                        a.status, a.H, a.Hk, a.T, a.N);

@@ -218,15 +218,10 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_ld16(col_part + col_qs(c), y);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 f = gate4(from_start, 16 * h + i);
-          const float2 o0 = __ffma2_rn(make_float2(f.x, f.y), as_float2(y[i], y[i + 1]), as_float2(x[i], x[i + 1]));
-          const float2 o1 =
-              __ffma2_rn(make_float2(f.z, f.w), as_float2(y[i + 2], y[i + 3]), as_float2(x[i + 2], x[i + 3]));
-          dst[i * DV] = __float2bfloat16_rn(o0.x);
-          dst[(i + 1) * DV] = __float2bfloat16_rn(o0.y);
-          dst[(i + 2) * DV] = __float2bfloat16_rn(o1.x);
-          dst[(i + 3) * DV] = __float2bfloat16_rn(o1.y);
+        for (int i = 0; i < 16; i += 2) {
+          const float2 o = __ffma2_rn(gate2(from_start, 16 * h + i), as_float2(y[i], y[i + 1]), as_float2(x[i], x[i + 1]));
+          dst[i * DV] = __float2bfloat16_rn(o.x);
+          dst[(i + 1) * DV] = __float2bfloat16_rn(o.y);
         }
       }
       fence_async_smem();
@@ -269,14 +264,11 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_ld16(col_part + col_ks(c), x);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float4 f = gate4(from_start, 16 * h + 2 * i), b = gate4(beta, 16 * h + 2 * i);
-          y[i] = __ffma2_rn(make_float2(-f.x, -f.y), as_float2(x[2 * i], x[2 * i + 1]),
-                            as_float2(V[i] << 16, V[i] & 0xffff0000u));
-          y[i + 1] = __ffma2_rn(make_float2(-f.z, -f.w), as_float2(x[2 * i + 2], x[2 * i + 3]),
-                                as_float2(V[i + 1] << 16, V[i + 1] & 0xffff0000u));
-          y[i] = __fmul2_rn(make_float2(b.x, b.y), y[i]);
-          y[i + 1] = __fmul2_rn(make_float2(b.z, b.w), y[i + 1]);
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = gate2(from_start, 16 * h + 2 * i);
+          y[i] = __fmul2_rn(gate2(beta, 16 * h + 2 * i),
+                            __ffma2_rn(make_float2(-f.x, -f.y), as_float2(x[2 * i], x[2 * i + 1]),
+                                       as_float2(V[i] << 16, V[i] & 0xffff0000u)));
         }
         put16(col_part + col_ks(c), y);
         tmem_wait_st();
@@ -302,12 +294,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_ld16(col_part + kColS + 64, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float4 f = gate4(to_end, 16 * h + 2 * i);
+        for (int i = 0; i < 8; ++i) {
           d[i] = __fadd2_rn(as_float2(x[2 * i], x[2 * i + 1]), as_float2(y[2 * i], y[2 * i + 1]));
-          d[i + 1] = __fadd2_rn(as_float2(x[2 * i + 2], x[2 * i + 3]), as_float2(y[2 * i + 2], y[2 * i + 3]));
-          z[i] = __fmul2_rn(make_float2(f.x, f.y), d[i]);
-          z[i + 1] = __fmul2_rn(make_float2(f.z, f.w), d[i + 1]);
+          z[i] = __fmul2_rn(gate2(to_end, 16 * h + 2 * i), d[i]);
         }
         put16(col_part + kColD, z);
         tmem_wait_st();
@@ -518,8 +507,7 @@ cudaError_t run_chain(const char *name, const GatedDeltaLaunch &a, const CUtenso
                       long long blocks) {
   constexpr int bytes = Layout<DK, DV, MODE>::kBytes;
   auto kern = gd_tc_kernel<DK, DV, MODE>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
+  GD_ALLOW_SMEM(kern, bytes);
   ProfileScope prof(name, a.stream);
   kern<<<(unsigned)blocks, kThreads, bytes, a.stream>>>(maps[0], maps[1], maps[2], maps[3], x);
   return cudaGetLastError();

@@ -352,7 +352,7 @@ __device__ __forceinline__ void stage_row(uint8_t *image, int rows, int row, int
         lo_half ? make_uint4(l[0], l[1], l[2], l[3]) : make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
-__device__ __forceinline__ float4 gate4(const float *g, int i) { return *reinterpret_cast<const float4 *>(g + i); }
+__device__ __forceinline__ float2 gate2(const float *g, int i) { return *reinterpret_cast<const float2 *>(g + i); }
 
 // Saved images of a chunk for its gradients: a state (or its gradient) [d_v
 // rows][d_k] and the writes (or theirs) [d_v rows][64 tokens], hi, then lo.
