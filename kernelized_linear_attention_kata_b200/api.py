@@ -269,15 +269,15 @@ def _ptr(t, name, index, dtype):
     """Device pointer of a contiguous tensor on CUDA device `index` (None for None)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.get_device() == index >= 0 and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index or index < 0:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, q is not")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 # the device's current stream as a handle, without making a Stream of it
@@ -285,33 +285,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _On:
-    """The device of a call's tensors and the stream it runs on (the device's
-    current stream unless one is given). What is allocated inside belongs to
-    that stream, so the caching allocator does not hand it out again while the
-    call's kernels still use it. A token of decoding is a call of a few
-    microseconds: the guards are entered only where they change something."""
-
-    __slots__ = ("index", "given", "guards")
-
-    def __init__(self, index, stream):
-        if stream is not None and stream.device_index != index:
-            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
-        self.index, self.given, self.guards = index, stream, ()
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.index:
-            self.guards = (torch.cuda.device(self.index),)
-            self.guards[0].__enter__()
-        if self.given is None:
-            return _raw_stream(self.index)
-        self.guards += (torch.cuda.stream(self.given),)
-        self.guards[-1].__enter__()
-        return self.given.cuda_stream
-
-    def __exit__(self, *exc):
-        for guard in reversed(self.guards):
-            guard.__exit__(*exc)
+def _on(index, stream, call):
+    """call(stream handle) on the device of the tensors and the stream the call
+    runs on (the device's current stream unless one is given). What is allocated
+    inside belongs to that stream, so the caching allocator does not hand it out
+    again while the call's kernels still use it. A token of decoding is a call of
+    a few microseconds: the guards are entered only where they change something."""
+    if stream is None:
+        if torch.cuda.current_device() == index:
+            return call(_raw_stream(index))
+        with torch.cuda.device(index):
+            return call(_raw_stream(index))
+    if stream.device_index != index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -330,9 +318,34 @@ def _gated_workspace(workspace, bytes_fn, shape, q, index):
         if n == 0:
             raise ValueError("unsupported shape for the gated delta rule: B, H_k, H, T, d_k, d_v = "
                              f"{shape}")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(n, dtype=torch.uint8)
+        return workspace.data_ptr(), n, workspace
     return (_ptr(workspace, "workspace", index, workspace.dtype),
             workspace.numel() * workspace.element_size(), workspace)
+
+
+def _gated_inputs(q, k, v, g, beta, i):
+    dt, f32 = q.dtype, torch.float32
+    return (_ptr(q, "q", i, dt), _ptr(k, "k", i, dt), _ptr(v, "v", i, dt), _ptr(g, "g", i, f32),
+            _ptr(beta, "beta", i, f32))
+
+
+def _run_fwd(q, k, v, g, beta, shape, outputs, S0, workspace, stream):
+    """`outputs`: makes (o, S_out) once the inputs are checked."""
+    _like(S0, (shape[0], shape[2], shape[4], shape[5]), torch.float32, "S0")
+    code, i = _dtype(q), q.get_device()
+    ptrs = _gated_inputs(q, k, v, g, beta, i)
+    start = _ptr(S0, "S0", i, torch.float32)
+
+    def call(s):
+        o, S = outputs()
+        ws, n, held = _gated_workspace(workspace, fwd_gated_delta_workspace_bytes, shape, q, i)
+        st = lib().kata_fwd_gated_delta(*ptrs, _ptr(o, "o", i, q.dtype), *shape, code, start,
+                                        _ptr(S, "S_out", i, torch.float32), ws, n, s)
+        if st:
+            check("kata_fwd_gated_delta", st)
+        return o, S
+    return _on(i, stream, call)
 
 
 def kata_fwd_gated_delta(q, k, v, g, beta, o, S0=None, S_out=None, workspace=None, stream=None):
@@ -340,18 +353,33 @@ def kata_fwd_gated_delta(q, k, v, g, beta, o, S0=None, S_out=None, workspace=Non
     [B, H_k, T, d_k], v, o [B, H, T, d_v], g (log decays) and beta (write
     strengths) fp32 [B, H, T]; S0 / S_out optional fp32 [B, H, d_k, d_v]."""
     shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
-    dt, f32, code, i = q.dtype, torch.float32, _dtype(q), q.get_device()
-    _like(o, v.shape, dt, "o")
-    _like(S0, (B, H, d_k, d_v), f32, "S0")
-    _like(S_out, (B, H, d_k, d_v), f32, "S_out")
-    ptrs = (_ptr(q, "q", i, dt), _ptr(k, "k", i, dt), _ptr(v, "v", i, dt), _ptr(g, "g", i, f32),
-            _ptr(beta, "beta", i, f32), _ptr(o, "o", i, dt))
-    states = _ptr(S0, "S0", i, f32), _ptr(S_out, "S_out", i, f32)
-    with _On(i, stream) as s:
-        ws, n, workspace = _gated_workspace(workspace, fwd_gated_delta_workspace_bytes, shape, q, i)
-        st = lib().kata_fwd_gated_delta(*ptrs, *shape, code, *states, ws, n, s)
-    check("kata_fwd_gated_delta", st)
-    return o
+    _like(o, v.shape, q.dtype, "o")
+    _like(S_out, (B, H, d_k, d_v), torch.float32, "S_out")
+    return _run_fwd(q, k, v, g, beta, shape, lambda: (o, S_out), S0, workspace, stream)[0]
+
+
+def _run_bwd(q, k, v, g, beta, dout, shape, outputs, S0, dS, workspace, stream):
+    """`outputs`: makes (dq, dk, dv, dg, dbeta, dS0) once the inputs are checked."""
+    dt, f32 = q.dtype, torch.float32
+    state = (shape[0], shape[2], shape[4], shape[5])
+    _like(dout, v.shape, dt, "dout")
+    _like(S0, state, f32, "S0")
+    _like(dS, state, f32, "dS")
+    code, i = _dtype(q), q.get_device()
+    ptrs = _gated_inputs(q, k, v, g, beta, i) + (_ptr(dout, "dout", i, dt), _ptr(S0, "S0", i, f32),
+                                                 _ptr(dS, "dS", i, f32))
+
+    def call(s):
+        out = dq, dk, dv, dg, dbeta, dS0 = outputs()
+        ws, n, held = _gated_workspace(workspace, bwd_gated_delta_workspace_bytes, shape, q, i)
+        st = lib().kata_bwd_gated_delta(*ptrs, _ptr(dq, "dq", i, dt), _ptr(dk, "dk", i, dt),
+                                        _ptr(dv, "dv", i, dt), _ptr(dg, "dg", i, f32),
+                                        _ptr(dbeta, "dbeta", i, f32), _ptr(dS0, "dS0", i, f32),
+                                        *shape, code, ws, n, s)
+        if st:
+            check("kata_bwd_gated_delta", st)
+        return out
+    return _on(i, stream, call)
 
 
 def kata_bwd_gated_delta(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0=None, dS=None, dS0=None,
@@ -360,55 +388,46 @@ def kata_bwd_gated_delta(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0=None,
     given, dS0, from dout = dL/do and optionally dS = dL/dS_out (see
     include/kata.h)."""
     shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
-    dt, f32, code, i = q.dtype, torch.float32, _dtype(q), q.get_device()
-    for t, like, dtype, name in ((dout, v, dt, "dout"), (dq, q, dt, "dq"), (dk, k, dt, "dk"), (dv, v, dt, "dv"),
-                                 (dg, g, f32, "dg"), (dbeta, g, f32, "dbeta")):
+    dt, f32 = q.dtype, torch.float32
+    for t, like, dtype, name in ((dq, q, dt, "dq"), (dk, k, dt, "dk"), (dv, v, dt, "dv"), (dg, g, f32, "dg"),
+                                 (dbeta, g, f32, "dbeta")):
         _like(t, like.shape, dtype, name)
-    for t, name in ((S0, "S0"), (dS, "dS"), (dS0, "dS0")):
-        _like(t, (B, H, d_k, d_v), f32, name)
-    ptrs = (_ptr(q, "q", i, dt), _ptr(k, "k", i, dt), _ptr(v, "v", i, dt), _ptr(g, "g", i, f32),
-            _ptr(beta, "beta", i, f32), _ptr(dout, "dout", i, dt), _ptr(S0, "S0", i, f32),
-            _ptr(dS, "dS", i, f32), _ptr(dq, "dq", i, dt), _ptr(dk, "dk", i, dt), _ptr(dv, "dv", i, dt),
-            _ptr(dg, "dg", i, f32), _ptr(dbeta, "dbeta", i, f32), _ptr(dS0, "dS0", i, f32))
-    with _On(i, stream) as s:
-        ws, n, workspace = _gated_workspace(workspace, bwd_gated_delta_workspace_bytes, shape, q, i)
-        st = lib().kata_bwd_gated_delta(*ptrs, *shape, code, ws, n, s)
-    check("kata_bwd_gated_delta", st)
-    return dq, dk, dv, dg, dbeta, dS0
+    _like(dS0, (B, H, d_k, d_v), f32, "dS0")
+    return _run_bwd(q, k, v, g, beta, dout, shape, lambda: (dq, dk, dv, dg, dbeta, dS0), S0, dS, workspace,
+                    stream)
 
 
 def kata_gated_delta_step(q, k, v, g, beta, S, y, stream=None):
     """In-place one-token step of the gated delta rule: q, k [B, H_k, d_k],
     v, y [B, H, d_v], g, beta fp32 [B, H]; S fp32 [B, H, d_k, d_v] updated."""
     B, H_k, H, d_k, d_v = _gated_shapes(q, k, v, g, beta, False)
-    dt, f32, code, i = q.dtype, torch.float32, _dtype(q), q.get_device()
+    dt, code, i = q.dtype, _dtype(q), q.get_device()
     _like(y, v.shape, dt, "y")
-    _like(S, (B, H, d_k, d_v), f32, "S")
-    ptrs = (_ptr(q, "q", i, dt), _ptr(k, "k", i, dt), _ptr(v, "v", i, dt), _ptr(g, "g", i, f32),
-            _ptr(beta, "beta", i, f32), _ptr(S, "S", i, f32), _ptr(y, "y", i, dt))
-    with _On(i, stream) as s:
-        st = lib().kata_gated_delta_step(*ptrs, B, H_k, H, d_k, d_v, code, s)
-    check("kata_gated_delta_step", st)
+    _like(S, (B, H, d_k, d_v), torch.float32, "S")
+    ptrs = _gated_inputs(q, k, v, g, beta, i) + (_ptr(S, "S", i, torch.float32), _ptr(y, "y", i, dt))
+    st = _on(i, stream, lambda s: lib().kata_gated_delta_step(*ptrs, B, H_k, H, d_k, d_v, code, s))
+    if st:
+        check("kata_gated_delta_step", st)
     return y
 
 
 def fwd_gated_delta(q, k, v, g, beta, S0=None, return_state=False):
     """(o) or (o, S) of the gated delta rule, allocated with torch."""
-    o = torch.empty_like(v)
-    S = None
-    if return_state:
-        S = torch.empty((q.shape[0], v.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
-                        device=q.device)
-    kata_fwd_gated_delta(q, k, v, g, beta, o, S0=S0, S_out=S)
+    shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
+
+    def outputs():
+        return torch.empty_like(v), v.new_empty((B, H, d_k, d_v), dtype=torch.float32) if return_state else None
+    o, S = _run_fwd(q, k, v, g, beta, shape, outputs, S0, None, None)
     return (o, S) if return_state else o
 
 
 def bwd_gated_delta(q, k, v, g, beta, dout, S0=None, dS=None):
     """(dq, dk, dv, dg, dbeta, dS0) of sum(dout * o) + sum(dS * S) for
     (o, S) = fwd_gated_delta(...); dS0 is None unless S0 is given."""
-    return kata_bwd_gated_delta(q, k, v, g, beta, dout, torch.empty_like(q), torch.empty_like(k),
-                                torch.empty_like(v), torch.empty_like(g), torch.empty_like(beta),
-                                S0=S0, dS=dS, dS0=None if S0 is None else torch.empty_like(S0))
+    new = torch.empty_like
+    return _run_bwd(q, k, v, g, beta, dout, _gated_shapes(q, k, v, g, beta, True),
+                    lambda: (new(q), new(k), new(v), new(g), new(beta), None if S0 is None else new(S0)),
+                    S0, dS, None, None)
 
 
 def gated_delta_step(q, k, v, g, beta, S):
