@@ -66,7 +66,7 @@ constexpr int gd_padded(int d) { return d <= 64 ? 64 : 128; }
 #define GD_TC_DISPATCH(FN)                                                    \
   (gd_padded(d_k) == 64 ? (gd_padded(d_v) == 64 ? FN(64, 64) : FN(64, 128)) \
                         : (gd_padded(d_v) == 64 ? FN(128, 64) : FN(128, 128)))
-void gd_tc_split(long long BH, int N, bool gradient, int *G, int *seg_chunks);
+void gd_tc_split(long long BH, int N, int d_k, int d_v, bool gradient, int *G, int *seg_chunks);
 size_t gd_tc_record_bytes();
 cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k);
 // Tensor-core gradient: the saved images of states and writes.

@@ -58,7 +58,7 @@ bool aligned16(std::initializer_list<const void *> ps) {
 
 // The tensor-core forward's regions (the gradient's first pass needs them too).
 void place_chain(GatedDeltaLaunch &a, int d_k, int d_v, bool gradient, Regions &r) {
-  if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, gradient, &a.G, &a.seg_chunks);
+  if (a.BH > 0 && a.T > 0) gd_tc_split(a.BH, a.N, d_k, d_v, gradient, &a.G, &a.seg_chunks);
   a.records = r.take_bytes((size_t)a.BH * a.N * gd_tc_record_bytes());
   if (a.G > 1) {
     const size_t dk = gd_padded(d_k), dv = gd_padded(d_v);

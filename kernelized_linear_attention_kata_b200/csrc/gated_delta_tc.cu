@@ -530,21 +530,22 @@ cudaError_t launch(const char *name, const GatedDeltaLaunch &a, int d_k, int d_v
 
 }  // namespace
 
-// Segments a head, by the time they should take in chunks of the output pass
-// (3.4 us): a wave runs one block an SM; an effect chunk costs 0.75; the gradient's
-// save, reverse and reverse effect chunks 1.2, 1.5 and 1; a join step 0.8, and a
-// further launch 2.
-void gd_tc_split(long long BH, int N, bool gradient, int *G, int *seg_chunks) {
+// Segments a head, by the time they should take. Microseconds a chunk of each
+// pass as measured for d_k <= 64 and above, one block an SM; every further launch
+// costs 7, a join step 4.
+void gd_tc_split(long long BH, int N, int d_k, int d_v, bool gradient, int *G, int *seg_chunks) {
+  struct Cost { double out, effect, save, reverse, reverse_effect; };
+  const Cost us = gd_padded(d_k) == 64 ? Cost{2.8, 3.2, 2.9, 4.1, 2.8} : Cost{3.3, 4.2, 4.2, 5.4, 3.3};
   int best = 1;
   double least = 1e300;
   auto waves = [](long long blocks) { return (double)((blocks + kGdSms - 1) / kGdSms); };
   for (int g = 1; g <= 64 && (g == 1 || (long long)g * BH <= kGdSms); ++g) {
     const int per = (N + g - 1) / g, used = per > 0 ? (N + per - 1) / per : 1;
     if (used != g) continue;
-    double time = (gradient ? 1.2 + 1.5 : 1.0) * waves(BH * g) * per;
+    double time = (gradient ? us.save + us.reverse : us.out) * waves(BH * g) * per;
     if (g > 1)
-      time += (0.75 + (gradient ? 1.0 : 0.0)) * waves(BH * (g - 1)) * per +
-              (g > 2 ? 2.0 + 0.8 * (g - 2) : 0.0) + (gradient ? 4.0 : 2.0);
+      time += (us.effect + (gradient ? us.reverse_effect : 0.0)) * waves(BH * (g - 1)) * per + (gradient ? 14.0 : 7.0);
+    if (g > 2) time += 7.0 + 4.0 * (g - 2) * waves(BH * (gd_padded(d_v) / 16) * (gradient ? 2 : 1));
     if (time < least) {
       least = time;
       best = g;
