@@ -17,6 +17,14 @@ constexpr int kLs = kC + 4;          // row stride of the solve's fp32 matrix
 constexpr float kMinLogDecay = -100.f;
 constexpr int kSpins = 64;           // tests of a barrier before a thread suspends
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
 // An fp32 pair as two bf16 pairs, x = hi + lo up to 2^-17 of its binade. The
 // tensor core multiplies bf16: an fp32 operand enters as hi + lo (q, k, v and
 // dout are bf16 already and enter as they are), so that a product keeps 16
