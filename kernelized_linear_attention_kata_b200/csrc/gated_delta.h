@@ -76,6 +76,7 @@ cudaError_t gd_tc_reverse_effect(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_reverse(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_join(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v);
+cudaError_t gd_tc_grads_wide(const GatedDeltaLaunch &a, int d_k, int d_v);   // 64 < d_k
 cudaError_t gd_tc_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
 // dq, dk of shared heads: the sums of the value heads' parts.
 cudaError_t gd_sum_groups(const GatedDeltaLaunch &a, int d_k, bool bf16);

@@ -1,6 +1,7 @@
 // The gradient of the gated delta rule, second kernel: dq, dk, dg and dbeta of
-// every chunk from what the chains saved at its borders (bf16; padded head sizes). With X = dR S^T, Y = dO S^T, Z = D dS'^T (64 x d_k), W_ts =
-// e^{G_t - G_s} and dP = dO D^T, dL = -dR D^T:
+// every chunk from what the chains saved at its borders (bf16; this kernel for
+// d_k <= 64, padded to 64, gated_delta_grads_tc.cu above). With X = dR S^T, Y = dO
+// S^T, Z = D dS'^T (64 x d_k), W_ts = e^{G_t - G_s} and dP = dO D^T, dL = -dR D^T:
 //   dq = e^G Y + (dP W) K,
 //   dk = -beta e^G X + e^{G_C - G} Z + (dP W)^T Q + (A + A^T) K,  A = dL beta W,
 //   dbeta_t = dR_t . v_t - e^{G_t} k_t . X_t + sum_s dL_ts W_ts k_t . k_s,
@@ -8,14 +9,14 @@
 //   dg_t = sum_{u >= t} dG_u + sum_s z_s + e^{G_C} <S, dS'>,
 // z_t = e^{G_C - G_t} k_t . Z_t, pairs = dP P + dL L.
 //
-// The chunks are independent: no chain, so blocks of eight warps walk them and
-// what bounds the kernel is the saved images (272 KB a chunk at d_k = d_v = 128:
-// 11K cycles of one SM's share of HBM) beside the products (25 MFLOP a chunk
-// with the operand halves). These run on the warp tensor instructions, whose
-// accumulators stay in registers through the row sums and scalings between
-// the products; in tensor memory each of the seven accumulators would be read
-// back and its operands written out between them. fp32 operands are bf16
-// halves; a product takes hi hi, hi lo and lo hi.
+// The chunks are independent: no chain, so blocks of eight warps walk them, bound
+// by the products: 5 MFLOP a chunk at d_v = 64 with the operand halves, 14K
+// cycles. These run on the warp tensor instructions, whose accumulators stay in
+// registers through the row sums and scalings between the products; in tensor
+// memory each of the seven accumulators would be read back and its operands
+// written out between them, which at this size takes longer (140 us instead of
+// 107 at 32 heads of 4096 tokens). fp32 operands are bf16 halves; a product takes
+// hi hi, hi lo and lo hi.
 //
 // Warp (rt, ch): rows 16 rt .. 16 rt + 15 of every 64-row result, half ch of
 // its columns. Values come in panels of 64: the tiles of dO, v, dR and D (two
@@ -539,9 +540,8 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k,
 }  // namespace
 
 cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v) {
-#define GD_RUN(DK, DV) launch<DK, DV>(a, d_k, d_v)
-  return GD_TC_DISPATCH(GD_RUN);
-#undef GD_RUN
+  if (gd_padded(d_k) == 128) return gd_tc_grads_wide(a, d_k, d_v);
+  return gd_padded(d_v) == 64 ? launch<64, 64>(a, d_k, d_v) : launch<64, 128>(a, d_k, d_v);
 }
 
 cudaError_t gd_tc_backward(const GatedDeltaLaunch &a, int d_k, int d_v) {
