@@ -7,7 +7,9 @@ contraction, so partial sums stay within a few times the result's largest
 entry. fp32: a value passes through at most n = d_k + d_v + 4 * 64 additions
 (a product with the state, the solve, a product with the writes, the update;
 for a gradient also the value axis), each off by at most half a step 2^-24 of
-a partial sum, taken as 4 times the largest entry: 4 n 2^-24 <= 1.3e-4. bf16:
+a partial sum, taken as 4 times the largest entry: 4 n 2^-24 <= 1.3e-4.
+Products of fp32 are made of three TF32 parts and off by at most 2^-22, four
+half steps of one of the n terms; the bound's 4 covers them as well. bf16:
 the tensor-core kernels take fp32 operands as two bf16 halves, off by at most
 2^-16 of the operand; a value meets at most 8 such operands in a row, 8 * 2^-16
 = 1.3e-4 on top. An output held in bf16 is rounded once more, half a step,
@@ -144,6 +146,49 @@ def test_one_long_head(dtype, d_k, d_v):
     close(S, ref_S, d_k, d_v, dtype == "bf16", "S")
     for name, x, r in zip(GRADS, backward(d), oracle_backward(t)):
         close(x, r, d_k, d_v, dtype == "bf16", name)
+
+
+@pytest.mark.parametrize("d_k, d_v", [(16, 128), (32, 16), (64, 64), (64, 128), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("B, Hk, H, T", [(1, 1, 3, 1000), (2, 1, 2, 129), (1, 4, 60, 540)])
+def test_sequences_in_segments(d_k, d_v, B, Hk, H, T):
+    """Few enough heads for the sequence to be cut: states and their gradients
+    pass over the borders of segments, the last of which is short, with shared
+    keys and padded head sizes; the first and the last head of the last batch."""
+    t = make(B, Hk, H, T, d_k, d_v, "bf16", seed=T + d_k + d_v)
+    t["g"] *= 0.05                                  # the carry matters over many chunks
+    d = on_gpu(t)
+    o, S = forward(d)
+    got = dict(zip(GRADS, backward(d)))
+    for h in (0, H - 1):
+        k = h // (H // Hk)
+        pick = {n: x[B - 1:, k:k + 1] if n in ("q", "k") else x[B - 1:, h:h + 1] for n, x in t.items()}
+        ref_o, ref_S = oracle_forward(pick)
+        close(o[B - 1:, h:h + 1], ref_o, d_k, d_v, True, "o")
+        close(S[B - 1:, h:h + 1], ref_S, d_k, d_v, True, "S")
+        ref = dict(zip(GRADS, oracle_backward(pick)))
+        for name in ("dv", "dg", "dbeta", "dS0"):
+            close(got[name][B - 1:, h:h + 1], ref[name], d_k, d_v, True, name)
+    if H // Hk <= 3:                                # the sums over a shared head's value heads
+        last = {n: x[B - 1:] for n, x in t.items()}
+        for name, r in zip(GRADS[:2], oracle_backward(last)):
+            close(got[name][B - 1:], r, d_k, d_v, True, name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d_k, d_v", [(128, 128), (64, 32)])
+def test_more_heads_than_run_at_once(dtype, d_k, d_v):
+    """200 heads: blocks take chunks of several heads one after another."""
+    t = make(40, 5, 5, 130, d_k, d_v, dtype, seed=17)
+    d = on_gpu(t)
+    o, S = forward(d)
+    got = backward(d)
+    for b, h in ((0, 0), (29, 3), (39, 4)):
+        pick = {n: x[b:b + 1, h:h + 1] for n, x in t.items()}
+        ref_o, ref_S = oracle_forward(pick)
+        close(o[b:b + 1, h:h + 1], ref_o, d_k, d_v, dtype == "bf16", "o")
+        close(S[b:b + 1, h:h + 1], ref_S, d_k, d_v, dtype == "bf16", "S")
+        for name, x, r in zip(GRADS, got, oracle_backward(pick)):
+            close(x[b:b + 1, h:h + 1], r, d_k, d_v, dtype == "bf16", name)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -304,6 +349,34 @@ def test_own_stream_and_captured_graph(dtype):
     torch.cuda.synchronize()
     for x, y in zip(out, eager):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_captured_training_steps(dtype):
+    """Two graphs of forward and gradient, replayed by turns and at once on two
+    streams: their workspaces are their own."""
+    sets = [on_gpu(make(1, 1, 2, 700, 64, 128, dtype, seed=s)) for s in (31, 32)]
+    want = [forward(d) + backward(d) for d in sets]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for d in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(forward(d) + backward(d))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for out in outs:
+            for x in out:
+                x.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(outs, want):
+            for x, y in zip(got, ref):
+                assert torch.equal(x, y)
 
 
 def test_captured_step():
