@@ -117,3 +117,23 @@ def lib() -> ctypes.CDLL:
 def check(fn: str, status: int) -> None:
     if status != KATA_OK:
         raise KataError(fn, status)
+
+
+_binding = None
+_BOUND = ("kata_fwd_gated_delta_workspace_bytes", "kata_fwd_gated_delta",
+          "kata_bwd_gated_delta_workspace_bytes", "kata_bwd_gated_delta", "kata_gated_delta_step")
+
+
+def binding():
+    """The compiled binding of the gated delta rule, bound to the loaded library."""
+    global _binding
+    if _binding is None:
+        handle = lib()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("KATA binding not built: run "
+                              "`python -m kernelized_linear_attention_kata_b200.build`.") from e
+        module.bind(*(ctypes.cast(getattr(handle, n), ctypes.c_void_p).value for n in _BOUND))
+        _binding = module
+    return _binding

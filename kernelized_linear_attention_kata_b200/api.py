@@ -10,13 +10,12 @@ only provides device memory and streams.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 import torch
 
 from . import _lib
 from ._lib import (KATA_DTYPE_BF16, KATA_DTYPE_F32, KATA_FEATURE_FIRST_ORDER, KATA_FEATURE_PSD,
-                   check, lib)
+                   binding, check, lib)
 
 _DTYPES = {torch.float32: KATA_DTYPE_F32, torch.bfloat16: KATA_DTYPE_BF16}
 _FEATURES = {"psd": KATA_FEATURE_PSD, "first_order": KATA_FEATURE_FIRST_ORDER,
@@ -240,146 +239,35 @@ def fwd_delta(q, k, v, beta, feature="psd", return_state=False, S0=None):
     return (o, S) if return_state else o
 
 
-def _gated_shapes(q, k, v, g, beta, token_axis):
-    """(B, H_k, H, T, d_k, d_v) of a gated delta rule's inputs, checked; the
-    one-token step's have no token axis and no T."""
-    qs, vs, dt = q.shape, v.shape, q.dtype
-    n = 4 if token_axis else 3
-    if len(qs) != n or k.shape != qs or len(vs) != n or vs[0] != qs[0] or (token_axis and vs[2] != qs[2]):
-        tok = ", T" if token_axis else ""
-        raise ValueError(f"expected q, k [B, H_k{tok}, d_k] and v [B, H{tok}, d_v]; got "
-                         f"{tuple(qs)}, {tuple(k.shape)}, {tuple(vs)}")
-    if k.dtype != dt or v.dtype != dt:
-        raise TypeError("q, k, v must share one dtype")
-    H_k, H = qs[1], vs[1]
-    if H and (H_k == 0 or H % H_k):
-        raise ValueError(f"the {H} value heads must be a multiple of the {H_k} key heads")
-    tokens = vs[:-1]
-    if g.shape != tokens or beta.shape != tokens:
-        raise ValueError(f"g and beta must be {list(tokens)} fp32, got {list(g.shape)} and {list(beta.shape)}")
-    return (qs[0], H_k, H, qs[2], qs[3], vs[3]) if token_axis else (qs[0], H_k, H, qs[2], vs[2])
-
-
-def _like(t, shape, dtype, name):
-    if t is not None and (t.shape != shape or t.dtype != dtype):
-        raise ValueError(f"{name} must be {list(shape)} {dtype}, got {list(t.shape)} {t.dtype}")
-
-
-def _ptr(t, name, index, dtype):
-    """Device pointer of a contiguous tensor on CUDA device `index` (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.get_device() == index >= 0 and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, q is not")
-    raise ValueError(f"{name} must be contiguous")
-
-
-# the device's current stream as a handle, without making a Stream of it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _on(index, stream, call):
-    """call(stream handle) on the device of the tensors and the stream the call
-    runs on (the device's current stream unless one is given). What is allocated
-    inside belongs to that stream, so the caching allocator does not hand it out
-    again while the call's kernels still use it. A token of decoding is a call of
-    a few microseconds: the guards are entered only where they change something."""
-    if stream is None:
-        if torch.cuda.current_device() == index:
-            return call(_raw_stream(index))
-        with torch.cuda.device(index):
-            return call(_raw_stream(index))
-    if stream.device_index != index:
-        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
-
-
-@functools.lru_cache(maxsize=1024)
 def fwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, dtype=torch.bfloat16) -> int:
     return int(lib().kata_fwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, _DTYPES[dtype]))
 
 
-@functools.lru_cache(maxsize=1024)
 def bwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, dtype=torch.bfloat16) -> int:
     return int(lib().kata_bwd_gated_delta_workspace_bytes(B, H_k, H, T, d_k, d_v, _DTYPES[dtype]))
 
 
-def _gated_workspace(workspace, bytes_fn, shape, q, index):
-    if workspace is None:
-        n = bytes_fn(*shape, q.dtype)
-        if n == 0:
-            raise ValueError("unsupported shape for the gated delta rule: B, H_k, H, T, d_k, d_v = "
-                             f"{shape}")
-        workspace = q.new_empty(n, dtype=torch.uint8)
-        return workspace.data_ptr(), n, workspace
-    return (_ptr(workspace, "workspace", index, workspace.dtype),
-            workspace.numel() * workspace.element_size(), workspace)
-
-
-def _gated_inputs(q, k, v, g, beta, i):
-    dt, f32 = q.dtype, torch.float32
-    return (_ptr(q, "q", i, dt), _ptr(k, "k", i, dt), _ptr(v, "v", i, dt), _ptr(g, "g", i, f32),
-            _ptr(beta, "beta", i, f32))
-
-
-def _run_fwd(q, k, v, g, beta, shape, outputs, S0, workspace, stream):
-    """`outputs`: makes (o, S_out) once the inputs are checked."""
-    _like(S0, (shape[0], shape[2], shape[4], shape[5]), torch.float32, "S0")
-    code, i = _dtype(q), q.get_device()
-    ptrs = _gated_inputs(q, k, v, g, beta, i)
-    start = _ptr(S0, "S0", i, torch.float32)
-
-    def call(s):
-        o, S = outputs()
-        ws, n, held = _gated_workspace(workspace, fwd_gated_delta_workspace_bytes, shape, q, i)
-        st = lib().kata_fwd_gated_delta(*ptrs, _ptr(o, "o", i, q.dtype), *shape, code, start,
-                                        _ptr(S, "S_out", i, torch.float32), ws, n, s)
-        if st:
-            check("kata_fwd_gated_delta", st)
-        return o, S
-    return _on(i, stream, call)
+def _on(stream, q, call, *args):
+    """call(*args) of the compiled binding, which checks the arguments and runs on
+    the current stream of the tensors' device; `stream` makes it the given one.
+    What is allocated inside belongs to that stream, so the caching allocator
+    does not hand it out again while the call's kernels still use it."""
+    if stream is None:
+        return call(*args)
+    if stream.device_index != q.get_device():
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {q.device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def kata_fwd_gated_delta(q, k, v, g, beta, o, S0=None, S_out=None, workspace=None, stream=None):
     """Gated delta rule forward into `o` (see include/kata.h): q, k
     [B, H_k, T, d_k], v, o [B, H, T, d_v], g (log decays) and beta (write
     strengths) fp32 [B, H, T]; S0 / S_out optional fp32 [B, H, d_k, d_v]."""
-    shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
-    _like(o, v.shape, q.dtype, "o")
-    _like(S_out, (B, H, d_k, d_v), torch.float32, "S_out")
-    return _run_fwd(q, k, v, g, beta, shape, lambda: (o, S_out), S0, workspace, stream)[0]
-
-
-def _run_bwd(q, k, v, g, beta, dout, shape, outputs, S0, dS, workspace, stream):
-    """`outputs`: makes (dq, dk, dv, dg, dbeta, dS0) once the inputs are checked."""
-    dt, f32 = q.dtype, torch.float32
-    state = (shape[0], shape[2], shape[4], shape[5])
-    _like(dout, v.shape, dt, "dout")
-    _like(S0, state, f32, "S0")
-    _like(dS, state, f32, "dS")
-    code, i = _dtype(q), q.get_device()
-    ptrs = _gated_inputs(q, k, v, g, beta, i) + (_ptr(dout, "dout", i, dt), _ptr(S0, "S0", i, f32),
-                                                 _ptr(dS, "dS", i, f32))
-
-    def call(s):
-        out = dq, dk, dv, dg, dbeta, dS0 = outputs()
-        ws, n, held = _gated_workspace(workspace, bwd_gated_delta_workspace_bytes, shape, q, i)
-        st = lib().kata_bwd_gated_delta(*ptrs, _ptr(dq, "dq", i, dt), _ptr(dk, "dk", i, dt),
-                                        _ptr(dv, "dv", i, dt), _ptr(dg, "dg", i, f32),
-                                        _ptr(dbeta, "dbeta", i, f32), _ptr(dS0, "dS0", i, f32),
-                                        *shape, code, ws, n, s)
-        if st:
-            check("kata_bwd_gated_delta", st)
-        return out
-    return _on(i, stream, call)
+    st = _on(stream, q, binding().fwd, q, k, v, g, beta, S0, False, o, S_out, workspace)[0]
+    if st:
+        check("kata_fwd_gated_delta", st)
+    return o
 
 
 def kata_bwd_gated_delta(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0=None, dS=None, dS0=None,
@@ -387,25 +275,19 @@ def kata_bwd_gated_delta(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0=None,
     """Gradient of kata_fwd_gated_delta into dq, dk, dv, dg, dbeta and, if
     given, dS0, from dout = dL/do and optionally dS = dL/dS_out (see
     include/kata.h)."""
-    shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
-    dt, f32 = q.dtype, torch.float32
-    for t, like, dtype, name in ((dq, q, dt, "dq"), (dk, k, dt, "dk"), (dv, v, dt, "dv"), (dg, g, f32, "dg"),
-                                 (dbeta, g, f32, "dbeta")):
-        _like(t, like.shape, dtype, name)
-    _like(dS0, (B, H, d_k, d_v), f32, "dS0")
-    return _run_bwd(q, k, v, g, beta, dout, shape, lambda: (dq, dk, dv, dg, dbeta, dS0), S0, dS, workspace,
-                    stream)
+    if dq is None:
+        raise TypeError("dq must be a tensor")
+    st = _on(stream, q, binding().bwd, q, k, v, g, beta, dout, S0, dS, dq, dk, dv, dg, dbeta, dS0,
+             workspace)[0]
+    if st:
+        check("kata_bwd_gated_delta", st)
+    return dq, dk, dv, dg, dbeta, dS0
 
 
 def kata_gated_delta_step(q, k, v, g, beta, S, y, stream=None):
     """In-place one-token step of the gated delta rule: q, k [B, H_k, d_k],
     v, y [B, H, d_v], g, beta fp32 [B, H]; S fp32 [B, H, d_k, d_v] updated."""
-    B, H_k, H, d_k, d_v = _gated_shapes(q, k, v, g, beta, False)
-    dt, code, i = q.dtype, _dtype(q), q.get_device()
-    _like(y, v.shape, dt, "y")
-    _like(S, (B, H, d_k, d_v), torch.float32, "S")
-    ptrs = _gated_inputs(q, k, v, g, beta, i) + (_ptr(S, "S", i, torch.float32), _ptr(y, "y", i, dt))
-    st = _on(i, stream, lambda s: lib().kata_gated_delta_step(*ptrs, B, H_k, H, d_k, d_v, code, s))
+    st, y = _on(stream, q, binding().step, q, k, v, g, beta, S, y)
     if st:
         check("kata_gated_delta_step", st)
     return y
@@ -413,26 +295,24 @@ def kata_gated_delta_step(q, k, v, g, beta, S, y, stream=None):
 
 def fwd_gated_delta(q, k, v, g, beta, S0=None, return_state=False):
     """(o) or (o, S) of the gated delta rule, allocated with torch."""
-    shape = B, H_k, H, T, d_k, d_v = _gated_shapes(q, k, v, g, beta, True)
-
-    def outputs():
-        return torch.empty_like(v), v.new_empty((B, H, d_k, d_v), dtype=torch.float32) if return_state else None
-    o, S = _run_fwd(q, k, v, g, beta, shape, outputs, S0, None, None)
+    st, o, S = binding().fwd(q, k, v, g, beta, S0, bool(return_state), None, None, None)
+    if st:
+        check("kata_fwd_gated_delta", st)
     return (o, S) if return_state else o
 
 
 def bwd_gated_delta(q, k, v, g, beta, dout, S0=None, dS=None):
     """(dq, dk, dv, dg, dbeta, dS0) of sum(dout * o) + sum(dS * S) for
     (o, S) = fwd_gated_delta(...); dS0 is None unless S0 is given."""
-    new = torch.empty_like
-    return _run_bwd(q, k, v, g, beta, dout, _gated_shapes(q, k, v, g, beta, True),
-                    lambda: (new(q), new(k), new(v), new(g), new(beta), None if S0 is None else new(S0)),
-                    S0, dS, None, None)
+    got = binding().bwd(q, k, v, g, beta, dout, S0, dS, None, None, None, None, None, None, None)
+    if got[0]:
+        check("kata_bwd_gated_delta", got[0])
+    return got[1:]
 
 
 def gated_delta_step(q, k, v, g, beta, S):
     """y of the one-token step, allocated with torch; S is updated in place."""
-    return kata_gated_delta_step(q, k, v, g, beta, S, torch.empty_like(v))
+    return kata_gated_delta_step(q, k, v, g, beta, S, None)
 
 
 def kata_workspace_status(workspace, stream=None) -> int:

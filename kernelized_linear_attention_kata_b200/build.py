@@ -3,7 +3,8 @@
     python -m kernelized_linear_attention_kata_b200.build [--force] [--verbose]
 
 The library is a plain C-ABI shared object (see include/kata.h); nothing in
-it depends on PyTorch. The CUDA runtime is linked statically, the driver API
+it depends on PyTorch. Beside it, _binding.so marshals the gated delta rule's
+calls for Python (csrc/binding.cpp, built against the installed torch). The CUDA runtime is linked statically, the driver API
 (needed for TMA descriptors) is resolved at run time through the runtime's
 driver entry-point query, so the .so runs on any machine with the driver.
 """
@@ -16,12 +17,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libkata.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
@@ -51,7 +55,34 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    deps = [BINDING_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and os.path.exists(BINDING_PATH) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(BINDING_PATH) for p in deps):
+        return BINDING_PATH
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    includes = [INCLUDE, os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BINDING_PATH + ".tmp"
+    # the system's g++, as nvcc uses it: the C++ runtime has to be the one torch uses
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in includes), BINDING_SRC, "-o", tmp, f"-L{os.path.join(root, 'lib')}",
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    done = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if done.returncode != 0:
+        raise RuntimeError(f"binding failed to build:\n{done.stdout.decode(errors='replace')}")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    build_binding(force, verbose)
     if not force and up_to_date():
         return LIB_PATH
     nvcc = nvcc_path()
