@@ -541,7 +541,8 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k,
 
 cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v) {
   if (gd_padded(d_k) == 128) return gd_tc_grads_wide(a, d_k, d_v);
-  return gd_padded(d_v) == 64 ? launch<64, 64>(a, d_k, d_v) : launch<64, 128>(a, d_k, d_v);
+  const cudaError_t e = gd_padded(d_v) == 64 ? launch<64, 64>(a, d_k, d_v) : launch<64, 128>(a, d_k, d_v);
+  return e == cudaSuccess && a.dq_part ? gd_sum_groups(a, d_k, true) : e;
 }
 
 cudaError_t gd_tc_backward(const GatedDeltaLaunch &a, int d_k, int d_v) {
@@ -551,9 +552,7 @@ cudaError_t gd_tc_backward(const GatedDeltaLaunch &a, int d_k, int d_v) {
   if (e == cudaSuccess) e = gd_tc_join(a, d_k, d_v);
   if (e == cudaSuccess) e = gd_tc_save(a, d_k, d_v);
   if (e == cudaSuccess) e = gd_tc_reverse(a, d_k, d_v);
-  if (e == cudaSuccess) e = gd_tc_grads(a, d_k, d_v);
-  if (e == cudaSuccess && a.dq_part) e = gd_sum_groups(a, d_k, true);
-  return e;
+  return e == cudaSuccess ? gd_tc_grads(a, d_k, d_v) : e;
 }
 
 }  // namespace kata

@@ -102,7 +102,8 @@ struct Args {
   unsigned *status;
   int H, Hk, T, N;
   int dk;                          // the tensors' d_k, <= DK
-  long long jobs;
+  int fold;                        // value heads a block takes one after another, adding up dq and dk
+  long long units;                 // chunks, of query / key heads if fold > 1
 };
 
 template <int DK, int DV>
@@ -122,8 +123,12 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   Gates *gates = reinterpret_cast<Gates *>(smem + L::kOffGates);
   RowSums &rows = *reinterpret_cast<RowSums *>(smem + L::kOffRows);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int jobs = (int)((a.jobs - blockIdx.x + gridDim.x - 1) / gridDim.x);       // of this block
-  auto job_of = [&](int j) { return (long long)blockIdx.x + (long long)j * gridDim.x; };
+  const int jobs = (int)((a.units - blockIdx.x + gridDim.x - 1) / gridDim.x) * a.fold;   // of this block
+  // value head and chunk of the block's j-th job, as head * N + chunk
+  auto job_of = [&](int j) {
+    const long long unit = (long long)blockIdx.x + (long long)(j / a.fold) * gridDim.x;
+    return (unit / a.N * a.fold + j % a.fold) * a.N + unit % a.N;
+  };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
@@ -349,17 +354,30 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       tmem_wait_ld();
       tc_fence_before();
       warp_arrive(&bars[kRead]);
-      if (a.dq_part) {
-        if (r < a.dk) {
+      const int nth = j % a.fold;                          // of the heads that are added up
+      const bool last = nth == a.fold - 1;
+      if (a.dq_part && r < a.dk) {
+        // parts: a value head's, or the sum so far of a query / key head's (which
+        // this thread has written)
+        const size_t row = ((size_t)(bh / a.fold) * a.T + t0 + 16 * h) * a.dk + r;
+        if (nth > 0) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (16 * h + i < left) {
-              const size_t at = (tok + 16 * h + i) * a.dk + r;
-              a.dq_part[at] = __uint_as_float(y[i]);
-              a.dk_part[at] = __uint_as_float(x[i]);
+              y[i] = __float_as_uint(a.dq_part[row + (size_t)i * a.dk] + __uint_as_float(y[i]));
+              x[i] = __float_as_uint(a.dk_part[row + (size_t)i * a.dk] + __uint_as_float(x[i]));
             }
         }
-      } else {
+        if (a.fold == 1 || !last) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (16 * h + i < left) {
+              a.dq_part[row + (size_t)i * a.dk] = __uint_as_float(y[i]);
+              a.dk_part[row + (size_t)i * a.dk] = __uint_as_float(x[i]);
+            }
+        }
+      }
+      if (!a.dq_part || (a.fold > 1 && last)) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           uint8_t *dst = smem + L::kOffQk + at_token(i);
@@ -473,14 +491,14 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     bool ok = true;
     auto store = [&](int j) {                              // dq, dk of the block's j-th chunk
       ok = ok && mbar_wait(&bars[kOut], j & 1, abort_flag);
-      if (!ok || a.dq_part) return;
+      if (!ok || (a.dq_part && (a.fold == 1 || j % a.fold != a.fold - 1))) return;
       const long long job = job_of(j);
       const int bh = (int)(job / a.N), t0 = (int)(job % a.N) * kC;
       const uint8_t *src = smem + L::kOffQk;
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        tma_store_3d(&tmdk, src + 2 * p * kPanel, 64 * p, t0, bh);
-        tma_store_3d(&tmdq, src + (2 * p + 1) * kPanel, 64 * p, t0, bh);
+        tma_store_3d(&tmdk, src + 2 * p * kPanel, 64 * p, t0, bh / a.fold);
+        tma_store_3d(&tmdq, src + (2 * p + 1) * kPanel, 64 * p, t0, bh / a.fold);
       }
       bulk_commit_group();
       bulk_wait_read_all();
@@ -560,7 +578,7 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   if (threadIdx.x == 0 && *abort_flag) flag_status(a.status, kStatusDeviceTimeout);
 }
 
-template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v) {
+template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v, int fold) {
   CUtensorMap tq, tk, tv, tdo, tdq, tdk;
   const long long BHk = a.BH / a.H * a.Hk;
   if (!make_tma_3d_bf16_box(&tq, a.q, d_k, a.T, BHk, 64, kC, true) ||
@@ -574,16 +592,24 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k,
   auto kern = gd_grads_tc_kernel<DK, DV>;
   GD_ALLOW_SMEM(kern, bytes);
   const Args x{a.g, a.beta, a.img_S, a.img_D, a.img_dS, a.img_dR, a.dg, a.dbeta, a.dq_part, a.dk_part,
-               a.status, a.H, a.Hk, a.T, a.N, d_k, a.BH * a.N};
+               a.status, a.H, a.Hk, a.T, a.N, d_k, fold, a.BH * a.N / fold};
   ProfileScope prof("gd_tc_grads", a.stream);
-  kern<<<(unsigned)(x.jobs < kGdSms ? x.jobs : kGdSms), kThreads, bytes, a.stream>>>(tq, tk, tv, tdo, tdq, tdk, x);
+  kern<<<(unsigned)(x.units < kGdSms ? x.units : kGdSms), kThreads, bytes, a.stream>>>(tq, tk, tv, tdo, tdq, tdk, x);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+// Where value heads share keys, a block adds up a chunk's dq and dk over them (in
+// head order), as long as there are chunks enough for the blocks; otherwise the
+// parts go through the workspace and a kernel of their own (8 heads of 16384 tokens,
+// each shared by two: 57 us, and 90 us of writing and reading back beside it).
 cudaError_t gd_tc_grads_wide(const GatedDeltaLaunch &a, int d_k, int d_v) {
-  return gd_padded(d_v) == 64 ? launch<128, 64>(a, d_k, d_v) : launch<128, 128>(a, d_k, d_v);
+  const int group = a.H / a.Hk;
+  const int fold = a.dq_part && a.BH / group * a.N >= 2 * kGdSms ? group : 1;
+  const cudaError_t e =
+      gd_padded(d_v) == 64 ? launch<128, 64>(a, d_k, d_v, fold) : launch<128, 128>(a, d_k, d_v, fold);
+  return e == cudaSuccess && a.dq_part && fold == 1 ? gd_sum_groups(a, d_k, true) : e;
 }
 
 }  // namespace kata

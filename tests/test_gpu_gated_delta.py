@@ -174,6 +174,19 @@ def test_sequences_in_segments(d_k, d_v, B, Hk, H, T):
             close(got[name][B - 1:], r, d_k, d_v, True, name)
 
 
+@pytest.mark.parametrize("d_k, d_v", [(128, 64), (128, 128), (64, 64)])
+def test_shared_heads_of_many_chunks(d_k, d_v):
+    """Three value heads a key head and more chunks than blocks: the gradients of
+    the keys are added up inside a block; one key head and its value heads."""
+    t = make(2, 5, 15, 1990, d_k, d_v, "bf16", seed=23)
+    got = dict(zip(GRADS, backward(on_gpu(t))))
+    for b, k in ((0, 0), (1, 4)):
+        pick = {n: x[b:b + 1, k:k + 1] if n in ("q", "k") else x[b:b + 1, 3 * k:3 * k + 3] for n, x in t.items()}
+        for name, r in zip(GRADS, oracle_backward(pick)):
+            part = slice(k, k + 1) if name in ("dq", "dk") else slice(3 * k, 3 * k + 3)
+            close(got[name][b:b + 1, part], r, d_k, d_v, True, name)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d_k, d_v", [(128, 128), (64, 32)])
 def test_more_heads_than_run_at_once(dtype, d_k, d_v):
