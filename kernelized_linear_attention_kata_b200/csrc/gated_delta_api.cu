@@ -50,6 +50,11 @@ struct Regions {
 // fp32 on kernels of its own.
 bool on_tensor_cores(kata_dtype_t dtype) { return dtype == KATA_DTYPE_BF16; }
 
+// The bf16 gradient of few tokens runs in fp32: the gradients of the gates are dots
+// whose terms cancel, and with few of them nothing averages out what 16-bit operands
+// leave (2e-5 of their norm for one token of two heads, 7e-6 from 30 tokens on).
+bool few_tokens(long long BH, int T) { return BH * T < 128; }
+
 bool aligned16(std::initializer_list<const void *> ps) {
   for (const void *p : ps)
     if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
@@ -88,7 +93,7 @@ size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype,
     a.dq_part = r.take(tokens * d_k);
     a.dk_part = r.take(tokens * d_k);
   }
-  if (on_tensor_cores(dtype)) {
+  if (on_tensor_cores(dtype) && !few_tokens(a.BH, a.T)) {
     place_chain(a, d_k, d_v, true, r);
     a.img_S = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
     a.img_dS = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
@@ -103,6 +108,11 @@ size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype,
   a.ends = r.take(chunks * d_k * d_v);
   a.writes = r.take(tokens * d_v);
   a.dR = r.take(tokens * d_v);
+  if (on_tensor_cores(dtype)) {
+    const size_t keys = a.H > 0 ? tokens / (a.H / a.Hk) * d_k : 0;
+    const size_t n[7] = {keys, keys, tokens * d_v, tokens * d_v, keys, keys, tokens * d_v};
+    for (int i = 0; i < 7; ++i) a.in_f32[i] = r.take(n[i]);
+  }
   return r.used;
 }
 
@@ -207,7 +217,9 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
   a.dout = dout; a.dS = dS; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
   a.status = static_cast<unsigned *>(workspace);
-  const cudaError_t e = tc ? gd_tc_backward(a, d_k, d_v) : gd_f32_backward(a, d_k, d_v);
+  const cudaError_t e = !tc                      ? gd_f32_backward(a, d_k, d_v)
+                        : few_tokens(a.BH, a.T) ? gd_bf16_gradient_in_f32(a, d_k, d_v)
+                                                : gd_tc_backward(a, d_k, d_v);
   return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
 }
 

@@ -174,6 +174,17 @@ def test_sequences_in_segments(d_k, d_v, B, Hk, H, T):
             close(got[name][B - 1:], r, d_k, d_v, True, name)
 
 
+@pytest.mark.parametrize("d_k, d_v", [(16, 32), (64, 64), (128, 128)])
+@pytest.mark.parametrize("B, Hk, H, T", [(1, 1, 3, 7), (2, 2, 4, 9), (1, 1, 2, 1), (1, 2, 4, 31), (1, 2, 4, 32)])
+def test_gradient_of_few_tokens(d_k, d_v, B, Hk, H, T):
+    """Shared heads below and at the size from which the bf16 gradient runs on the
+    tensor cores; below it the sums are fp32's."""
+    t = make(B, Hk, H, T, d_k, d_v, "bf16", seed=5 * T + d_k)
+    ref = oracle_backward(t)
+    for name, x, r in zip(GRADS, backward(on_gpu(t)), ref):
+        close(x, r, d_k, d_v, B * H * T >= 128, name)
+
+
 @pytest.mark.parametrize("d_k, d_v", [(128, 64), (128, 128), (64, 64)])
 def test_shared_heads_of_many_chunks(d_k, d_v):
     """Three value heads a key head and more chunks than blocks: the gradients of
