@@ -427,7 +427,8 @@ KATA_API kata_status_t kata_fwd_delta(const void *q, const void *k, const void *
  * d_k, d_v in {16, 32, 64, 128}; any T. T = 0 copies S0 to S_out. bf16 runs
  * on the tensor cores (fp32 operands of a product as two bf16 halves, 16 bits;
  * fp32 sums and state) and takes 16-byte aligned q, k, v, o
- * (KATA_ERR_INVALID_ARGUMENT otherwise); fp32 on the CUDA cores.
+ * (KATA_ERR_INVALID_ARGUMENT otherwise); fp32 products are made of three TF32
+ * parts, as exact as fp32 arithmetic.
  * A NaN or infinity in a token reaches the whole of its chunk and all later
  * tokens of its head.
  * Outputs may not overlap inputs.
@@ -449,7 +450,8 @@ KATA_API kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const 
  * [B, H, d_k, d_v]). The forward's output is not an input: the states at the
  * chunks' borders are rebuilt into the workspace. Outputs may not overlap
  * inputs. Results are bitwise reproducible, as the forward's are. bf16 runs in
- * fp32 where B x H x T < 128 (few gate gradients, whose terms cancel). T = 0 copies dS to dS0.
+ * fp32 where B x H x T < 128 (few gate gradients, whose terms cancel). T = 0
+ * copies dS to dS0.
  */
 KATA_API size_t kata_bwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_k, int d_v,
                                                      kata_dtype_t dtype);

@@ -18,8 +18,8 @@ template <typename From, typename To>
 __global__ void gd_convert_kernel(const Arrays<From, To> a) {
   const From *from = a.from[blockIdx.y];
   To *to = a.to[blockIdx.y];
-  for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < a.n[blockIdx.y]; e += (size_t)gridDim.x * blockDim.x)
-    to[e] = from_f<To>(to_f(from[e]));
+  const size_t n = a.n[blockIdx.y], step = (size_t)gridDim.x * blockDim.x;
+  for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += step) to[e] = from_f<To>(to_f(from[e]));
 }
 
 template <typename From, typename To>
@@ -46,7 +46,8 @@ cudaError_t gd_bf16_gradient_in_f32(const GatedDeltaLaunch &a, int d_k, int d_v)
   e = gd_f32_backward(f, d_k, d_v);
   if (e != cudaSuccess) return e;
   const Arrays<float, bf16> out{{t[4], t[5], t[6], nullptr},
-                                {static_cast<bf16 *>(a.dq), static_cast<bf16 *>(a.dk), static_cast<bf16 *>(a.dv), nullptr},
+                                {static_cast<bf16 *>(a.dq), static_cast<bf16 *>(a.dk), static_cast<bf16 *>(a.dv),
+                                 nullptr},
                                 {keys, keys, values, 0}};
   return run(out, 3, a.stream);
 }

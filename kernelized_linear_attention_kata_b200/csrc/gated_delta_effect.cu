@@ -6,7 +6,7 @@
 // The two chains share K, M and the decays, and each waits most of the time (for
 // its MMAs, then the MMAs for its next operand): the state warps make one
 // chain's operands while the tensor core works on the other's. A chunk of both
-// takes 4.6K cycles where each alone takes 5.7K. Segment 0 starts from the
+// takes 3.4 us at d_k = 64 and 4.2 at 128, where the two alone take 5.0 and 5.5. Segment 0 starts from the
 // caller's state, which makes its B the next one's starting state: it needs no F.
 //
 // Layout, operands and warps as in gated_delta_tc.cu; tensor memory columns of

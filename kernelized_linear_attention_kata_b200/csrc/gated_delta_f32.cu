@@ -61,9 +61,9 @@ cudaError_t grads(const GatedDeltaLaunch &a, int d_v) {
   return cudaGetLastError();
 }
 
-// Value columns a block of the chains: the columns are independent, and 16
-// instead of 32 take three quarters of the time a chunk, so 16 as long as all
-// blocks still run at once.
+// Value columns a block of the chains: the columns are independent and a block
+// of 16 has half the products of one of 32, so 16 as long as all blocks still run
+// at once.
 bool narrow(const GatedDeltaLaunch &a, int d_v) { return d_v == 16 || a.BH * (d_v / 16) <= kGdSms; }
 
 template <int DK>

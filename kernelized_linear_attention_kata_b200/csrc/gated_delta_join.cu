@@ -40,7 +40,8 @@ __device__ __forceinline__ void join(JoinSmem<DK> &s, const float *__restrict__ 
   fetch(0);
   {
     const float *first = states + (size_t)(BACK ? G - 2 : 1) * DK * DV;
-    for (int e = tid; e < DK * kCols; e += kThreads) s.S[e / kCols * LS + e % kCols] = first[(size_t)(e / kCols) * DV + e % kCols];
+    for (int e = tid; e < DK * kCols; e += kThreads)
+      s.S[e / kCols * LS + e % kCols] = first[(size_t)(e / kCols) * DV + e % kCols];
   }
   for (int i = 0; i < steps; ++i) {
     fetch(i + 1);

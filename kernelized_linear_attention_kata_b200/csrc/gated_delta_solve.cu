@@ -1,5 +1,6 @@
-// The chunk-local part of the gated delta rule, all chunks at once (bf16): M = (I + L)^-1 and P of each 64-token chunk as MMA operands, with
-// its decays, into the workspace (the record of gated_delta_tc.cuh).
+// The chunk-local part of the gated delta rule, all chunks at once (bf16): M =
+// (I + L)^-1 and P of each 64-token chunk as MMA operands, with its decays, into
+// the workspace (the record of gated_delta_tc.cuh).
 //
 // One block of four warps a chunk: [K; Q] K^T by tcgen05 (K rows on TMEM lanes
 // 0-63, Q rows on 64-127), thread = row; the K rows become L and are inverted

@@ -23,13 +23,14 @@
 // every later state.
 //
 // What bounds it: the chain S -> K S -> R -> D -> S' of one chunk, three MMA
-// rounds and three passes of the value threads over the columns. What does
-// not depend on S is kept off it: M, P and the decays come ready from the
-// solve (gated_delta_solve.cu), and a chunk's P D runs while the state warps make
-// S' and its operand, its outputs leave during the next one's K S (d_k = 64: M R). With fewer heads than SMs the sequence is cut into G
-// segments: each but the last is first walked for its effect on a state, S_end =
-// F S_start + B (gated_delta_effect.cu), a small kernel joins them, and the segments
-// then run side by side. For the gradient the same kernel without outputs saves every
+// rounds and three passes of the value threads over the columns. What does not
+// depend on S is kept off it: M, P and the decays come ready from the solve
+// (gated_delta_solve.cu), and a chunk's P D runs while the state warps make S'
+// and its operand, its outputs leave during the next one's K S (d_k = 64: M R).
+// With fewer heads than SMs the sequence is cut into G segments: each but the
+// last is first walked for its effect on a state, S_end = F S_start + B
+// (gated_delta_effect.cu), a small kernel joins them, and the segments then run
+// side by side. For the gradient the same kernel without outputs saves every
 // chunk's S and D (gated_delta_bwd_tc.cu).
 //
 // An MMA takes 70-85 cycles here whatever its N (from one issuing thread or from
