@@ -37,7 +37,7 @@ struct GatedDeltaLaunch {
   float *writes = nullptr, *dR = nullptr;       // [BH][T][d_v]
   float *dq_part = nullptr, *dk_part = nullptr; // [BH][T][d_k], only where heads share keys
   float *in_f32[7] = {};                        // fp32 q, k, v, dout, dq, dk, dv of a small bf16 gradient
-  // tensor-core kernels: G segments of seg_chunks chunks a head. A segment takes
+  // G segments of seg_chunks chunks a head. A segment takes
   // a state S to F S + B and, back, its gradient E to F^T E + B'.
   unsigned *status = nullptr;
   int G = 1, seg_chunks = 0;
@@ -61,6 +61,8 @@ struct GatedDeltaStep {
 // fp32 kernels.
 cudaError_t gd_f32(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_f32_backward(const GatedDeltaLaunch &a, int d_k, int d_v);
+void gd_f32_split(long long BH, int N, int d_k, int d_v, bool gradient, int *G, int *seg_chunks);
+cudaError_t gd_f32_join(const GatedDeltaLaunch &a, int d_k, int d_v);
 cudaError_t gd_bf16_gradient_in_f32(const GatedDeltaLaunch &a, int d_k, int d_v);   // bf16 tensors
 // Tensor-core forward (bf16, 16-byte aligned q, k, v, o).
 // The kernels' head sizes: 64 or 128.

@@ -73,6 +73,17 @@ void place_chain(GatedDeltaLaunch &a, int d_k, int d_v, bool gradient, Regions &
   }
 }
 
+// The fp32 kernels' segments.
+void place_segments(GatedDeltaLaunch &a, int d_k, int d_v, bool gradient, Regions &r) {
+  a.seg_chunks = a.N;
+  if (a.BH > 0 && a.T > 0) gd_f32_split(a.BH, a.N, d_k, d_v, gradient, &a.G, &a.seg_chunks);
+  if (a.G > 1) {
+    a.F = r.take((size_t)a.BH * (a.G - 2) * d_k * d_k);
+    a.starts_seg = r.take((size_t)a.BH * a.G * d_k * d_v);
+    if (gradient) a.ends_seg = r.take((size_t)a.BH * a.G * d_k * d_v);
+  }
+}
+
 size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, void *ws) {
   Regions r{static_cast<unsigned char *>(ws)};
   if (on_tensor_cores(dtype)) {
@@ -83,6 +94,7 @@ size_t place_forward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype, 
   a.M = r.take(square);
   a.P = r.take(square);
   a.gates = r.take((size_t)a.BH * a.N * 3 * kGdChunk);
+  place_segments(a, d_k, d_v, false, r);
   return r.used;
 }
 
@@ -104,6 +116,7 @@ size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype,
   a.M = r.take(chunks * kGdChunk * kGdChunk);
   a.P = r.take(chunks * kGdChunk * kGdChunk);
   a.gates = r.take(chunks * 3 * kGdChunk);
+  place_segments(a, d_k, d_v, true, r);
   a.starts = r.take(chunks * d_k * d_v);
   a.ends = r.take(chunks * d_k * d_v);
   a.writes = r.take(tokens * d_v);

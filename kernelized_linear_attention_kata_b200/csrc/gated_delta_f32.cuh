@@ -26,9 +26,10 @@
 // -100: e^-100 is 0 in fp32, and the differences stay finite.
 //
 // Kernels: solve (M, P and the decays of every chunk, all chunks at once),
-// chain (one block per head and CB value columns walks the chunks: the columns
-// of S follow the rule on their own), chain_reverse (dS, dR, dV, last chunk
-// first), grads (dq, dk, dg, dbeta, all chunks at once).
+// chain (one block per head, segment and CB value columns walks the chunks: the
+// columns of S follow the rule on their own), chain_reverse (dS, dR, dV, last
+// chunk first), grads (dq, dk, dg, dbeta, all chunks at once). Few heads are cut
+// into segments as in bf16: their effects first, joined by gated_delta_join.cu.
 #pragma once
 
 #include "common.cuh"
@@ -293,42 +294,61 @@ struct ChainSmem {
   float S[DK * LS], V[2][kC * LS], R[kC * LS], D[kC * LS], gates[2][kRec];
 };
 
-template <int DK, int CB>
+// A head's sequence may be cut into G segments of seg_chunks chunks. EFFECT: what a
+// segment does to a state, S -> F S + B, without outputs: the first kind0 blocks walk
+// segments 0 .. G - 2 from S = 0 (segment 0: from S0) to B, into `states` of the next
+// segment, the others segments 1 .. G - 2 from S = I without V to F.
+struct Segments {
+  float *states, *F;
+  int G, chunks, kind0;
+};
+
+template <int DK, int CB, bool EFFECT>
 __global__ void __launch_bounds__(kThreads)
 gd_chain_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
                 const float *__restrict__ gates, const float *__restrict__ M, const float *__restrict__ P,
                 const float *__restrict__ S0, float *__restrict__ o, float *__restrict__ S_out,
-                float *__restrict__ starts, float *__restrict__ writes, int H, int Hk, int T, int N, int DV) {
+                float *__restrict__ starts, float *__restrict__ writes, int H, int Hk, int T, int N, int DV,
+                const Segments sg) {
   extern __shared__ __align__(16) float sm[];
   using Smem = ChainSmem<DK, CB>;
   Smem &s = *reinterpret_cast<Smem *>(sm);
   constexpr int LD = Smem::LD, LS = Smem::LS;
-  const int NB = DV / CB, tid = threadIdx.x;
-  const long long bh = blockIdx.x / NB;
-  const int c0 = (blockIdx.x % NB) * CB;
+  const int tid = threadIdx.x;
+  const bool to_F = EFFECT && (int)blockIdx.x >= sg.kind0;
+  const int block = (int)blockIdx.x - (to_F ? sg.kind0 : 0), NB = (to_F ? DK : DV) / CB;
+  const int segs = EFFECT ? sg.G - 1 - to_F : sg.G, seg = block / NB % segs + to_F;
+  const long long bh = block / NB / segs;
+  const int c0 = (block % NB) * CB;
+  const int first = seg * sg.chunks, end = first + sg.chunks < N ? first + sg.chunks : N;
   const Where at(bh, H, Hk, T);
-  const size_t state = (size_t)bh * DK * DV, chunk0 = (size_t)bh * N;
+  const size_t state = (size_t)DK * DV, chunk0 = (size_t)bh * N;
+  const float *from = seg == 0 ? (S0 ? S0 + bh * state : nullptr) : EFFECT ? nullptr : sg.states + (bh * sg.G + seg) * state;
   for (int e = tid; e < DK * CB; e += kThreads)
-    s.S[(e / CB) * LS + e % CB] = S0 ? S0[state + (size_t)(e / CB) * DV + c0 + e % CB] : 0.f;
+    s.S[(e / CB) * LS + e % CB] = to_F ? (e / CB == c0 + e % CB ? 1.f : 0.f)
+                                  : from ? from[(size_t)(e / CB) * DV + c0 + e % CB]
+                                         : 0.f;
+  if (to_F)
+    for (int e = tid; e < kC * CB; e += kThreads) s.V[0][(e / CB) * LS + e % CB] = 0.f;
   using GS = Gemm<kC, CB, false, false, LD, LS>;         // K S, Q S
   using GD = Gemm<kC, CB, false, false, kLD, LS>;        // M R, P D: the same tiles
   using GU = Gemm<DK, CB, true, false, LD, LS>;          // K^T D
   auto fetch_kqv = [&](int n) {
-    if (n < N) {
+    if (n < end) {
       fetch_rows<DK, LD>(s.k[n & 1], k + at.k * DK, n * kC, T, DK, 0);
       if (o) fetch_rows<DK, LD>(s.q, q + at.k * DK, n * kC, T, DK, 0);
-      fetch_rows<CB, LS>(s.V[0], v + at.v * DV, n * kC, T, DV, c0);
+      if (!to_F) fetch_rows<CB, LS>(s.V[0], v + at.v * DV, n * kC, T, DV, c0);
       fetch_gates(s.gates[n & 1], gates + (chunk0 + n) * kRec);
     }
     copies_done();
   };
   auto fetch_tile = [&](float *dst, const float *src, int n, bool wanted) {
-    if (n < N && wanted) fetch_square(dst, src + (chunk0 + n) * kC * kC);
+    if (n < end && wanted) fetch_square(dst, src + (chunk0 + n) * kC * kC);
     copies_done();
   };
-  fetch_kqv(0);
-  fetch_tile(s.M, M, 0, true);
-  for (int n = 0; n < N; ++n) {
+  fetch_kqv(first);
+  fetch_tile(s.M, M, first, true);
+  for (int n = first; n < end; ++n) {
     const int t0 = n * kC;
     const float *sk = s.k[n & 1], *from_start = s.gates[n & 1], *to_end = from_start + kC, *beta = to_end + kC;
     copies_wait<1>();
@@ -394,40 +414,53 @@ gd_chain_kernel(const float *__restrict__ q, const float *__restrict__ k, const 
     }
   }
   __syncthreads();
-  if (S_out)
+  float *to = nullptr;
+  if (!EFFECT)
+    to = S_out && seg == sg.G - 1 ? S_out + bh * state : nullptr;
+  else
+    to = to_F ? sg.F + (bh * (sg.G - 2) + seg - 1) * DK * DK : sg.states + (bh * sg.G + seg + 1) * state;
+  const int ld = to_F ? DK : DV;
+  if (to)
     for (int e = tid; e < DK * CB; e += kThreads)
-      S_out[state + (size_t)(e / CB) * DV + c0 + e % CB] = s.S[(e / CB) * LS + e % CB];
+      to[(size_t)(e / CB) * ld + c0 + e % CB] = s.S[(e / CB) * LS + e % CB];
 }
 
 // ---------------------------------------------------------------------------
 // The reverse chain: dS through the chunks, last first, for CB value columns.
 // K, dO and the gates have two buffers; Q is fetched at the chunk's beginning for
-// its end.
+// its end. EFFECT: what segments 1 .. G - 1 pass on from dS' = 0 (the last: from dS)
+// into `states` of the segment before.
 // ---------------------------------------------------------------------------
-template <int DK, int CB>
+template <int DK, int CB, bool EFFECT>
 __global__ void __launch_bounds__(kThreads)
 gd_chain_reverse_kernel(const float *__restrict__ q, const float *__restrict__ k,
                         const float *__restrict__ dout, const float *__restrict__ gates,
                         const float *__restrict__ M, const float *__restrict__ P,
                         const float *__restrict__ dS, float *__restrict__ dv, float *__restrict__ dR,
-                        float *__restrict__ ends, float *__restrict__ dS0, int H, int Hk, int T, int N, int DV) {
+                        float *__restrict__ ends, float *__restrict__ dS0, int H, int Hk, int T, int N, int DV,
+                        const Segments sg) {
   extern __shared__ __align__(16) float sm[];
   using Smem = ChainSmem<DK, CB>;
   Smem &s = *reinterpret_cast<Smem *>(sm);
   constexpr int LD = Smem::LD, LS = Smem::LS;
-  const int NB = DV / CB, tid = threadIdx.x;
-  const long long bh = blockIdx.x / NB;
-  const int c0 = (blockIdx.x % NB) * CB;
+  const int tid = threadIdx.x, NB = DV / CB, block = (int)blockIdx.x;
+  const int segs = EFFECT ? sg.G - 1 : sg.G, seg = block / NB % segs + (EFFECT ? 1 : 0);
+  const long long bh = block / NB / segs;
+  const int c0 = (block % NB) * CB;
+  const int first = seg * sg.chunks, end = first + sg.chunks < N ? first + sg.chunks : N;
   const Where at(bh, H, Hk, T);
-  const size_t state = (size_t)bh * DK * DV, chunk0 = (size_t)bh * N;
+  const size_t state = (size_t)DK * DV, chunk0 = (size_t)bh * N;
+  const float *from = seg == sg.G - 1 ? (dS ? dS + bh * state : nullptr)
+                      : EFFECT        ? nullptr
+                                      : sg.states + (bh * sg.G + seg) * state;
   for (int e = tid; e < DK * CB; e += kThreads)
-    s.S[(e / CB) * LS + e % CB] = dS ? dS[state + (size_t)(e / CB) * DV + c0 + e % CB] : 0.f;
+    s.S[(e / CB) * LS + e % CB] = from ? from[(size_t)(e / CB) * DV + c0 + e % CB] : 0.f;
   using GS = Gemm<kC, CB, false, false, LD, LS>;         // K dS
   using GD = Gemm<kC, CB, true, false, kLD, LS>;         // P^T dO, M^T dD: the same tiles
   using GU = Gemm<DK, CB, true, false, LD, LS>;          // Q^T dO, K^T dV
   auto fetch_kp = [&](int i) {                           // the i-th from the end
-    if (i < N) {
-      const int n = N - 1 - i;
+    if (i < end - first) {
+      const int n = end - 1 - i;
       fetch_rows<DK, LD>(s.k[i & 1], k + at.k * DK, n * kC, T, DK, 0);
       fetch_rows<CB, LS>(s.V[i & 1], dout + at.v * DV, n * kC, T, DV, c0);
       fetch_gates(s.gates[i & 1], gates + (chunk0 + n) * kRec);
@@ -436,21 +469,22 @@ gd_chain_reverse_kernel(const float *__restrict__ q, const float *__restrict__ k
     copies_done();
   };
   auto fetch_m = [&](int i) {
-    if (i < N) fetch_square(s.M, M + (chunk0 + N - 1 - i) * kC * kC);
+    if (i < end - first) fetch_square(s.M, M + (chunk0 + end - 1 - i) * kC * kC);
     copies_done();
   };
   fetch_kp(0);
   fetch_m(0);
-  for (int i0 = 0; i0 < N; ++i0) {
-    const int n = N - 1 - i0, t0 = n * kC;
+  for (int i0 = 0; i0 < end - first; ++i0) {
+    const int n = end - 1 - i0, t0 = n * kC;
     const float *sk = s.k[i0 & 1], *dO = s.V[i0 & 1], *from_start = s.gates[i0 & 1], *to_end = from_start + kC,
                 *beta = to_end + kC;
     copies_wait<1>();
     __syncthreads();                                       // K, dO, P, the gates and dS are there; Q has been read
     fetch_rows<DK, LD>(s.q, q + at.k * DK, t0, T, DK, 0);
     copies_done();
-    for (int e = tid; e < DK * CB; e += kThreads)
-      ends[(chunk0 + n) * DK * DV + (size_t)(e / CB) * DV + c0 + e % CB] = s.S[(e / CB) * LS + e % CB];
+    if (!EFFECT)
+      for (int e = tid; e < DK * CB; e += kThreads)
+        ends[(chunk0 + n) * DK * DV + (size_t)(e / CB) * DV + c0 + e % CB] = s.S[(e / CB) * LS + e % CB];
     float ks[GS::TM][GS::TN];
     GS::zero(ks);
     GS::run(sk, s.S, ks, 0, DK);
@@ -476,7 +510,7 @@ gd_chain_reverse_kernel(const float *__restrict__ q, const float *__restrict__ k
         const int t = GD::row(i), c = GD::col(j);
         const float x = beta[t] * d[i][j];
         s.R[t * LS + c] = -from_start[t] * x;
-        if (t0 + t < T) {
+        if (!EFFECT && t0 + t < T) {
           dv[(at.v + t0 + t) * DV + c0 + c] = x;
           dR[(at.v + t0 + t) * DV + c0 + c] = d[i][j];
         }
@@ -500,9 +534,10 @@ gd_chain_reverse_kernel(const float *__restrict__ q, const float *__restrict__ k
     }
   }
   __syncthreads();
-  if (dS0)
+  float *to = EFFECT ? sg.states + (bh * sg.G + seg - 1) * state : seg == 0 && dS0 ? dS0 + bh * state : nullptr;
+  if (to)
     for (int e = tid; e < DK * CB; e += kThreads)
-      dS0[state + (size_t)(e / CB) * DV + c0 + e % CB] = s.S[(e / CB) * LS + e % CB];
+      to[(size_t)(e / CB) * DV + c0 + e % CB] = s.S[(e / CB) * LS + e % CB];
 }
 
 // ---------------------------------------------------------------------------

@@ -98,5 +98,10 @@ cudaError_t gd_tc_join(const GatedDeltaLaunch &a, int d_k, int d_v) {
   if (a.G <= 2) return cudaSuccess;                        // one border: its state is there
   return gd_padded(d_k) == 64 ? run<64>(a, gd_padded(d_v)) : run<128>(a, gd_padded(d_v));
 }
+cudaError_t gd_f32_join(const GatedDeltaLaunch &a, int d_k, int d_v) {
+  if (a.G <= 2) return cudaSuccess;
+  if (d_k <= 32) return d_k == 16 ? run<16>(a, d_v) : run<32>(a, d_v);
+  return d_k == 64 ? run<64>(a, d_v) : run<128>(a, d_v);
+}
 
 }  // namespace kata

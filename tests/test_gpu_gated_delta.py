@@ -148,13 +148,14 @@ def test_one_long_head(dtype, d_k, d_v):
         close(x, r, d_k, d_v, dtype == "bf16", name)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d_k, d_v", [(16, 128), (32, 16), (64, 64), (64, 128), (128, 32), (128, 64), (128, 128)])
-@pytest.mark.parametrize("B, Hk, H, T", [(1, 1, 3, 1000), (2, 1, 2, 129), (1, 4, 60, 540)])
-def test_sequences_in_segments(d_k, d_v, B, Hk, H, T):
+@pytest.mark.parametrize("B, Hk, H, T", [(1, 1, 3, 1000), (2, 1, 2, 129), (1, 4, 60, 540), (1, 2, 2, 2500)])
+def test_sequences_in_segments(dtype, d_k, d_v, B, Hk, H, T):
     """Few enough heads for the sequence to be cut: states and their gradients
     pass over the borders of segments, the last of which is short, with shared
     keys and padded head sizes; the first and the last head of the last batch."""
-    t = make(B, Hk, H, T, d_k, d_v, "bf16", seed=T + d_k + d_v)
+    t = make(B, Hk, H, T, d_k, d_v, dtype, seed=T + d_k + d_v)
     t["g"] *= 0.05                                  # the carry matters over many chunks
     d = on_gpu(t)
     o, S = forward(d)
@@ -163,15 +164,15 @@ def test_sequences_in_segments(d_k, d_v, B, Hk, H, T):
         k = h // (H // Hk)
         pick = {n: x[B - 1:, k:k + 1] if n in ("q", "k") else x[B - 1:, h:h + 1] for n, x in t.items()}
         ref_o, ref_S = oracle_forward(pick)
-        close(o[B - 1:, h:h + 1], ref_o, d_k, d_v, True, "o")
-        close(S[B - 1:, h:h + 1], ref_S, d_k, d_v, True, "S")
+        close(o[B - 1:, h:h + 1], ref_o, d_k, d_v, dtype == "bf16", "o")
+        close(S[B - 1:, h:h + 1], ref_S, d_k, d_v, dtype == "bf16", "S")
         ref = dict(zip(GRADS, oracle_backward(pick)))
         for name in ("dv", "dg", "dbeta", "dS0"):
-            close(got[name][B - 1:, h:h + 1], ref[name], d_k, d_v, True, name)
+            close(got[name][B - 1:, h:h + 1], ref[name], d_k, d_v, dtype == "bf16", name)
     if H // Hk <= 3:                                # the sums over a shared head's value heads
         last = {n: x[B - 1:] for n, x in t.items()}
         for name, r in zip(GRADS[:2], oracle_backward(last)):
-            close(got[name][B - 1:], r, d_k, d_v, True, name)
+            close(got[name][B - 1:], r, d_k, d_v, dtype == "bf16", name)
 
 
 @pytest.mark.parametrize("d_k, d_v", [(16, 32), (64, 64), (128, 128)])
