@@ -264,6 +264,8 @@ def kata_fwd_gated_delta(q, k, v, g, beta, o, S0=None, S_out=None, workspace=Non
     """Gated delta rule forward into `o` (see include/kata.h): q, k
     [B, H_k, T, d_k], v, o [B, H, T, d_v], g (log decays) and beta (write
     strengths) fp32 [B, H, T]; S0 / S_out optional fp32 [B, H, d_k, d_v]."""
+    if o is None:
+        raise TypeError("o must be a tensor")
     st = _on(stream, q, binding().fwd, q, k, v, g, beta, S0, False, o, S_out, workspace)[0]
     if st:
         check("kata_fwd_gated_delta", st)
@@ -287,7 +289,9 @@ def kata_bwd_gated_delta(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, S0=None,
 def kata_gated_delta_step(q, k, v, g, beta, S, y, stream=None):
     """In-place one-token step of the gated delta rule: q, k [B, H_k, d_k],
     v, y [B, H, d_v], g, beta fp32 [B, H]; S fp32 [B, H, d_k, d_v] updated."""
-    st, y = _on(stream, q, binding().step, q, k, v, g, beta, S, y)
+    if y is None:
+        raise TypeError("y must be a tensor")
+    st = _on(stream, q, binding().step, q, k, v, g, beta, S, y)[0]
     if st:
         check("kata_gated_delta_step", st)
     return y
@@ -312,7 +316,10 @@ def bwd_gated_delta(q, k, v, g, beta, dout, S0=None, dS=None):
 
 def gated_delta_step(q, k, v, g, beta, S):
     """y of the one-token step, allocated with torch; S is updated in place."""
-    return kata_gated_delta_step(q, k, v, g, beta, S, None)
+    st, y = binding().step(q, k, v, g, beta, S, None)
+    if st:
+        check("kata_gated_delta_step", st)
+    return y
 
 
 def kata_workspace_status(workspace, stream=None) -> int:

@@ -116,3 +116,33 @@ def test_binding_refuses_states_and_outputs():
     with pytest.raises(ValueError):
         api.gated_delta_step(*(t[n][:, :, 0] for n in ("q", "k", "v", "g", "beta")),
                              torch.zeros(2, 2, 64, 64))
+
+
+def test_binding_refuses_what_is_no_tensor():
+    t = tensors()
+    for name in t:
+        with pytest.raises(TypeError):
+            api.fwd_gated_delta(**{**t, name: None})
+        with pytest.raises(TypeError):
+            api.bwd_gated_delta(**{**t, name: 1.0}, dout=t["v"])
+    with pytest.raises(TypeError):
+        api.bwd_gated_delta(**t, dout=None)
+    with pytest.raises(TypeError):
+        api.fwd_gated_delta(**t, S0="none")
+    with pytest.raises(TypeError):
+        api.kata_fwd_gated_delta(**t, o=None)
+    with pytest.raises(TypeError):
+        api.kata_bwd_gated_delta(**t, dout=t["v"], dq=t["q"], dk=None, dv=t["v"], dg=t["g"], dbeta=t["g"])
+    token = [t[n][:, :, 0] for n in ("q", "k", "v", "g", "beta")]
+    with pytest.raises(TypeError):
+        api.kata_gated_delta_step(*token, torch.zeros(2, 4, 64, 64), None)
+    with pytest.raises(TypeError):
+        api.gated_delta_step(*token, None)
+
+
+def test_binding_refuses_sizes_beyond_32_bits():
+    n = 1 << 31
+    q = torch.zeros(1, 1, 1, 64).expand(1, 1, n, 64)
+    gate = torch.zeros(1, 1, 1).expand(1, 1, n)
+    with pytest.raises(ValueError):
+        api.fwd_gated_delta(q, q, q, gate, gate)
