@@ -18,6 +18,7 @@
 // cut into segments, a segment passes F^T dS' + B' on: F is the forward's, B' what
 // the same chain leaves from dO and dS' = 0.
 #include "common.cuh"
+#include "gated_delta_sync.h"
 #include "gated_delta_tc.cuh"
 #include "profile.h"
 #include "tma_host.h"
@@ -53,8 +54,11 @@ template <int DK, int DV> struct Layout {
   static_assert(kOffDo + NS * kDo + kPanel <= kOffBars + 512, "operand rows stay in shared memory");
   static_assert(kBytes <= 232448, "shared memory budget");
 };
+// dV is ready: a barrier per stage, since the value warps may be as many chunks
+// ahead of the storing warp as there are stages (gated_delta_sync.h).
 enum {
-  kLoaded = 0, kFree = 4, kStored = 8, kXDone = 12, kUDone, kRDone, kSDone, kStaged, kSaved, kDvReady, kEnd, kNumBars
+  kLoaded = 0, kFree = 4, kStored = 8, kDvReady = 12, kXDone = 16, kUDone, kRDone, kSDone, kStaged, kSaved, kEnd,
+  kNumBars
 };
 // hardware barriers, value warps to issuer (0 is the block's)
 enum { kSReady = 1, kDReady, kZReady };
@@ -99,7 +103,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if ((i >= kFree && i < kFree + 4) || i == kStaged || i == kDvReady) count = kStateWarps;
+      if ((i >= kFree && i < kFree + 4) || (i >= kDvReady && i < kDvReady + 4) || i == kStaged) count = kStateWarps;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -241,7 +245,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
           }
         }
         staged();                                          // fences dV's writes too
-        warp_arrive(&bars[kDvReady]);
+        warp_arrive(&bars[kDvReady + gdsync::dv_ready(i, NS).place]);
       }
 
       // dS = e^{G_C} dS' + Q^T (e^G dO) - K^T (e^G dV)
@@ -403,7 +407,8 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       // ---------------------------------------------------------- dV's stores
       tma_prefetch_desc(&tmdv);
       for (int i = 0; i < n; ++i) {
-        if (!mbar_wait(&bars[kDvReady], i & 1, abort_flag)) break;
+        const gdsync::Turn ready = gdsync::dv_ready(i, NS);
+        if (!mbar_wait(&bars[kDvReady + ready.place], ready.parity, abort_flag)) break;
 #pragma unroll
         for (int p = 0; p < NV; ++p)
           tma_store_3d(&tmdv, smem + L::kOffDo + i % NS * L::kDo + p * kPanel, 64 * p, kC * (first + n - 1 - i), bh);
