@@ -159,7 +159,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         tmem_wait_st();
       }
       tc_fence_before();
-      hand_over(kSReady);
+      hand_over(kSReady, ok);
       if (!EFFECT) {
         ok &= stage_free(3 * i);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, false);
@@ -203,7 +203,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         tmem_wait_st();
       }
       tc_fence_before();
-      hand_over(kDReady);
+      hand_over(kDReady, ok);
       if (!EFFECT) {
         ok &= stage_free(3 * i + 1);
         if (active) stage_row<HK / 8>(stage, DV, r, HK * h, S, true);
@@ -230,7 +230,7 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         tmem_wait_st();
       }
       tc_fence_before();
-      hand_over(kZReady);
+      hand_over(kZReady, ok);
       const float whole = from_start[kC - 1];
       if (!EFFECT) {
         ok &= stage_free(3 * i + 2);

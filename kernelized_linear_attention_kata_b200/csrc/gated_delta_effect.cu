@@ -135,7 +135,7 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         tmem_wait_st();
       }
       tc_fence_before();
-      hand_over(kSReady + x);
+      hand_over(kSReady + x, ok);
     };
     ok &= warp_wait(&bars[kLoaded], 0, abort_flag);
 #pragma unroll
@@ -169,7 +169,7 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
           tmem_wait_st();
         }
         tc_fence_before();
-        hand_over(kRReady + x);
+        hand_over(kRReady + x, ok);
       }
       // D~ = e^{G_C - G} D, from its two accumulators
 #pragma unroll
@@ -192,7 +192,7 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
           tmem_wait_st();
         }
         tc_fence_before();
-        hand_over(kDtReady + x);
+        hand_over(kDtReady + x, ok);
       }
       // S' = e^{G_C} S + K^T D~, and the next chunk's operand
       const float whole = from_start[kC - 1];

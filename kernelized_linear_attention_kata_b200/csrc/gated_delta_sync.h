@@ -28,5 +28,20 @@ GD_SYNC_FN Turn turn(int use, int places) { return Turn{use % places, (uint32_t)
 // `stages` rounds ahead of the warp that stores.
 GD_SYNC_FN Turn dv_ready(int round, int stages) { return turn(round, stages); }
 
+// Hand-overs from the state warps to an issuer, on hardware barriers: these count
+// arrivals, whoever they come from, and an issuer's wait there has no limit. So no
+// state warp may come twice before the issuer has come once. A warp that passes
+// (arrives and goes on) next waits for the MMAs which the issuer starts behind the
+// barrier. Once one of its waits has given up, that order is gone, and the warp waits
+// at each further hand-over until all have come. Then all roles meet at every hand-over
+// in the same order and come to their ends. Each is of another barrier than the
+// one before it, so the first of them waits for what the warp passed last, too.
+GD_SYNC_FN bool passes(bool ok) { return ok; }
+
+// The one hand-over that a warp apart may take (D, for the outputs) is not followed
+// by a wait for it in the same chunk: two barriers by turns, so that the hand-over of
+// the next chunk is of another barrier than the one that may still be open.
+GD_SYNC_FN int output_place(int chunk) { return chunk & 1; }
+
 }  // namespace gdsync
 }  // namespace kata

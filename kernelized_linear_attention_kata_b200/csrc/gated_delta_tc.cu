@@ -93,7 +93,7 @@ enum {
   kNumBars = kEnd + 2
 };
 static_assert(8 * kNumBars + 8 <= 512, "barrier area");
-// hardware barriers, state warps to issuers (0 is the block's)
+// hardware barriers, state warps to issuers (0 is the block's; two for D by turns)
 enum { kSReady = 1, kRReady, kDtReady, kDlReady };
 
 struct Args {
@@ -159,7 +159,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     constexpr uint32_t id_64 = idesc_bf16(128, 64, false, false);
     const uint32_t acc = tbase + col_ks(c);
     const uint64_t d_p = smem_desc(smem_u32(smem) + L::kOffP + c % NV * L::kP, 16, 1024, kSw128);
-    take_over(kDlReady);
+    take_over(kDlReady + gdsync::output_place(c));
     tc_fence_after();
     if (lane == 0) {
 #pragma unroll
@@ -239,7 +239,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_st();
       }
       tc_fence_before();
-      hand_over(kSReady);
+      hand_over(kSReady, ok);
       if (OUT && !kOwnPd && c > 0) outputs(c - 1);
       if (SAVE) {
         ok &= stage_free(3 * c);
@@ -275,7 +275,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_st();
       }
       tc_fence_before();
-      hand_over(kRReady);
+      hand_over(kRReady, ok);
       if (OUT && kOwnPd && c > 0) outputs(c - 1);
       if (SAVE) {
         ok &= stage_free(3 * c + 1);
@@ -303,7 +303,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         tmem_wait_st();
       }
       tc_fence_before();
-      hand_over(kDtReady);
+      hand_over(kDtReady, ok);
       const float whole = from_start[kC - 1];
       if (OUT) {
         if (active) {
@@ -311,7 +311,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           tmem_wait_st();
         }
         tc_fence_before();
-        hand_over(kDlReady);
+        hand_over(kDlReady + gdsync::output_place(c), ok);
       }
 
       if (SAVE) {

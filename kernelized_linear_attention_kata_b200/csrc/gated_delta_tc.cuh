@@ -4,6 +4,7 @@
 #pragma once
 
 #include "gated_delta.h"
+#include "gated_delta_sync.h"
 #include "tc_common.cuh"
 
 namespace kata {
@@ -42,7 +43,8 @@ __device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) {
 // A wait by a whole warp: the result is the same in all lanes. Most waits of the
 // chains end within a few tests; a suspended thread comes back later than that.
 // Once a wait has given up, all others do at once: a warp of the chains then goes
-// on through its barriers and leaves garbage behind, and the block reports it.
+// on through its hand-overs (which it now waits for, see below) and leaves garbage
+// behind, and the block reports it.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
 #pragma unroll 1
   for (int i = 0; i < kSpins; ++i)
@@ -58,10 +60,19 @@ constexpr int kStateWarps = 16, kIssuer = 16, kLoader = 17, kSaver = 18, kChainT
 
 // Hardware barrier `id` of the state warps and the issuer: the state warps pass,
 // the issuer waits for them. Through an mbarrier the same takes 300 cycles
-// instead of 40, three or four times a chunk.
-__device__ __forceinline__ void hand_over(int id) {
+// instead of 40, three or four times a chunk. A hardware barrier counts warps, not
+// which: a state warp must not come to it again before the issuer has been there.
+// Its waits see to that as long as none of them has given up (`ok`: of this warp);
+// from then on the warp waits at the hand-overs themselves (gated_delta_sync.h).
+__device__ __forceinline__ void hand_over(int id, bool ok) {
   __syncwarp();
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(32 * (kStateWarps + 1)) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "@p bar.arrive %0, %1;\n\t"
+      "@!p bar.sync %0, %1;\n\t}" ::"r"(id),
+      "n"(32 * (kStateWarps + 1)), "r"((uint32_t)gdsync::passes(ok))
+      : "memory");
 }
 __device__ __forceinline__ void take_over(int id) {
   __syncwarp();

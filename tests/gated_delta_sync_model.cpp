@@ -5,74 +5,138 @@
 //   gated_delta_sync_model dv STAGES ROUNDS kernel|one
 //     Reverse chain: loads, value warps and the warp that stores dV, with the
 //     kernel's rule for dV's barriers or with one barrier for all rounds.
+//   gated_delta_sync_model CHAIN WARPS CHUNKS kernel|pass|place
+//     Hand-overs from WARPS state warps to the issuers of a chain (forward,
+//     forward_apart, save, effect, reverse), where any wait of a state warp may give
+//     up: with the kernels' rules, with state warps that always pass, or with one
+//     barrier for all hand-overs of D.
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <set>
 #include <string>
+#include <tuple>
 #include <vector>
 
 #include "gated_delta_sync.h"
 
-using kata::gdsync::Turn;
+namespace gdsync = kata::gdsync;
 
 namespace {
 
 struct Step {
-  enum Kind { kArrive, kWait } kind;
+  // mbarriers: one arrival completes a phase; a wait of a role that may give up
+  // goes on without it. Hardware barriers count arrivals of hand and take.
+  enum Kind { kArrive, kWait, kHand, kTake } kind;
   int bar;
   unsigned parity = 0;               // of a wait, as the kernel gives it
   int phase = 0;                     // the phase it means
 };
-using Role = std::vector<Step>;
 
 struct State {
-  std::vector<int> at, phase;        // each role's next step, each barrier's phases completed
-  bool operator<(const State &o) const { return at != o.at ? at < o.at : phase < o.phase; }
+  std::vector<int> at;               // each role's next step
+  std::vector<int> inside;           // -1, or the generation of the hardware barrier it waits at
+  std::vector<char> ok;              // none of its waits has given up
+  std::vector<int> phase;            // mbarriers: phases completed
+  std::vector<int> count, generation;   // hardware barriers
+  bool aborted = false;
+  bool operator<(const State &o) const {
+    auto tie = [](const State &s) { return std::tie(s.at, s.inside, s.ok, s.phase, s.count, s.generation, s.aborted); };
+    return tie(*this) < tie(o);
+  }
 };
 
 struct Model {
-  std::vector<Role> roles;
-  int bars = 0;
+  std::vector<std::vector<Step>> roles;
+  std::vector<char> gives_up;        // its waits have a limit
+  int bars = 0, hardware = 0, quota = 0;
+  bool (*passes)(bool) = [](bool ok) { return gdsync::passes(ok); };
+
+  void resize(int n) {
+    roles.resize(n);
+    gives_up.resize(n);
+  }
   void arrive(int role, int bar) { roles[role].push_back({Step::kArrive, bar}); }
   void wait(int role, int bar, unsigned parity, int phase) { roles[role].push_back({Step::kWait, bar, parity, phase}); }
+  void hand(int role, int bar) { roles[role].push_back({Step::kHand, bar}); }
+  void take(int role, int bar) { roles[role].push_back({Step::kTake, bar}); }
+
+  // The states that role r can come to from s by one step.
+  void moves(const State &s, int r, std::vector<State> &out, std::string &wrong) const {
+    if (s.at[r] == (int)roles[r].size()) return;
+    const Step &step = roles[r][s.at[r]];
+    State t = s;
+    if (step.kind == Step::kArrive) {
+      ++t.at[r];
+      ++t.phase[step.bar];
+      out.push_back(t);
+    } else if (step.kind == Step::kWait) {
+      // a test of a parity is true if the barrier's running phase has the other one
+      const bool there = (unsigned)(s.phase[step.bar] & 1) != step.parity;
+      ++t.at[r];
+      if (there) {
+        if (s.ok[r] && s.phase[step.bar] <= step.phase) wrong = "a wait ended early";
+        out.push_back(t);
+      }
+      if (gives_up[r] && (!there || s.aborted)) {
+        t.ok[r] = 0;
+        t.aborted = true;
+        out.push_back(t);
+      }
+    } else if (s.inside[r] >= 0) {                         // waits at a hardware barrier
+      if (s.generation[step.bar] == s.inside[r]) return;
+      ++t.at[r];
+      t.inside[r] = -1;
+      out.push_back(t);
+    } else {
+      const bool goes_on = step.kind == Step::kHand && passes(s.ok[r]);
+      if (goes_on)
+        ++t.at[r];
+      else
+        t.inside[r] = s.generation[step.bar];
+      if (++t.count[step.bar] == quota) {
+        t.count[step.bar] = 0;
+        ++t.generation[step.bar];
+      }
+      out.push_back(t);
+    }
+  }
 
   std::string walk() const {
-    std::set<State> seen;
-    std::vector<State> open{State{std::vector<int>(roles.size()), std::vector<int>(bars)}};
-    seen.insert(open[0]);
+    State first;
+    first.at.resize(roles.size());
+    first.inside.assign(roles.size(), -1);
+    first.ok.assign(roles.size(), 1);
+    first.phase.resize(bars);
+    first.count.resize(hardware);
+    first.generation.resize(hardware);
+    std::set<State> seen{first};
+    std::vector<State> open{first}, next;
+    std::string wrong;
     while (!open.empty()) {
       const State s = open.back();
       open.pop_back();
-      bool moved = false, ended = true;
+      next.clear();
+      bool ended = true;
       for (size_t r = 0; r < roles.size(); ++r) {
-        if (s.at[r] == (int)roles[r].size()) continue;
-        ended = false;
-        const Step &step = roles[r][s.at[r]];
-        State t = s;
-        ++t.at[r];
-        if (step.kind == Step::kArrive) {
-          ++t.phase[step.bar];
-        } else {
-          // a test of a parity is true if the barrier's running phase has the other one
-          if ((unsigned)(s.phase[step.bar] & 1) == step.parity) continue;
-          if (s.phase[step.bar] <= step.phase) return "a wait ended early";
-        }
-        moved = true;
-        if (seen.insert(t).second) open.push_back(t);
+        ended = ended && s.at[r] == (int)roles[r].size();
+        moves(s, (int)r, next, wrong);
       }
-      if (!ended && !moved) return "stuck";
+      if (!wrong.empty()) return wrong;
+      if (!ended && next.empty()) return "stuck";
+      for (const State &t : next)
+        if (seen.insert(t).second) open.push_back(t);
     }
     return "ok";
   }
 };
 
-int dv(int stages, int rounds, bool one) {
-  auto ready = [&](int i) { return one ? kata::gdsync::turn(i, 1) : kata::gdsync::dv_ready(i, stages); };
+std::string dv(int stages, int rounds, bool one) {
+  auto ready = [&](int i) { return one ? gdsync::turn(i, 1) : gdsync::dv_ready(i, stages); };
   const int loaded = 0, freed = stages, stored = 2 * stages, dv_ready = 3 * stages;
   Model m;
   m.bars = 4 * stages;
-  m.roles.resize(3);
+  m.resize(3);
   for (int i = 0; i < rounds; ++i) {
     const int st = i % stages, nth = i / stages;
     if (i >= stages) {
@@ -86,14 +150,75 @@ int dv(int stages, int rounds, bool one) {
     m.wait(2, dv_ready + ready(i).place, ready(i).parity, one ? i : nth);
     m.arrive(2, stored + st);
   }
-  const std::string found = m.walk();
-  puts(found.c_str());
-  return 0;
+  return m.walk();
+}
+
+std::string chain(const std::string &name, int warps, int chunks, const std::string &rule) {
+  Model m;
+  m.quota = warps + 1;
+  m.bars = m.hardware = 6;
+  if (rule == "pass") m.passes = [](bool) { return true; };
+  auto place = [&](int c) { return rule == "place" ? 0 : gdsync::output_place(c); };
+  const bool apart = name == "forward_apart";
+  m.resize(warps + 1 + apart);
+  const int issuer = warps, outputs = warps + apart;       // who takes D for the outputs
+  for (int w = 0; w < warps; ++w) m.gives_up[w] = 1;
+  auto hand = [&](int bar) {
+    for (int w = 0; w < warps; ++w) m.hand(w, bar);
+  };
+  auto wait = [&](int bar, int c) {
+    for (int w = 0; w < warps; ++w) m.wait(w, bar, c & 1, c);
+  };
+  auto issue = [&](int role, int taken, int done) {
+    m.take(role, taken);
+    m.arrive(role, done);
+  };
+  if (name == "effect") {                                  // two chains; S, R, D~ of each
+    hand(0), hand(1);
+    for (int c = 0; c < chunks; ++c) {
+      for (int part = 0; part < 3; ++part)
+        for (int x = 0; x < 2; ++x) {
+          wait(2 * part + x, c);
+          if (part < 2) hand(2 * (part + 1) + x);
+          else if (c + 1 < chunks) hand(x);
+          issue(issuer, 2 * part + x, 2 * part + x);
+        }
+    }
+  } else if (name == "reverse") {                          // S, D, Z; X is P^T dO
+    m.arrive(issuer, 3);
+    for (int i = 0; i < chunks; ++i) {
+      hand(0), wait(3, i), wait(0, i);
+      hand(1), wait(1, i);
+      hand(2), wait(2, i);
+      issue(issuer, 0, 0), issue(issuer, 1, 1), issue(issuer, 2, 2);
+      if (i + 1 < chunks) m.arrive(issuer, 3);
+    }
+  } else {                                                 // S, R, D~ and, with outputs, D in two places
+    const bool out = name != "save";
+    for (int c = 0; c < chunks; ++c) {
+      hand(0);
+      if (out && !apart && c > 0) wait(3, c - 1);
+      wait(0, c);
+      hand(1);
+      if (out && apart && c > 0) wait(3, c - 1);
+      wait(1, c);
+      hand(2);
+      if (out) hand(3 + place(c));
+      wait(2, c);
+      issue(issuer, 0, 0), issue(issuer, 1, 1), issue(issuer, 2, 2);
+      if (out) issue(outputs, 3 + place(c), 3);
+    }
+    if (out) wait(3, chunks - 1);
+  }
+  return m.walk();
 }
 
 }  // namespace
 
 int main(int argc, char **argv) {
-  if (argc == 5 && !strcmp(argv[1], "dv")) return dv(atoi(argv[2]), atoi(argv[3]), !strcmp(argv[4], "one"));
-  return 2;
+  if (argc != 5) return 2;
+  const std::string name = argv[1], rule = argv[4];
+  const int n = atoi(argv[2]), rounds = atoi(argv[3]);
+  puts((name == "dv" ? dv(n, rounds, rule == "one") : chain(name, n, rounds, rule)).c_str());
+  return 0;
 }
