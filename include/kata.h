@@ -450,7 +450,7 @@ KATA_API kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const 
  * [B, H, d_k, d_v]). The forward's output is not an input: the states at the
  * chunks' borders are rebuilt into the workspace. Outputs may not overlap
  * inputs. Results are bitwise reproducible, as the forward's are. bf16 runs in
- * fp32 where B x H x T < 128 (few gate gradients, whose terms cancel). T = 0
+ * fp32 where T < 32 (few tokens a head, whose gate gradients cancel). T = 0
  * copies dS to dS0.
  */
 KATA_API size_t kata_bwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_k, int d_v,

@@ -51,9 +51,13 @@ struct Regions {
 bool on_tensor_cores(kata_dtype_t dtype) { return dtype == KATA_DTYPE_BF16; }
 
 // The bf16 gradient of few tokens runs in fp32: the gradients of the gates are dots
-// whose terms cancel, and with few of them nothing averages out what 16-bit operands
-// leave (2e-5 of their norm for one token of two heads, 7e-6 from 30 tokens on).
-bool few_tokens(long long BH, int T) { return BH * T < 128; }
+// whose terms cancel, and with few tokens to a head nothing averages out what 16-bit
+// operands leave. Of 512 heads the worst one's dg is off by 2e-2 of its norm at one
+// token, 5e-5 at 4, 2.5e-5 at 16, 1.9e-5 at 32, 1e-5 from 64 on (in fp32: 1e-3,
+// 2.5e-6, then 1e-6; the median head 3.5e-6 and 2e-7 at any length). A head's own
+// tokens count, not the call's: a head has the same gradient in any batch. 31 tokens
+// of 4 / 128 / 512 heads, d = 64: 58 / 83 / 260 us, 38 / 39 / 98 in bf16 halves.
+bool few_tokens(int T) { return T < 32; }
 
 bool aligned16(std::initializer_list<const void *> ps) {
   for (const void *p : ps)
@@ -105,7 +109,7 @@ size_t place_backward(GatedDeltaLaunch &a, int d_k, int d_v, kata_dtype_t dtype,
     a.dq_part = r.take(tokens * d_k);
     a.dk_part = r.take(tokens * d_k);
   }
-  if (on_tensor_cores(dtype) && !few_tokens(a.BH, a.T)) {
+  if (on_tensor_cores(dtype) && !few_tokens(a.T)) {
     place_chain(a, d_k, d_v, true, r);
     a.img_S = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
     a.img_dS = r.take_bytes(chunks * gd_tc_state_image(d_k, d_v));
@@ -230,9 +234,9 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
   a.dout = dout; a.dS = dS; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
   a.status = static_cast<unsigned *>(workspace);
-  const cudaError_t e = !tc                      ? gd_f32_backward(a, d_k, d_v)
-                        : few_tokens(a.BH, a.T) ? gd_bf16_gradient_in_f32(a, d_k, d_v)
-                                                : gd_tc_backward(a, d_k, d_v);
+  const cudaError_t e = !tc             ? gd_f32_backward(a, d_k, d_v)
+                        : few_tokens(T) ? gd_bf16_gradient_in_f32(a, d_k, d_v)
+                                        : gd_tc_backward(a, d_k, d_v);
   return e == cudaSuccess ? KATA_OK : KATA_ERR_CUDA;
 }
 
