@@ -3,10 +3,11 @@
     python -m kernelized_linear_attention_kata_b200.build [--force] [--verbose]
 
 The library is a plain C-ABI shared object (see include/kata.h); nothing in
-it depends on PyTorch. Beside it, _binding.so marshals the gated delta rule's
-calls for Python (csrc/binding.cpp, built against the installed torch). The CUDA runtime is linked statically, the driver API
+it depends on PyTorch. The CUDA runtime is linked statically, the driver API
 (needed for TMA descriptors) is resolved at run time through the runtime's
 driver entry-point query, so the .so runs on any machine with the driver.
+After it, and not needed by it, _binding.so marshals the gated delta rule's calls
+for Python (csrc/binding.cpp, built against the installed torch).
 """
 
 from __future__ import annotations
@@ -18,6 +19,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -82,7 +84,18 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    build_binding(force, verbose)
+    """The library, then the binding. A binding that cannot be built (no torch, no
+    Python headers, another compiler) is a warning: every other call works without."""
+    path = build_library(force, verbose, extra)
+    try:
+        build_binding(force, verbose)
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"the gated delta rule cannot be called from Python, its binding was not built: {e}",
+                      RuntimeWarning, stacklevel=2)
+    return path
+
+
+def build_library(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     if not force and up_to_date():
         return LIB_PATH
     nvcc = nvcc_path()
