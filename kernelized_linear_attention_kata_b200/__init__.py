@@ -11,4 +11,4 @@ from .api import (alloc_workspace, bwd_chunked, bwd_chunked_workspace_bytes,  # 
                   kata_decode_step, kata_fwd_chunked, kata_fwd_chunked_sequential,
                   kata_fwd_gated_delta, kata_fwd_quadratic, kata_gated_delta_step,
                   kata_workspace_status, state_dim)
-from ._lib import KataError, binding, lib  # noqa: F401
+from ._lib import KataError, lib  # noqa: F401

@@ -8,6 +8,7 @@ point raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -128,12 +129,17 @@ def binding():
     """The compiled binding of the gated delta rule, bound to the loaded library."""
     global _binding
     if _binding is None:
+        from .build import binding_path
         handle = lib()
+        path, command = binding_path(), "`python -m kernelized_linear_attention_kata_b200.build`"
+        if not os.path.exists(path):
+            raise ImportError(f"KATA binding not built for this torch and Python: {path} is missing. Run {command}.")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._binding", path)
         try:
-            from . import _binding as module
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
         except ImportError as e:
-            raise ImportError("KATA binding not built: run "
-                              "`python -m kernelized_linear_attention_kata_b200.build`.") from e
+            raise ImportError(f"KATA binding does not load ({e}). Run {command} --force.") from e
         module.bind(*(ctypes.cast(getattr(handle, n), ctypes.c_void_p).value for n in _BOUND))
         _binding = module
     return _binding

@@ -6,8 +6,8 @@ The library is a plain C-ABI shared object (see include/kata.h); nothing in
 it depends on PyTorch. The CUDA runtime is linked statically, the driver API
 (needed for TMA descriptors) is resolved at run time through the runtime's
 driver entry-point query, so the .so runs on any machine with the driver.
-After it, and not needed by it, _binding.so marshals the gated delta rule's calls
-for Python (csrc/binding.cpp, built against the installed torch).
+After it, and not needed by it, _binding-<torch><python>.so marshals the gated delta
+rule's calls for Python (csrc/binding.cpp, built against the installed torch).
 """
 
 from __future__ import annotations
@@ -27,7 +27,6 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libkata.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
-BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
@@ -57,18 +56,26 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def binding_path() -> str:
+    """Where the binding for this torch and this Python lies: it holds their inline
+    code and runs with no other, so both are in its name."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(PKG_DIR, f"_binding-torch{torch.__version__}-abi{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
+    path = binding_path()
     deps = [BINDING_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))]
-    if not force and os.path.exists(BINDING_PATH) and \
-            all(os.path.getmtime(p) <= os.path.getmtime(BINDING_PATH) for p in deps):
-        return BINDING_PATH
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return path
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
     includes = [INCLUDE, os.path.join(root, "include"),
                 os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    tmp = BINDING_PATH + ".tmp"
+    tmp = path + ".tmp"
     # the system's g++, as nvcc uses it: the C++ runtime has to be the one torch uses
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -79,8 +86,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     done = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if done.returncode != 0:
         raise RuntimeError(f"binding failed to build:\n{done.stdout.decode(errors='replace')}")
-    os.replace(tmp, BINDING_PATH)
-    return BINDING_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
