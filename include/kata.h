@@ -412,9 +412,10 @@ KATA_API kata_status_t kata_fwd_delta(const void *q, const void *k, const void *
  *   q, k               device [B, H_k, T, d_k], dtype. Value head h reads query
  *                      / key head h / (H / H_k): H must be a multiple of H_k.
  *   v, o               device [B, H, T, d_v], dtype.
- *   g, beta            device fp32 [B, H, T]. A g below -100 (-inf included: the
- *                      state is dropped before the token) counts as -100, whose
- *                      decay is 0 in fp32. A token with beta = 0 and g = 0 leaves
+ *   g, beta            device fp32 [B, H, T]. A g below -110 (-inf included: the
+ *                      state is dropped before the token) counts as -110, whose
+ *                      decay is 0 in fp32; bf16 takes decays below 2^-126 as 0.
+ *                      A token with beta = 0 and g = 0 leaves
  *                      the state as it is (padding). Values outside g <= 0,
  *                      0 <= beta |k|^2 <= 2 give the rule's arithmetic, which may
  *                      then grow without bound.
@@ -466,7 +467,8 @@ KATA_API kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const 
 /*
  * One token of the gated delta rule, batched over B x H heads, the state
  * updated in place: q, k [B, H_k, d_k], v, y [B, H, d_v] (dtype), g, beta fp32
- * [B, H], S fp32 [B, H, d_k, d_v], 16-byte aligned. No workspace.
+ * [B, H], S fp32 [B, H, d_k, d_v], 16-byte aligned. A g of -110 or below drops the
+ * state, as in the forward. No workspace.
  */
 KATA_API kata_status_t kata_gated_delta_step(const void *q, const void *k, const void *v,
                                              const float *g, const float *beta, float *S, void *y,

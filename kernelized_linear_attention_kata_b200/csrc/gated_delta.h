@@ -10,6 +10,10 @@
 namespace kata {
 
 constexpr int kGdChunk = 64;     // tokens a chunk, in every kernel of the family
+// A log decay below this (a reset, -inf included) counts as this, so that sums and
+// their differences stay finite. Its exponential is 0 in fp32, whose least value is
+// e^-103.3 (and at half of which, e^-103.98, rounding turns to 0).
+constexpr float kGdMinLogDecay = -110.f;
 // SMs of a B200. Sizes the split of a sequence into segments; a constant, so that
 // a workspace's size follows from the shape alone, with or without a device.
 constexpr int kGdSms = 148;

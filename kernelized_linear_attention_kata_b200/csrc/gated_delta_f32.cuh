@@ -22,8 +22,7 @@
 //
 // The running sums are kept in fp64 and differenced there: with strong decays
 // G reaches thousands, and an fp32 difference of two such sums would lose the
-// ratio's digits. A log decay below -100 (a reset, -inf included) counts as
-// -100: e^-100 is 0 in fp32, and the differences stay finite.
+// ratio's digits. Resets (kGdMinLogDecay) keep the differences finite.
 //
 // Kernels: solve (M, P and the decays of every chunk, all chunks at once),
 // chain (one block per head, segment and CB value columns walks the chunks: the
@@ -44,9 +43,8 @@ constexpr int kC = kGdChunk;
 constexpr int kThreads = 256;
 constexpr int kLD = kC + 4;          // row stride of a 64 x 64 matrix
 constexpr int kRec = 3 * kC;         // a chunk's gates in the workspace: e^G, e^{G_C - G}, beta
-constexpr float kMinLogDecay = -100.f;
 
-__device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }
+__device__ __forceinline__ float clamp_decay(float g) { return g < kGdMinLogDecay ? kGdMinLogDecay : g; }
 
 // acc += A B for an M x N tile, operands in shared memory, 8 warps. A[m][k] at
 // A[m * LDA + k] (TA: A[k * LDA + m]); B[k][n] at B[k * LDB + n] (TB: B[n * LDB

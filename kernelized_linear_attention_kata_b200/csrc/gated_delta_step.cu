@@ -1,5 +1,6 @@
 // One token of the gated delta rule, the state updated in place:
 //   S <- e^g S + k d^T,  d = beta (v - e^g S^T k),  y = S^T q.
+// e^g is 0 from -104 on, the clamp of the chunked forms included: no clamp here.
 // With u = S^T k and w = S^T q of the old state, y = e^g w + (k . q) d, so one
 // reading of S gives both products and it stays in registers for the update:
 // S moves once in and once out, which is the floor (the step is bound by that

@@ -15,7 +15,6 @@ using namespace tc;
 constexpr int kC = kGdChunk;         // 64 tokens a chunk
 constexpr int kPanel = 8192;         // 64 rows x 128 bytes: one 64-column bf16 panel
 constexpr int kLs = kC + 4;          // row stride of the solve's fp32 matrix
-constexpr float kMinLogDecay = -100.f;
 constexpr int kSpins = 64;           // tests of a barrier before a thread suspends
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -150,7 +149,7 @@ __device__ __forceinline__ void make_gates(Gates &s, float gx, float gy, float b
   constexpr float kLog2e = 1.44269504088896340736f, kLog2eRest = 1.92596299112661746887e-8f;
   const int lane = threadIdx.x % 32;
   auto units = [&](float x) {                              // x / log 2 as two floats
-    x = x < kMinLogDecay ? kMinLogDecay : x;
+    x = x < kGdMinLogDecay ? kGdMinLogDecay : x;
     const float h = x * kLog2e;
     return make_float2(h, fmaf(x, kLog2eRest, fmaf(x, kLog2e, -h)));
   };
