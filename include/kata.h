@@ -447,7 +447,7 @@ KATA_API kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const 
  * Gradient of kata_fwd_gated_delta: given dout = dL/do and, optionally, dS =
  * dL/dS_out (NULL: zero), writes dq, dk, dv (dtype, shapes of q, k, v; dq and
  * dk of a shared head are summed over its value heads in fp32, in head order,
- * then rounded once), dg and dbeta (fp32 [B, H, T]) and, unless NULL, dS0 (fp32
+ * then rounded once; 0 where H = 0), dg and dbeta (fp32 [B, H, T]) and, unless NULL, dS0 (fp32
  * [B, H, d_k, d_v]). The forward's output is not an input: the states at the
  * chunks' borders are rebuilt into the workspace. Outputs may not overlap
  * inputs. Results are bitwise reproducible, as the forward's are. bf16 runs in

@@ -29,7 +29,7 @@ kata_status_t check_shape(int B, int H_k, int H, int T, int d_k, int d_v, kata_d
   // one block per head, chunk and 16 or 32 value columns: the largest grid
   const long long N = T / kGdChunk + (T % kGdChunk != 0);
   const long long per_head = N > d_v / 16 ? N : d_v / 16;
-  if ((long long)B * H > 0x7fffffffLL / (per_head > 0 ? per_head : 1)) return KATA_ERR_UNSUPPORTED;
+  if ((long long)B * (H > H_k ? H : H_k) > 0x7fffffffLL / (per_head > 0 ? per_head : 1)) return KATA_ERR_UNSUPPORTED;
   return KATA_OK;
 }
 
@@ -228,6 +228,13 @@ kata_status_t kata_bwd_gated_delta(const void *q, const void *k, const void *v, 
       (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta ||
        (tc && !aligned16({q, k, v, dout, dq, dk, dv}))))
     return KATA_ERR_INVALID_ARGUMENT;
+  // no value heads: dq and dk are sums over none
+  const size_t lone = H == 0 ? (size_t)B * H_k * T * d_k * (dtype == KATA_DTYPE_F32 ? 4 : 2) : 0;
+  if (lone > 0) {
+    if (!dq || !dk) return KATA_ERR_INVALID_ARGUMENT;
+    if (cudaMemsetAsync(dq, 0, lone, a.stream) != cudaSuccess || cudaMemsetAsync(dk, 0, lone, a.stream) != cudaSuccess)
+      return KATA_ERR_CUDA;
+  }
   const bool empty = a.BH == 0 || T == 0;                  // the fp32 kernels write the status themselves
   if ((tc || empty) && cudaMemsetAsync(workspace, 0, sizeof(unsigned), a.stream) != cudaSuccess) return KATA_ERR_CUDA;
   if (empty) return pass_state(dS, dS0, state, a.stream);
