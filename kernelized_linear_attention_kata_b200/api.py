@@ -252,7 +252,7 @@ def _on(stream, q, call, *args):
     the current stream of the tensors' device; `stream` makes it the given one.
     What is allocated inside belongs to that stream, so the caching allocator
     does not hand it out again while the call's kernels still use it."""
-    if stream is None:
+    if stream is None or not isinstance(q, torch.Tensor):   # the binding names what is no tensor
         return call(*args)
     if stream.device_index != q.get_device():
         raise ValueError(f"the stream is on {stream.device}, the tensors on {q.device}")

@@ -1,6 +1,7 @@
 """Calls of the gated delta rule at the edges of what its header allows."""
 
 import ctypes
+import types
 
 import pytest
 import torch
@@ -19,6 +20,22 @@ def test_no_value_heads_on_the_host(lib):  # noqa: F811
     for call in (fwd, bwd, step):
         assert call(lib, B=1 << 30, H=0, Hk=64) == L.KATA_ERR_UNSUPPORTED
     assert step(lib, H=0, Hk=2, y=ctypes.c_void_p(None)) == L.KATA_OK
+
+
+def test_no_tensor_with_a_stream_given():
+    """The refusal is the same with a stream as without."""
+    stream = types.SimpleNamespace(device_index=0, device="cuda:0")
+    t = torch.zeros(1, 1, 8, 64)
+    gate = torch.zeros(1, 1, 8)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        api.kata_fwd_gated_delta(None, t, t, gate, gate, t, stream=stream)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        api.kata_bwd_gated_delta(1.0, t, t, gate, gate, t, t, t, t, gate, gate, stream=stream)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        api.kata_gated_delta_step(None, t[:, :, 0], t[:, :, 0], gate[:, :, 0], gate[:, :, 0],
+                                  torch.zeros(1, 1, 64, 64), t[:, :, 0], stream=stream)
+    with pytest.raises(ValueError, match="stream"):
+        api.kata_fwd_gated_delta(t, t, t, gate, gate, t, stream=stream)
 
 
 @pytest.mark.gpu
