@@ -108,7 +108,8 @@ cudaError_t gd_f32(const GatedDeltaLaunch &a, int d_k, int d_v) { GD_DISPATCH(fo
 cudaError_t gd_f32_backward(const GatedDeltaLaunch &a, int d_k, int d_v) { GD_DISPATCH(backward) }
 
 // Segments a head, as for bf16 (gated_delta_tc.cu): 4.5 us a chunk of the chains
-// and the effects, 5.4 of the reverse ones, 32 value columns a block.
+// and the effects, 5.4 of the reverse ones, 32 value columns a block. Where the blocks
+// of this many segments all fit with 16 columns each, they run so (narrow), with half the products.
 void gd_f32_split(long long BH, int N, int d_k, int d_v, bool gradient, int *G, int *seg_chunks) {
   const long long nb = d_v > 32 ? d_v / 32 : 1, nf = d_k > 32 ? d_k / 32 : 1;
   int best = 1;

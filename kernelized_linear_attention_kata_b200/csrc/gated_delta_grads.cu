@@ -32,17 +32,18 @@ namespace {
 using namespace gdtc;
 
 constexpr int kThreads = 256;
+constexpr int DK = 64;               // one panel of keys; smaller heads are padded
 
-template <int DK, int DV> struct Layout {
-  static constexpr int NP = DK / 64, NV = DV / 64;
+template <int DV> struct Layout {
+  static constexpr int NV = DV / 64;
   static constexpr int kT = 6 * kPanel;                    // dO, v, dR hi, lo, D hi, lo of 64 values
-  static constexpr int kS = 2 * NP * kPanel;               // hi panels, lo panels of 64 values
+  static constexpr int kS = 2 * kPanel;                    // hi, lo of 64 values
   static constexpr int kOffT = 0;
   static constexpr int kOffS = 2 * kT;
   static constexpr int kOffDS = kOffS + kS;
   static constexpr int kOffQ = kOffDS + kS;
-  static constexpr int kOffK = kOffQ + NP * kPanel;
-  static constexpr int kOffA = kOffK + NP * kPanel;        // a 64 x 64 pair matrix, hi, lo
+  static constexpr int kOffK = kOffQ + kPanel;
+  static constexpr int kOffA = kOffK + kPanel;             // a 64 x 64 pair matrix, hi, lo
   static constexpr int kOffGates = kOffA + 2 * kPanel;
   static constexpr int kOffRows = kOffGates + (int)sizeof(Gates);   // row sums [6][2][64], column sums [4][64]
   static constexpr int kOffBars = kOffRows + (6 * 2 + 4) * kC * 4 + 64;
@@ -105,14 +106,14 @@ struct Args {
   long long jobs;
 };
 
-template <int DK, int DV>
+template <int DV>
 __global__ void __launch_bounds__(kThreads, 1)
-gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
-                   const __grid_constant__ CUtensorMap tmdq, const __grid_constant__ CUtensorMap tmdk,
-                   const Args a) {
-  using L = Layout<DK, DV>;
-  constexpr int NP = L::NP, NV = L::NV, NT = DK / 16, HC = DK / 2;     // column tiles, columns of a warp
+gd_grads_warp_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
+                     const __grid_constant__ CUtensorMap tmdq, const __grid_constant__ CUtensorMap tmdk,
+                     const Args a) {
+  using L = Layout<DV>;
+  constexpr int NV = L::NV, NT = DK / 16, HC = DK / 2;     // column tiles, columns of a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
@@ -151,22 +152,15 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     mbar_arrive_expect_tx(bar, L::kS);
 #pragma unroll
     for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-        bulk_load(smem + off + (lo * NP + p) * kPanel,
-                  img + (size_t)job * state_image(DK, DV) + lo * (state_image(DK, DV) / 2) +
-                      (size_t)p * DV * 128 + vp * kPanel,
-                  kPanel, bar);
+      bulk_load(smem + off + lo * kPanel,
+                img + (size_t)job * state_image(DK, DV) + lo * (state_image(DK, DV) / 2) + vp * kPanel, kPanel, bar);
   };
   auto load_qk = [&](long long job) {
     const int bh = head(job), t0 = (int)(job % a.N) * kC;
     const int kh = bh / a.H * a.Hk + bh % a.H / (a.H / a.Hk);
-    mbar_arrive_expect_tx(&bars[kQkFull], 2 * NP * kPanel);
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      tma_load_3d(smem + L::kOffQ + p * kPanel, &tmq, &bars[kQkFull], 64 * p, t0, kh);
-      tma_load_3d(smem + L::kOffK + p * kPanel, &tmk, &bars[kQkFull], 64 * p, t0, kh);
-    }
+    mbar_arrive_expect_tx(&bars[kQkFull], 2 * kPanel);
+    tma_load_3d(smem + L::kOffQ, &tmq, &bars[kQkFull], 0, t0, kh);
+    tma_load_3d(smem + L::kOffK, &tmk, &bars[kQkFull], 0, t0, kh);
   };
   const long long first = blockIdx.x;
   if (tid == 0 && first < a.jobs) {
@@ -207,8 +201,6 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       if (tid == 0 && more) load_t(next_job, next_vp, slot ^ 1);       // free since the unit before ended
       const uint32_t t_dO = base + L::kOffT + slot * L::kT, t_v = t_dO + kPanel, t_dR = t_dO + 2 * kPanel,
                      t_D = t_dO + 4 * kPanel;
-      const uint32_t s_col = (uint32_t)(HC * ch / 64) * kPanel;        // the warp's columns: panel, column in it
-      const int n_col = HC * ch % 64;
       mbar_wait(&bars[kTFull + slot], (unit >> 1) & 1, abort_flag);
       mbar_wait(&bars[kSFull], unit & 1, abort_flag);
 #pragma unroll 1
@@ -242,8 +234,8 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         }
 #pragma unroll
         for (int n = 0; n < NT / 2; ++n) {
-          right(b, base + L::kOffS + s_col, k, n_col + 16 * n);
-          right(c, base + L::kOffS + NP * kPanel + s_col, k, n_col + 16 * n);
+          right(b, base + L::kOffS, k, HC * ch + 16 * n);
+          right(c, base + L::kOffS + kPanel, k, HC * ch + 16 * n);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             mma(Y[2 * n + i], fo, b[2 * i], b[2 * i + 1]);
@@ -256,11 +248,11 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       }
       mbar_wait(&bars[kDSFull], unit & 1, abort_flag);
       // <S, dS'>: the tiles hold both in the same places
-      for (int e = tid; e < NP * kPanel / 16; e += kThreads) {
+      for (int e = tid; e < kPanel / 16; e += kThreads) {
         const uint4 sh = *reinterpret_cast<const uint4 *>(smem + L::kOffS + 16 * e);
-        const uint4 sl = *reinterpret_cast<const uint4 *>(smem + L::kOffS + NP * kPanel + 16 * e);
+        const uint4 sl = *reinterpret_cast<const uint4 *>(smem + L::kOffS + kPanel + 16 * e);
         const uint4 dh = *reinterpret_cast<const uint4 *>(smem + L::kOffDS + 16 * e);
-        const uint4 dl = *reinterpret_cast<const uint4 *>(smem + L::kOffDS + NP * kPanel + 16 * e);
+        const uint4 dl = *reinterpret_cast<const uint4 *>(smem + L::kOffDS + kPanel + 16 * e);
         auto pair = [&](uint32_t h1, uint32_t l1, uint32_t h2, uint32_t l2) {
           const float2 p = unpack(h1), q = unpack(l1), r = unpack(h2), s = unpack(l2);
           dot = fmaf(p.x + q.x, r.x + s.x, fmaf(p.y + q.y, r.y + s.y, dot));
@@ -279,8 +271,8 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         left_t(dl, t_D + kPanel, 16 * rt, k);
 #pragma unroll
         for (int n = 0; n < NT / 2; ++n) {
-          right(b, base + L::kOffDS + s_col, k, n_col + 16 * n);
-          right(c, base + L::kOffDS + NP * kPanel + s_col, k, n_col + 16 * n);
+          right(b, base + L::kOffDS, k, HC * ch + 16 * n);
+          right(c, base + L::kOffDS + kPanel, k, HC * ch + 16 * n);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             mma(Z[2 * n + i], dh, b[2 * i], b[2 * i + 1]);
@@ -304,13 +296,12 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     if (below) {
 #pragma unroll 1
       for (int k = 0; k < DK; k += 16) {
-        const uint32_t p = (uint32_t)(k / 64) * kPanel;
         uint32_t fq[4], fk[4], b[4];
-        left(fq, t_q + p, 16 * rt, k % 64);
-        left(fk, t_k + p, 16 * rt, k % 64);
+        left(fq, t_q, 16 * rt, k);
+        left(fk, t_k, 16 * rt, k);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          right_n(b, t_k + p, k % 64, 32 * ch + 16 * n);
+          right_n(b, t_k, k, 32 * ch + 16 * n);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             mma(qk[2 * n + i], fq, b[2 * i], b[2 * i + 1]);
@@ -347,7 +338,7 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int col = HC * ch + 8 * n + q2;
-        const uint32_t at = (uint32_t)(col / 64) * kPanel + sw128(t, col % 64 / 8) + (col % 8) * 2;
+        const uint32_t at = sw128(t, col / 8) + (col % 8) * 2;
         const float2 q = unpack(*reinterpret_cast<const uint32_t *>(smem + L::kOffQ + at));
         const float2 k = unpack(*reinterpret_cast<const uint32_t *>(smem + L::kOffK + at));
         float &x0 = X[n][2 * hrow], &x1 = X[n][2 * hrow + 1], &y0 = Y[n][2 * hrow], &y1 = Y[n][2 * hrow + 1];
@@ -441,7 +432,7 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 #pragma unroll
         for (int n = 0; n < NT / 2; ++n) {
           const int col = HC * ch + 16 * n;
-          right(b, tile + (uint32_t)(col / 64) * kPanel, k, col % 64);
+          right(b, tile, k, col);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             mma(acc[2 * n + i], h, b[2 * i], b[2 * i + 1]);
@@ -481,7 +472,7 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int col = HC * ch + 8 * n + q2;
-          const uint32_t at = (uint32_t)(col / 64) * kPanel + sw128(t, col % 64 / 8) + (col % 8) * 2;
+          const uint32_t at = sw128(t, col / 8) + (col % 8) * 2;
           *reinterpret_cast<uint32_t *>(smem + L::kOffQ + at) = pack_bf16x2(Y[n][2 * hrow], Y[n][2 * hrow + 1]);
           *reinterpret_cast<uint32_t *>(smem + L::kOffK + at) = pack_bf16x2(X[n][2 * hrow], X[n][2 * hrow + 1]);
         }
@@ -489,11 +480,8 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       fence_async_smem();
       __syncthreads();
       if (tid == 0) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          tma_store_3d(&tmdq, smem + L::kOffQ + p * kPanel, 64 * p, t0, bh);
-          tma_store_3d(&tmdk, smem + L::kOffK + p * kPanel, 64 * p, t0, bh);
-        }
+        tma_store_3d(&tmdq, smem + L::kOffQ, 0, t0, bh);
+        tma_store_3d(&tmdk, smem + L::kOffK, 0, t0, bh);
         bulk_commit_group();
         bulk_wait_read_all();
         if (job + gridDim.x < a.jobs) load_qk(job + gridDim.x);
@@ -517,7 +505,7 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   }
 }
 
-template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v) {
+template <int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k, int d_v) {
   CUtensorMap tq, tk, tv, tdo, tdq, tdk;
   const long long BHk = a.BH / a.H * a.Hk;
   if (!make_tma_3d_bf16_box(&tq, a.q, d_k, a.T, BHk, 64, kC, true) ||
@@ -527,8 +515,8 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k,
       !make_tma_3d_bf16_box(&tdq, a.dq, d_k, a.T, BHk, 64, kC, true) ||
       !make_tma_3d_bf16_box(&tdk, a.dk, d_k, a.T, BHk, 64, kC, true))
     return cudaErrorInvalidValue;
-  constexpr int bytes = Layout<DK, DV>::kBytes;
-  auto kern = gd_grads_tc_kernel<DK, DV>;
+  constexpr int bytes = Layout<DV>::kBytes;
+  auto kern = gd_grads_warp_kernel<DV>;
   GD_ALLOW_SMEM(kern, bytes);
   const Args x{a.g, a.beta, a.img_S, a.img_D, a.img_dS, a.img_dR, a.dg, a.dbeta, a.dq_part, a.dk_part,
                a.status, a.H, a.Hk, a.T, a.N, d_k, a.BH * a.N};
@@ -541,7 +529,7 @@ template <int DK, int DV> cudaError_t launch(const GatedDeltaLaunch &a, int d_k,
 
 cudaError_t gd_tc_grads(const GatedDeltaLaunch &a, int d_k, int d_v) {
   if (gd_padded(d_k) == 128) return gd_tc_grads_wide(a, d_k, d_v);
-  const cudaError_t e = gd_padded(d_v) == 64 ? launch<64, 64>(a, d_k, d_v) : launch<64, 128>(a, d_k, d_v);
+  const cudaError_t e = gd_padded(d_v) == 64 ? launch<64>(a, d_k, d_v) : launch<128>(a, d_k, d_v);
   return e == cudaSuccess && a.dq_part ? gd_sum_groups(a, d_k, true) : e;
 }
 

@@ -166,8 +166,8 @@ template <int DK> cudaError_t launch(const GatedDeltaLaunch &a, int d_k) {
 
 size_t gd_tc_record_bytes() { return kRecBytes; }
 
-cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k) { 
+cudaError_t gd_tc_solve(const GatedDeltaLaunch &a, int d_k) {
   return gd_padded(d_k) == 64 ? launch<64>(a, d_k) : launch<128>(a, d_k);
- }
+}
 
 }  // namespace kata

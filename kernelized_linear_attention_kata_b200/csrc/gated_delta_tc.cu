@@ -97,7 +97,7 @@ static_assert(8 * kNumBars + 8 <= 512, "barrier area");
 enum { kSReady = 1, kRReady, kDtReady, kDlReady };
 
 struct Args {
-  const float *g, *beta, *S0;
+  const float *S0;
   float *S_out;
   uint8_t *img_S, *img_D;          // kSave
   const uint8_t *records;          // [BH][N]
@@ -524,7 +524,7 @@ cudaError_t launch(const char *name, const GatedDeltaLaunch &a, int d_k, int d_v
       !make_tma_3d_bf16_box(&m[2], a.v, d_v, a.T, a.BH, DV, kC, false) ||
       !make_tma_3d_bf16_box(&m[3], o, d_v, a.T, a.BH, DV, kC, false))
     return cudaErrorInvalidValue;
-  const Args x{a.g, a.beta, a.S0, a.S_out, a.img_S, a.img_D, a.records, a.starts_seg,
+  const Args x{a.S0, a.S_out, a.img_S, a.img_D, a.records, a.starts_seg,
                a.status, a.H, a.Hk, a.T, a.N, a.G, a.seg_chunks, d_k, d_v};
   return run_chain<DK, DV, MODE>(name, a, m, x, a.BH * a.G);
 }
