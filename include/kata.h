@@ -425,11 +425,13 @@ KATA_API kata_status_t kata_fwd_delta(const void *q, const void *k, const void *
  *   workspace          device, >= kata_fwd_gated_delta_workspace_bytes(...),
  *                      256-byte aligned, contents on entry ignored, not shared by
  *                      calls that run concurrently; kata_workspace_status applies.
+ *                      About 524 bytes a token and value head (T rounded up to 64).
  * d_k, d_v in {16, 32, 64, 128}; any T. T = 0 copies S0 to S_out. bf16 runs
  * on the tensor cores (fp32 operands of a product as two bf16 halves, 16 bits;
- * fp32 sums and state) and takes 16-byte aligned q, k, v, o
- * (KATA_ERR_INVALID_ARGUMENT otherwise); fp32 products are made of three TF32
- * parts, as exact as fp32 arithmetic.
+ * fp32 sums and state: S_out is off by 4e-6 of its norm) and takes 16-byte aligned
+ * q, k, v, o (KATA_ERR_INVALID_ARGUMENT otherwise); fp32 products are made of
+ * three TF32 parts, as exact as fp32 arithmetic. For a state of that accuracy, bf16
+ * tensors are passed as fp32.
  * A NaN or infinity in a token reaches the whole of its chunk and all later
  * tokens of its head.
  * Outputs may not overlap inputs.
@@ -451,8 +453,11 @@ KATA_API kata_status_t kata_fwd_gated_delta(const void *q, const void *k, const 
  * [B, H, d_k, d_v]). The forward's output is not an input: the states at the
  * chunks' borders are rebuilt into the workspace. Outputs may not overlap
  * inputs. Results are bitwise reproducible, as the forward's are. bf16 runs in
- * fp32 where T < 32 (few tokens a head, whose gate gradients cancel). T = 0
- * copies dS to dS0.
+ * fp32 where T < 32 (few tokens a head, whose gate gradients cancel); from there on
+ * its fp32 outputs are off by 3e-6 to 6e-6 of their norm. T = 0 copies dS to dS0.
+ * The workspace is large: 3.5 KB a token and value head at d_k = d_v = 128 (7.6 GB
+ * for 16 heads of 131072 tokens), 1.5 KB at 64, and 8 d_k bytes more where heads
+ * share keys.
  */
 KATA_API size_t kata_bwd_gated_delta_workspace_bytes(int B, int H_k, int H, int T, int d_k, int d_v,
                                                      kata_dtype_t dtype);

@@ -8,7 +8,7 @@
 // a product takes hi hi, lo hi and hi lo. Bound by its MMAs (144 a chunk at d_v
 // = 128, 70-85 cycles each) and by the passes over tensor memory between them,
 // whose loads come slowly while MMAs run: 21K cycles a chunk, where accumulators
-// in registers took 28K (330 us instead of 425 at 16 heads of 16384 tokens). For
+// in registers took 28K (366 us instead of 425 at 16 heads of 16384 tokens). For
 // d_k = 64 it is the other way round: 140 us against 107 at 32 heads of 4096.
 //
 // Warps: 0-15 the lanes' warps (four warpgroups, 16 tokens each), of which 8 (TMEM

@@ -151,8 +151,8 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
 
   // P D of chunk c, by a whole warp. For d_k = 64 a warp of its own issues it
   // while the issuer goes on: P D takes as long as K S, which the state warps then
-  // wait for (94 us instead of 103 at 128 heads of 2048 tokens). For d_k = 128 it
-  // comes after the update, which it would only slow down (792 us instead of 817 at
+  // wait for (99 us instead of 108 at 128 heads of 2048 tokens). For d_k = 128 it
+  // comes after the update, which it would only slow down (778 us instead of 799 at
   // 16 heads of 131072).
   constexpr bool kOwnPd = DK == 64;
   auto issue_pd = [&](int c) {
