@@ -365,8 +365,8 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
       int sent = 0;
       for (int i = 0; i < n; ++i) {
         const int st = i % NS, c = first + n - 1 - i, row = kC * c;
-        if (i >= NS && (!mbar_wait(&bars[kFree + st], (i / NS - 1) & 1, abort_flag) ||
-                        (!EFFECT && !mbar_wait(&bars[kStored + st], (i / NS - 1) & 1, abort_flag))))
+        if (i >= NS && (!free_to_load(&bars[kFree + st], (i / NS - 1) & 1, abort_flag) ||
+                        (!EFFECT && !free_to_load(&bars[kStored + st], (i / NS - 1) & 1, abort_flag))))
           break;
         uint8_t *kq = smem + L::kOffKq + st * L::kKq, *dO = smem + L::kOffDo + st * L::kDo;
         const uint8_t *rec = a.records + ((size_t)bh * a.N + c) * kRecBytes;
@@ -382,8 +382,8 @@ gd_reverse_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         bulk_load(smem + L::kOffTiles + st * L::kTiles, rec + kRecM, L::kTiles, &bars[kLoaded + st]);
         sent = i + 1;
       }
-      if (*abort_flag)
-        for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) drain(&bars[kLoaded + i % NS], (i / NS) & 1);
+      // copies in flight land before the exit
+      for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) drain(&bars[kLoaded + i % NS], (i / NS) & 1);
     }
   } else if (!EFFECT && warp == kSaver) {
     if (lane == 0) {

@@ -313,7 +313,7 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     int sent = 0;
     for (; sent < n; ++sent) {
       const int st = sent % NS, row = t_begin + kC * sent;
-      if (sent >= NS && !mbar_wait(&bars[kFree + st], (sent / NS - 1) & 1, abort_flag)) break;
+      if (sent >= NS && !free_to_load(&bars[kFree + st], (sent / NS - 1) & 1, abort_flag)) break;
       uint64_t *bar = &bars[kLoaded + st];
       mbar_arrive_expect_tx(bar, L::kOne);
 #pragma unroll
@@ -322,8 +322,8 @@ gd_effect_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
       bulk_load(smem + L::kOffM + st * L::kM, rec + (size_t)sent * kRecBytes + kRecM, L::kM, bar);
       tma_load_3d(smem + L::kOffV + st * L::kV, &tmv, bar, 0, row, bh);
     }
-    if (*abort_flag)                                       // copies in flight land before the exit
-      for (int c = sent > NS ? sent - NS : 0; c < sent; ++c) drain(&bars[kLoaded + c % NS], (c / NS) & 1);
+    // copies in flight land before the exit
+    for (int c = sent > NS ? sent - NS : 0; c < sent; ++c) drain(&bars[kLoaded + c % NS], (c / NS) & 1);
   }
   __syncwarp();
   tc_fence_before();

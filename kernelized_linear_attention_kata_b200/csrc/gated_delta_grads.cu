@@ -171,8 +171,12 @@ gd_grads_warp_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
   }
 
   // A wait that gave up leaves garbage behind and the abort flag up: the block
-  // goes on through its barriers and reports at the end.
-  int unit = 0, nth = 0;
+  // goes on through its barriers and reports at the end. Thread 0 loads no more then: a
+  // load on each barrier starts only after its own wait for the one before.
+  int unit = 0, nth = 0, sent_t = 1, sent_s = 1, sent_ds = 1, sent_qk = 1;
+  bool ok = true;
+  auto landed = [&](int bar, uint32_t parity) { ok &= mbar_wait(&bars[bar], parity, abort_flag); };
+  auto may_load = [&]() { return tid == 0 && gdsync::may_load_own(ok); };
   for (long long job = first; job < a.jobs; job += gridDim.x, ++nth) {
     const int bh = head(job), t0 = (int)(job % a.N) * kC;
     const size_t tok = (size_t)bh * a.T + t0;
@@ -198,11 +202,14 @@ gd_grads_warp_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
       const long long next_job = vp + 1 < NV ? job : job + gridDim.x;
       const int next_vp = vp + 1 < NV ? vp + 1 : 0;
       const bool more = next_job < a.jobs;
-      if (tid == 0 && more) load_t(next_job, next_vp, slot ^ 1);       // free since the unit before ended
+      if (more && may_load()) {                            // free since the unit before ended
+        load_t(next_job, next_vp, slot ^ 1);
+        ++sent_t;
+      }
       const uint32_t t_dO = base + L::kOffT + slot * L::kT, t_v = t_dO + kPanel, t_dR = t_dO + 2 * kPanel,
                      t_D = t_dO + 4 * kPanel;
-      mbar_wait(&bars[kTFull + slot], (unit >> 1) & 1, abort_flag);
-      mbar_wait(&bars[kSFull], unit & 1, abort_flag);
+      landed(kTFull + slot, (unit >> 1) & 1);
+      landed(kSFull, unit & 1);
 #pragma unroll 1
       for (int k = 0; k < 64; k += 16) {
         uint32_t fo[4], rh[4], rl[4], b[4], c[4];
@@ -246,7 +253,7 @@ gd_grads_warp_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
           }
         }
       }
-      mbar_wait(&bars[kDSFull], unit & 1, abort_flag);
+      landed(kDSFull, unit & 1);
       // <S, dS'>: the tiles hold both in the same places
       for (int e = tid; e < kPanel / 16; e += kThreads) {
         const uint4 sh = *reinterpret_cast<const uint4 *>(smem + L::kOffS + 16 * e);
@@ -263,7 +270,10 @@ gd_grads_warp_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         pair(sh.w, sl.w, dh.w, dl.w);
       }
       __syncthreads();                                     // S has been read
-      if (tid == 0 && more) load_state(a.img_S, next_job, next_vp, L::kOffS, &bars[kSFull]);
+      if (more && may_load()) {
+        load_state(a.img_S, next_job, next_vp, L::kOffS, &bars[kSFull]);
+        ++sent_s;
+      }
 #pragma unroll 1
       for (int k = 0; k < 64; k += 16) {
         uint32_t dh[4], dl[4], b[4], c[4];
@@ -282,11 +292,14 @@ gd_grads_warp_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         }
       }
       __syncthreads();                                     // dS' and the slot have been read; the gates are there
-      if (tid == 0 && more) load_state(a.img_dS, next_job, next_vp, L::kOffDS, &bars[kDSFull]);
+      if (more && may_load()) {
+        load_state(a.img_dS, next_job, next_vp, L::kOffDS, &bars[kDSFull]);
+        ++sent_ds;
+      }
     }
 
     // ---- pairs of tokens
-    mbar_wait(&bars[kQkFull], nth & 1, abort_flag);
+    landed(kQkFull, nth & 1);
     const uint32_t t_q = base + L::kOffQ, t_k = base + L::kOffK, t_a = base + L::kOffA;
     float qk[4][4], kk[4][4];
 #pragma unroll
@@ -464,7 +477,10 @@ gd_grads_warp_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
             }
           }
       }
-      if (tid == 0 && job + gridDim.x < a.jobs) load_qk(job + gridDim.x);
+      if (job + gridDim.x < a.jobs && may_load()) {
+        load_qk(job + gridDim.x);
+        ++sent_qk;
+      }
     } else {
 #pragma unroll
       for (int hrow = 0; hrow < 2; ++hrow) {
@@ -484,24 +500,22 @@ gd_grads_warp_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         tma_store_3d(&tmdk, smem + L::kOffK, 0, t0, bh);
         bulk_commit_group();
         bulk_wait_read_all();
-        if (job + gridDim.x < a.jobs) load_qk(job + gridDim.x);
+        if (job + gridDim.x < a.jobs && may_load()) {
+          load_qk(job + gridDim.x);
+          ++sent_qk;
+        }
       }
     }
   }
   if (tid == 0) {
     bulk_wait_all();
-    if (*abort_flag) {                                     // copies in flight land before the exit
-      for (int s = 0; s < 2; ++s) {
-        const int uses = unit > s ? (unit - s + 1) / 2 : 0;
-        if (uses > 0) drain(&bars[kTFull + s], (uses - 1) & 1);
-      }
-      if (unit > 0) {
-        drain(&bars[kSFull], (unit - 1) & 1);
-        drain(&bars[kDSFull], (unit - 1) & 1);
-        drain(&bars[kQkFull], (nth - 1) & 1);
-      }
-      flag_status(a.status, kStatusDeviceTimeout);
+    if (first < a.jobs) {                                  // copies in flight land before the exit
+      for (int u = sent_t > 2 ? sent_t - 2 : 0; u < sent_t; ++u) drain(&bars[kTFull + (u & 1)], (u >> 1) & 1);
+      drain(&bars[kSFull], (sent_s - 1) & 1);
+      drain(&bars[kDSFull], (sent_ds - 1) & 1);
+      drain(&bars[kQkFull], (sent_qk - 1) & 1);
     }
+    if (*abort_flag) flag_status(a.status, kStatusDeviceTimeout);
   }
 }
 

@@ -490,7 +490,7 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     int unit = 0;
     bool ok = true;
     auto store = [&](int j) {                              // dq, dk of the block's j-th chunk
-      ok = ok && mbar_wait(&bars[kOut], j & 1, abort_flag);
+      ok = ok && free_to_load(&bars[kOut], j & 1, abort_flag);
       if (!ok || (a.dq_part && (a.fold == 1 || j % a.fold != a.fold - 1))) return;
       const long long job = job_of(j);
       const int bh = (int)(job / a.N), t0 = (int)(job % a.N) * kC;
@@ -503,15 +503,16 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       bulk_commit_group();
       bulk_wait_read_all();
     };
-    int loaded_qk = 0;
+    int sent_t = 0, sent_v = 0, sent_s = 0, sent_ds = 0, sent_qk = 0;
     for (int j = 0; j < jobs && ok; ++j) {
       const long long job = job_of(j);
       const int bh = (int)(job / a.N), t0 = (int)(job % a.N) * kC;
       const int kh = bh / a.H * a.Hk + bh % a.H / (a.H / a.Hk);
       for (int p = 0; p < NV; ++p, ++unit) {
         const int slot = unit & 1;
-        if (unit >= 2) ok = ok && mbar_wait(&bars[kTFree + slot], ((unit >> 1) - 1) & 1, abort_flag);
+        if (unit >= 2) ok = free_to_load(&bars[kTFree + slot], ((unit >> 1) - 1) & 1, abort_flag);
         if (!ok) break;
+        ++sent_t;
         uint8_t *dst = smem + L::kOffT + slot * L::kT;
         mbar_arrive_expect_tx(&bars[kTFull + slot], L::kT);
         tma_load_3d(dst, &tmdo, &bars[kTFull + slot], 64 * p, t0, bh);
@@ -521,7 +522,9 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
           bulk_load(dst + (1 + lo) * kPanel, a.img_dR + at, kPanel, &bars[kTFull + slot]);
           bulk_load(dst + (3 + lo) * kPanel, a.img_D + at, kPanel, &bars[kTFull + slot]);
         }
-        if (unit >= 1) ok = ok && mbar_wait(&bars[kVFree], (unit - 1) & 1, abort_flag);
+        if (unit >= 1) ok = free_to_load(&bars[kVFree], (unit - 1) & 1, abort_flag);
+        if (!ok) break;
+        ++sent_v;
         mbar_arrive_expect_tx(&bars[kVFull], kPanel);
         tma_load_3d(smem + L::kOffV, &tmv, &bars[kVFull], 64 * p, t0, bh);
         auto load_state = [&](const uint8_t *img, int off, uint64_t *bar) {
@@ -535,16 +538,17 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                             (size_t)c * DV * 128 + p * kPanel,
                         kPanel, bar);
         };
-        if (unit >= 1) ok = ok && mbar_wait(&bars[kSFree], (unit - 1) & 1, abort_flag);
+        if (unit >= 1) ok = free_to_load(&bars[kSFree], (unit - 1) & 1, abort_flag);
+        if (!ok) break;
+        ++sent_s;
         load_state(a.img_S, L::kOffS, &bars[kSFull]);
-        if (unit >= 1) ok = ok && mbar_wait(&bars[kDSFree], (unit - 1) & 1, abort_flag);
+        if (unit >= 1) ok = free_to_load(&bars[kDSFree], (unit - 1) & 1, abort_flag);
+        if (!ok) break;
+        ++sent_ds;
         load_state(a.img_dS, L::kOffDS, &bars[kDSFull]);
         if (p == 0) {
           if (j > 0) store(j - 1);
-          if (!ok) {
-            ++unit;
-            break;
-          }
+          if (!ok) break;
           uint64_t *bar = &bars[kQkFull];
           uint8_t *kq = smem + L::kOffQk;
           mbar_arrive_expect_tx(bar, L::kQk);
@@ -553,22 +557,18 @@ gd_grads_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             tma_load_3d(kq + 2 * c * kPanel, &tmk, bar, 64 * c, t0, kh);
             tma_load_3d(kq + (2 * c + 1) * kPanel, &tmq, bar, 64 * c, t0, kh);
           }
-          loaded_qk = j + 1;
+          ++sent_qk;
         }
       }
     }
     if (ok) store(jobs - 1);
     bulk_wait_all();
-    if (*abort_flag && unit > 0) {                         // copies in flight land before the exit
-      for (int s = 0; s < 2; ++s) {
-        const int uses = unit > s ? (unit - s + 1) / 2 : 0;
-        if (uses > 0) drain(&bars[kTFull + s], (uses - 1) & 1);
-      }
-      drain(&bars[kVFull], (unit - 1) & 1);
-      drain(&bars[kSFull], (unit - 1) & 1);
-      drain(&bars[kDSFull], (unit - 1) & 1);
-      if (loaded_qk > 0) drain(&bars[kQkFull], (loaded_qk - 1) & 1);
-    }
+    // copies in flight land before the exit
+    for (int u = sent_t > 2 ? sent_t - 2 : 0; u < sent_t; ++u) drain(&bars[kTFull + (u & 1)], (u >> 1) & 1);
+    if (sent_v > 0) drain(&bars[kVFull], (sent_v - 1) & 1);
+    if (sent_s > 0) drain(&bars[kSFull], (sent_s - 1) & 1);
+    if (sent_ds > 0) drain(&bars[kDSFull], (sent_ds - 1) & 1);
+    if (sent_qk > 0) drain(&bars[kQkFull], (sent_qk - 1) & 1);
   }
   __syncwarp();
   tc_fence_before();

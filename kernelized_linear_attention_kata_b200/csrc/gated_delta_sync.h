@@ -43,5 +43,13 @@ GD_SYNC_FN bool passes(bool ok) { return ok; }
 // the next chunk is of another barrier than the one that may still be open.
 GD_SYNC_FN int output_place(int chunk) { return chunk & 1; }
 
+// Loads: a barrier takes the next one's arrival only when the one before it there has
+// landed, and a block ends only when all have. That a place is free says the first as
+// long as no wait has given up: a warp that went on without its load frees the place,
+// too. So no load starts after an abort, and the last ones are waited for in any case.
+GD_SYNC_FN bool may_load(bool waited, bool aborted) { return waited && !aborted; }
+// A thread that has itself waited for the loads before knows it from its own waits.
+GD_SYNC_FN bool may_load_own(bool ok) { return ok; }
+
 }  // namespace gdsync
 }  // namespace kata

@@ -454,7 +454,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
       for (int c = 0; c <= n; ++c) {
         if (OUT && c > 0) {
           const int sv = (c - 1) % NV;
-          if (!mbar_wait(&bars[kOutputs + sv], ((c - 1) / NV) & 1, abort_flag)) break;
+          if (!free_to_load(&bars[kOutputs + sv], ((c - 1) / NV) & 1, abort_flag)) break;
           tma_store_3d(&tmo, smem + L::kOffV + sv * L::kV, 0, t_begin + kC * (c - 1), bh);
           bulk_commit_group();
           if (late < n) {
@@ -463,7 +463,7 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
           }
         }
         if (early < n) {
-          if (!mbar_wait(&bars[kFree + c % NS], (c / NS) & 1, abort_flag)) break;
+          if (!free_to_load(&bars[kFree + c % NS], (c / NS) & 1, abort_flag)) break;
           load_early(early++);
           if (!OUT) load_late(late++);
         } else if (!OUT) {
@@ -471,10 +471,9 @@ gd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         }
       }
       bulk_wait_all();
-      if (*abort_flag) {                                   // copies in flight land before the exit
-        for (int c = early > NS ? early - NS : 0; c < early; ++c) drain(&bars[kKqFull + c % NS], (c / NS) & 1);
-        for (int c = late > NV ? late - NV : 0; c < late; ++c) drain(&bars[kVFull + c % NV], (c / NV) & 1);
-      }
+      // copies in flight land before the exit
+      for (int c = early > NS ? early - NS : 0; c < early; ++c) drain(&bars[kKqFull + c % NS], (c / NS) & 1);
+      for (int c = late > NV ? late - NV : 0; c < late; ++c) drain(&bars[kVFull + c % NV], (c / NV) & 1);
     }
   } else if (SAVE && warp == kSaver) {
     if (lane == 0) {

@@ -85,7 +85,12 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
   __syncwarp();
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
-// Waits (at most kWaitLimitNs) for copies or MMAs in flight after an abort.
+// A place is free for the next load into it.
+__device__ __forceinline__ bool free_to_load(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+  const bool waited = mbar_wait(bar, parity, abort_flag);
+  return gdsync::may_load(waited, *abort_flag != 0);
+}
+// Waits (at most kWaitLimitNs) for copies or MMAs in flight before the block ends.
 static __device__ __noinline__ void drain(uint64_t *bar, uint32_t parity) {
   const uint64_t start = global_ns();
   while (!mbar_try_wait(bar, parity, kSuspendHintNs))

@@ -10,6 +10,9 @@
 //     forward_apart, save, effect, reverse), where any wait of a state warp may give
 //     up: with the kernels' rules, with state warps that always pass, or with one
 //     barrier for all hand-overs of D.
+//   gated_delta_sync_model loads|own_loads STAGES ROUNDS kernel|waited|leave
+//     Loads by a warp of their own, or by the warp that uses them: with the kernels'
+//     rules, with loads after any wait that ended, or leaving what is in flight.
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -26,11 +29,14 @@ namespace {
 
 struct Step {
   // mbarriers: one arrival completes a phase; a wait of a role that may give up
-  // goes on without it. Hardware barriers count arrivals of hand and take.
-  enum Kind { kArrive, kWait, kHand, kTake } kind;
+  // goes on without it. Hardware barriers count arrivals of hand and take. A load
+  // lands some time after its start and completes a phase; a drain waits
+  // for it. Whether it starts: by the wait before it (`exit`), or by the role's waits.
+  enum Kind { kArrive, kWait, kHand, kTake, kLoad, kDrain } kind;
   int bar;
   unsigned parity = 0;               // of a wait, as the kernel gives it
   int phase = 0;                     // the phase it means
+  int exit = -1;                     // the step to go to where the wait does not allow a load
 };
 
 struct State {
@@ -39,9 +45,12 @@ struct State {
   std::vector<char> ok;              // none of its waits has given up
   std::vector<int> phase;            // mbarriers: phases completed
   std::vector<int> count, generation;   // hardware barriers
+  std::vector<char> flying;          // mbarriers: a load is in flight
   bool aborted = false;
   bool operator<(const State &o) const {
-    auto tie = [](const State &s) { return std::tie(s.at, s.inside, s.ok, s.phase, s.count, s.generation, s.aborted); };
+    auto tie = [](const State &s) {
+      return std::tie(s.at, s.inside, s.ok, s.phase, s.count, s.generation, s.flying, s.aborted);
+    };
     return tie(*this) < tie(o);
   }
 };
@@ -51,6 +60,8 @@ struct Model {
   std::vector<char> gives_up;        // its waits have a limit
   int bars = 0, hardware = 0, quota = 0;
   bool (*passes)(bool) = [](bool ok) { return gdsync::passes(ok); };
+  bool (*may_load)(bool, bool) = [](bool waited, bool aborted) { return gdsync::may_load(waited, aborted); };
+  bool (*may_load_own)(bool) = [](bool ok) { return gdsync::may_load_own(ok); };
 
   void resize(int n) {
     roles.resize(n);
@@ -60,6 +71,8 @@ struct Model {
   void wait(int role, int bar, unsigned parity, int phase) { roles[role].push_back({Step::kWait, bar, parity, phase}); }
   void hand(int role, int bar) { roles[role].push_back({Step::kHand, bar}); }
   void take(int role, int bar) { roles[role].push_back({Step::kTake, bar}); }
+  void load(int role, int bar) { roles[role].push_back({Step::kLoad, bar}); }
+  void drain(int role, int bar) { roles[role].push_back({Step::kDrain, bar}); }
 
   // The states that role r can come to from s by one step.
   void moves(const State &s, int r, std::vector<State> &out, std::string &wrong) const {
@@ -70,15 +83,28 @@ struct Model {
       ++t.at[r];
       ++t.phase[step.bar];
       out.push_back(t);
+    } else if (step.kind == Step::kLoad) {
+      ++t.at[r];
+      if (step.exit >= 0 || may_load_own(s.ok[r])) {
+        if (s.flying[step.bar]) wrong = "a load started over another";
+        t.flying[step.bar] = 1;
+      }
+      out.push_back(t);
+    } else if (step.kind == Step::kDrain) {
+      if (s.flying[step.bar]) return;
+      ++t.at[r];
+      out.push_back(t);
     } else if (step.kind == Step::kWait) {
       // a test of a parity is true if the barrier's running phase has the other one
       const bool there = (unsigned)(s.phase[step.bar] & 1) != step.parity;
       ++t.at[r];
       if (there) {
-        if (s.ok[r] && s.phase[step.bar] <= step.phase) wrong = "a wait ended early";
+        if (s.ok[r] && !s.aborted && s.phase[step.bar] <= step.phase) wrong = "a wait ended early";
+        if (step.exit >= 0 && !may_load(true, s.aborted)) t.at[r] = step.exit;
         out.push_back(t);
       }
       if (gives_up[r] && (!there || s.aborted)) {
+        t.at[r] = step.exit >= 0 && !may_load(false, true) ? step.exit : s.at[r] + 1;
         t.ok[r] = 0;
         t.aborted = true;
         out.push_back(t);
@@ -108,6 +134,7 @@ struct Model {
     first.inside.assign(roles.size(), -1);
     first.ok.assign(roles.size(), 1);
     first.phase.resize(bars);
+    first.flying.resize(bars);
     first.count.resize(hardware);
     first.generation.resize(hardware);
     std::set<State> seen{first};
@@ -123,6 +150,13 @@ struct Model {
         moves(s, (int)r, next, wrong);
       }
       if (!wrong.empty()) return wrong;
+      for (int b = 0; b < bars; ++b)
+        if (s.flying[b]) {
+          if (ended) return "a load in flight at the end";
+          next.push_back(s);
+          next.back().flying[b] = 0;
+          ++next.back().phase[b];
+        }
       if (!ended && next.empty()) return "stuck";
       for (const State &t : next)
         if (seen.insert(t).second) open.push_back(t);
@@ -150,6 +184,36 @@ std::string dv(int stages, int rounds, bool one) {
     m.wait(2, dv_ready + ready(i).place, ready(i).parity, one ? i : nth);
     m.arrive(2, stored + st);
   }
+  return m.walk();
+}
+
+// Role 0 loads, role 1 uses the places and frees them; or role 0 does both, and has
+// the next round's load in flight while it uses this one's.
+std::string loads(bool own, int stages, int rounds, const std::string &rule) {
+  Model m;
+  m.bars = 2 * stages;
+  m.resize(own ? 1 : 2);
+  for (char &g : m.gives_up) g = 1;
+  if (rule == "waited") m.may_load = [](bool waited, bool) { return waited; };
+  if (rule == "waited") m.may_load_own = [](bool) { return true; };
+  if (own) m.load(0, 0);
+  for (int c = 0; c < rounds; ++c) {
+    const gdsync::Turn t = gdsync::turn(c, stages);
+    if (own) {
+      if (c + 1 < rounds) m.load(0, (c + 1) % stages);
+      m.wait(0, t.place, t.parity, c / stages);
+    } else {
+      if (c >= stages) m.wait(0, stages + t.place, t.parity ^ 1, c / stages - 1);
+      m.load(0, t.place);
+      m.wait(1, t.place, t.parity, c / stages);
+      m.arrive(1, stages + t.place);
+    }
+  }
+  const int exit = (int)m.roles[0].size();
+  if (!own)
+    for (Step &step : m.roles[0]) step.exit = exit;
+  if (rule != "leave")
+    for (int b = 0; b < stages; ++b) m.drain(0, b);
   return m.walk();
 }
 
@@ -219,6 +283,10 @@ int main(int argc, char **argv) {
   if (argc != 5) return 2;
   const std::string name = argv[1], rule = argv[4];
   const int n = atoi(argv[2]), rounds = atoi(argv[3]);
-  puts((name == "dv" ? dv(n, rounds, rule == "one") : chain(name, n, rounds, rule)).c_str());
+  const bool own = name == "own_loads";
+  puts((name == "dv"                    ? dv(n, rounds, rule == "one")
+        : own || name == "loads" ? loads(own, n, rounds, rule)
+                                 : chain(name, n, rounds, rule))
+           .c_str());
   return 0;
 }

@@ -61,6 +61,20 @@ def test_one_place_for_the_outputs_is_caught(model):
     assert model("forward_apart", 2, 3, "place") == "stuck"
 
 
+@pytest.mark.parametrize("loads, stages, rounds", [("loads", 2, 6), ("loads", 3, 8), ("loads", 4, 9),
+                                                   ("own_loads", 2, 6)])
+def test_loads_start_and_end_in_order(model, loads, stages, rounds):
+    """No load starts on a barrier whose last one has not landed, and none is in flight
+    when the block ends, whichever waits give up."""
+    assert model(loads, stages, rounds, "kernel") == "ok"
+
+
+@pytest.mark.parametrize("loads", ["loads", "own_loads"])
+def test_loads_after_giving_up_are_caught(model, loads):
+    assert model(loads, 2, 6, "waited") == "a load started over another"
+    assert model(loads, 2, 6, "leave") == "a load in flight at the end"
+
+
 @pytest.fixture(scope="module")
 def handover(tmp_path_factory):
     program = str(tmp_path_factory.mktemp("handover") / "handover")
